@@ -11,7 +11,9 @@ from .configs import WORKLOADS, HEADLINE, Workload, D_STATE  # noqa: F401
 
 def __getattr__(name):
     if name in ("bidir_fwd", "workspace_bytes", "status_string", "VimscanError", "lib_path",
-                "load_library", "launch_info"):
+                "load_library", "launch_info", "gated_fwd", "gated_step", "gated_info", "block_norm", "norm_info",
+                "PreparedGated", "PreparedGatedGrad", "PreparedGatedStep", "PreparedBlockNorm",
+                "PreparedBlockNormGrad"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

@@ -50,7 +50,9 @@ class _Conv(ctypes.Structure):
 
 EXPORTED = ("vimscan_bidir_fwd", "vimscan_bidir_conv_fwd", "vimscan_fwd", "vimscan_plan_launch",
             "vimscan_workspace_bytes", "vimscan_status_string", "vimscan_version", "vimscan_ncssd_fwd",
-            "vimscan_ncssd_plan", "vimscan_bidir_order_fwd", "vimscan_bidir_fwd_noalloc", "vimscan_wait_timeouts")
+            "vimscan_ncssd_plan", "vimscan_bidir_order_fwd", "vimscan_bidir_fwd_noalloc", "vimscan_wait_timeouts",
+            "vimscan_gated_fwd", "vimscan_gated_bwd", "vimscan_gated_step", "vimscan_gated_plan", "vimscan_norm_fwd",
+            "vimscan_norm_bwd", "vimscan_norm_plan")
 
 # Size of the static scratch array behind vimscan_bidir_fwd_noalloc (VIMSCAN_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 96 << 20
@@ -96,6 +98,8 @@ def load_library():
             lib.vimscan_ncssd_plan.argtypes = [ctypes.POINTER(_Launch), ctypes.c_int64, ctypes.POINTER(_Plan)]
             lib.vimscan_wait_timeouts.restype = ctypes.c_int
             lib.vimscan_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
+            from . import block
+            block.declare(lib)
             _lib = lib
     return _lib
 
@@ -366,3 +370,9 @@ def ncssd_fwd(x, B, C, m, seg_len: int = 0, out=None, chunk_len: int = 0, worksp
     """NC-SSD global-state form y = C (B^T (x . m)) on the GPU (vimscan_ncssd_fwd); arguments as
     ``PreparedNcssd``. Queued on torch's current stream; does not synchronise."""
     return PreparedNcssd(x, B, C, m, seg_len, out, chunk_len, workspace)()
+
+
+# The recurrent block's operators are part of this interface (block.py uses the helpers above).
+from .block import (GATED_STRIDE, GatedInputs, PreparedBlockNorm, PreparedBlockNormGrad,  # noqa: E402,F401
+                    PreparedGated, PreparedGatedGrad, PreparedGatedStep, block_norm, gated_fwd, gated_info, gated_step,
+                    norm_info)

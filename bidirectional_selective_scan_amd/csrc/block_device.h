@@ -1,0 +1,125 @@
+// Device helpers shared by the recurrent block's kernels (gated.hip, blocknorm.hip).
+#ifndef VIMSCAN_BLOCK_DEVICE_H
+#define VIMSCAN_BLOCK_DEVICE_H
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace vimscan_dev {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Bf16 {};  // tag for bf16 io
+
+template <typename IO> struct IoOf;
+template <> struct IoOf<float> { using elem = float; };
+template <> struct IoOf<Bf16> { using elem = uint16_t; };
+
+__device__ __forceinline__ float fast_exp2(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ float fast_log2(float v) { return __builtin_amdgcn_logf(v); }
+__device__ __forceinline__ float fast_rcp(float v) { return __builtin_amdgcn_rcpf(v); }
+__device__ __forceinline__ float fast_sqrt(float v) { return __builtin_amdgcn_sqrtf(v); }
+__device__ __forceinline__ float fast_rsq(float v) { return __builtin_amdgcn_rsqf(v); }
+
+// bf16 from fp32, to nearest even (the hardware conversion).
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    return static_cast<uint32_t>(bf16_bits(lo)) | (static_cast<uint32_t>(bf16_bits(hi)) << 16);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// V consecutive elements as they are in memory: one load of 2 to 16 bytes (two of 16 for 8 fp32).
+// The address is a multiple of the load's size.
+template <typename IO, int V> struct Raw;
+template <> struct Raw<Bf16, 1> {
+    uint16_t w;
+    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const uint16_t*>(p); }
+    __device__ __forceinline__ void zero() { w = 0; }
+    __device__ __forceinline__ float get(int) const { return __uint_as_float(static_cast<uint32_t>(w) << 16); }
+    __device__ __forceinline__ void set(const float* v) { w = bf16_bits(v[0]); }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<uint16_t*>(p) = w; }
+};
+template <> struct Raw<Bf16, 2> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ void zero() { w = 0; }
+    __device__ __forceinline__ float get(int k) const { return k ? bf16_hi(w) : bf16_lo(w); }
+    __device__ __forceinline__ void set(const float* v) { w = bf16_pair(v[0], v[1]); }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<uint32_t*>(p) = w; }
+};
+template <> struct Raw<Bf16, 4> {
+    uint2 w;
+    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const uint2*>(p); }
+    __device__ __forceinline__ void zero() { w = make_uint2(0, 0); }
+    __device__ __forceinline__ float get(int k) const {
+        const uint32_t u = k < 2 ? w.x : w.y;
+        return (k & 1) ? bf16_hi(u) : bf16_lo(u);
+    }
+    __device__ __forceinline__ void set(const float* v) { w = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])); }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<uint2*>(p) = w; }
+};
+template <> struct Raw<Bf16, 8> {
+    uint4 w;
+    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int k) const {
+        const uint32_t u = k < 2 ? w.x : k < 4 ? w.y : k < 6 ? w.z : w.w;
+        return (k & 1) ? bf16_hi(u) : bf16_lo(u);
+    }
+    __device__ __forceinline__ void set(const float* v) {
+        w = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+    }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = w; }
+};
+template <> struct Raw<float, 1> {
+    float w;
+    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const float*>(p); }
+    __device__ __forceinline__ void zero() { w = 0.0f; }
+    __device__ __forceinline__ float get(int) const { return w; }
+    __device__ __forceinline__ void set(const float* v) { w = v[0]; }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<float*>(p) = w; }
+};
+template <> struct Raw<float, 2> {
+    float2 w;
+    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const float2*>(p); }
+    __device__ __forceinline__ void zero() { w = make_float2(0, 0); }
+    __device__ __forceinline__ float get(int k) const { return k ? w.y : w.x; }
+    __device__ __forceinline__ void set(const float* v) { w = make_float2(v[0], v[1]); }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<float2*>(p) = w; }
+};
+template <> struct Raw<float, 4> {
+    float4 w;
+    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const float4*>(p); }
+    __device__ __forceinline__ void zero() { w = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int k) const { return k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w; }
+    __device__ __forceinline__ void set(const float* v) { w = make_float4(v[0], v[1], v[2], v[3]); }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<float4*>(p) = w; }
+};
+template <> struct Raw<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* p) {
+        a = static_cast<const float4*>(p)[0];
+        b = static_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int k) const {
+        return k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : k == 3 ? a.w : k == 4 ? b.x : k == 5 ? b.y : k == 6 ? b.z : b.w;
+    }
+    __device__ __forceinline__ void set(const float* v) {
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void store(void* p) const {
+        static_cast<float4*>(p)[0] = a;
+        static_cast<float4*>(p)[1] = b;
+    }
+};
+
+}  // namespace vimscan_dev
+
+#endif  // VIMSCAN_BLOCK_DEVICE_H

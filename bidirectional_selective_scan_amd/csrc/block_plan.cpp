@@ -1,0 +1,293 @@
+// Host side of the gated recurrence and the block norm (see block_plan.h).
+
+#include "block_plan.h"
+
+#include <cmath>
+#include <cstring>
+
+namespace vimscan_host {
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 31;
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool positive(float v) { return std::isfinite(v) && v > 0.0f; }
+
+// A byte range; a NULL pointer is an empty one.
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+// The whole extent of rows of width elements, ld elements apart.
+Span rows_span(const void* p, int64_t rows, int64_t ld, int64_t width, size_t e) {
+    if (!p || rows <= 0 || width <= 0) return {nullptr, 0};
+    return {p, (static_cast<size_t>(rows - 1) * ld + width) * e};
+}
+
+Span dense_span(const void* p, int64_t rows, int64_t width, size_t e) { return rows_span(p, rows, width, width, e); }
+
+bool meet(const Span& a, const Span& b) {
+    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.n && y < x + a.n;
+}
+
+template <size_t N, size_t M>
+bool any_meet(const Span (&a)[N], const Span (&b)[M]) {
+    for (const Span& x : a)
+        for (const Span& y : b)
+            if (meet(x, y)) return true;
+    return false;
+}
+
+// The checks that every launch of these operators shares.
+int check_launch(const vimscan_launch* l, int64_t d_state, int32_t flags) {
+    if (!l) return VIMSCAN_ERR_NULL;
+    if (l->batch < 0 || l->seqlen < 0 || l->d_inner < 0 || l->d_state != d_state) return VIMSCAN_ERR_SHAPE;
+    if (l->d_inner >= (int64_t(1) << 22)) return VIMSCAN_ERR_SHAPE;
+    if (l->batch >= kMaxTokens || l->seqlen >= kMaxTokens || l->batch * l->seqlen >= kMaxTokens)
+        return VIMSCAN_ERR_SHAPE;
+    if (l->io_dtype != VIMSCAN_F32 && l->io_dtype != VIMSCAN_BF16) return VIMSCAN_ERR_DTYPE;
+    if (l->chunk_len != 0) return VIMSCAN_ERR_CHUNK;
+    if (l->flags & ~flags) return VIMSCAN_ERR_FLAGS;
+    return VIMSCAN_OK;
+}
+
+size_t io_bytes(const vimscan_launch* l) { return l->io_dtype == VIMSCAN_F32 ? 4 : 2; }
+
+bool good_stride(int64_t ld, int64_t d) { return ld >= d && ld < kMaxRowStride; }
+
+// The workspace: there, large enough, aligned, apart from every array of the call.
+template <size_t N, size_t M>
+int check_workspace(const vimscan_launch* l, size_t need, const Span (&ins)[N], const Span (&outs)[M]) {
+    if (need == 0) return VIMSCAN_OK;
+    if (!l->workspace || l->workspace_bytes < need) return VIMSCAN_ERR_WORKSPACE;
+    if (!is_aligned(l->workspace, 16)) return VIMSCAN_ERR_ALIGN;
+    const Span w[] = {{l->workspace, need}};
+    return any_meet(w, ins) || any_meet(w, outs) ? VIMSCAN_ERR_ALIAS : VIMSCAN_OK;
+}
+
+}  // namespace
+
+int make_gated_plan(const vimscan_launch* l, int64_t seg_len, bool packed, int64_t nseq, bool backward, GatedPlan* p) {
+    const int rc = check_launch(l, 1, VIMSCAN_FLAG_REVERSE);
+    if (rc != VIMSCAN_OK) return rc;
+    if (seg_len < 0 || (seg_len > 0 && l->seqlen % seg_len != 0)) return VIMSCAN_ERR_SEGLEN;
+    if (packed && seg_len != 0) return VIMSCAN_ERR_PARAM;
+    if (packed && (nseq < 0 || nseq >= kMaxTokens)) return VIMSCAN_ERR_SHAPE;
+    std::memset(p, 0, sizeof(*p));
+    p->packed = packed;
+    p->tokens = l->batch * l->seqlen;
+    if (packed && nseq == 0 && p->tokens > 0) return VIMSCAN_ERR_SHAPE;
+    p->Lp = packed ? 0 : (seg_len > 0 ? seg_len : l->seqlen);
+    // uniform sequences of no tokens: one per batch row
+    p->nseq = packed ? nseq : (p->tokens > 0 ? p->tokens / p->Lp : l->batch);
+    if (l->d_inner == 0 || p->nseq == 0) return VIMSCAN_OK;
+    p->ncb = (l->d_inner + 63) / 64;
+    if (p->nseq > kMaxGatedWgs / p->ncb) return VIMSCAN_ERR_SHAPE;
+    p->wgs = p->nseq * p->ncb;
+    if (backward) {
+        p->off_dlam = 0;
+        p->ws = up256(static_cast<size_t>(p->nseq) * l->d_inner * sizeof(float));
+    }
+    return VIMSCAN_OK;
+}
+
+int check_gated_call(const vimscan_gated* g, const void* y, const float* h_last, const float* states,
+                     const vimscan_gated_grad* grad, const vimscan_launch* l, const GatedPlan& p) {
+    const int64_t n = p.tokens, d = l->d_inner;
+    const size_t e = io_bytes(l);
+    if (!positive(g->c)) return VIMSCAN_ERR_PARAM;
+    if (!good_stride(g->ld_x, d) || !good_stride(g->ld_r, d) || !good_stride(g->ld_i, d)) return VIMSCAN_ERR_PARAM;
+    if (grad && (!good_stride(grad->ld_dx, d) || (grad->dy && !good_stride(grad->ld_dy, d)) ||
+                 (grad->dr && !good_stride(grad->ld_dr, d)) || (grad->di && !good_stride(grad->ld_di, d))))
+        return VIMSCAN_ERR_PARAM;
+    if (!g->lam && (n > 0 || (grad && grad->dlam))) return VIMSCAN_ERR_NULL;
+    if (n > 0) {
+        if (!g->x || !g->r || !g->i) return VIMSCAN_ERR_NULL;
+        if (grad ? (!grad->states || !grad->dx) : !y) return VIMSCAN_ERR_NULL;
+    }
+    const void* io[] = {g->x, g->r, g->i, y, grad ? grad->dy : nullptr, grad ? grad->dx : nullptr,
+                        grad ? grad->dr : nullptr, grad ? grad->di : nullptr};
+    for (const void* q : io)
+        if (!is_aligned(q, e)) return VIMSCAN_ERR_ALIGN;
+    const void* w4[] = {g->lam, g->h0, g->offsets, h_last, states, grad ? grad->dh_last : nullptr,
+                        grad ? grad->states : nullptr, grad ? grad->dlam : nullptr, grad ? grad->dh0 : nullptr};
+    for (const void* q : w4)
+        if (!is_aligned(q, 4)) return VIMSCAN_ERR_ALIGN;
+    const int64_t groups = (n + kGatedStride - 1) / kGatedStride;
+    const Span none = {nullptr, 0};
+    const Span ins[] = {rows_span(g->x, n, g->ld_x, d, e),
+                        rows_span(g->r, n, g->ld_r, d, e),
+                        rows_span(g->i, n, g->ld_i, d, e),
+                        dense_span(g->lam, 1, d, 4),
+                        dense_span(g->h0, p.nseq, d, 4),
+                        p.packed ? dense_span(g->offsets, p.nseq + 1, 1, 4) : none,
+                        grad ? rows_span(grad->dy, n, grad->ld_dy, d, e) : none,
+                        grad ? dense_span(grad->dh_last, p.nseq, d, 4) : none,
+                        grad ? dense_span(grad->states, groups, d, 4) : none};
+    if (!grad) {
+        const Span outs[] = {dense_span(y, n, d, e), dense_span(h_last, p.nseq, d, 4), dense_span(states, groups, d, 4)};
+        if (any_meet(outs, ins) || meet(outs[0], outs[1]) || meet(outs[0], outs[2]) || meet(outs[1], outs[2]))
+            return VIMSCAN_ERR_ALIAS;
+        return check_workspace(l, p.ws, ins, outs);
+    }
+    const Span outs[] = {rows_span(grad->dx, n, grad->ld_dx, d, e), rows_span(grad->dr, n, grad->ld_dr, d, e),
+                         rows_span(grad->di, n, grad->ld_di, d, e), dense_span(grad->dlam, 1, d, 4),
+                         dense_span(grad->dh0, p.nseq, d, 4)};
+    if (any_meet(outs, ins) || meet(outs[3], outs[4])) return VIMSCAN_ERR_ALIAS;
+    for (int k = 0; k < 3; ++k)  // dx, dr, di may be interleaved slices, but not the same rows
+        for (int j = 0; j < k; ++j)
+            if (outs[k].p && outs[k].p == outs[j].p) return VIMSCAN_ERR_ALIAS;
+    for (int k = 0; k < 3; ++k)
+        if (meet(outs[k], outs[3]) || meet(outs[k], outs[4])) return VIMSCAN_ERR_ALIAS;
+    return check_workspace(l, p.ws, ins, outs);
+}
+
+int check_gated_step(const vimscan_gated* g, const float* state, int64_t nslots, const int32_t* slots_in,
+                     const int32_t* slots_out, const void* y, const vimscan_launch* l) {
+    if (!g) return VIMSCAN_ERR_NULL;
+    const int rc = check_launch(l, 1, 0);
+    if (rc != VIMSCAN_OK) return rc;
+    if (l->seqlen != 1 || nslots < 0 || nslots >= kMaxTokens) return VIMSCAN_ERR_SHAPE;
+    const int64_t n = l->batch, d = l->d_inner;
+    if (!positive(g->c)) return VIMSCAN_ERR_PARAM;
+    if (!good_stride(g->ld_x, d) || !good_stride(g->ld_r, d) || !good_stride(g->ld_i, d)) return VIMSCAN_ERR_PARAM;
+    if (n == 0 || d == 0) return VIMSCAN_OK;
+    if (n > kMaxGatedWgs / ((d + 63) / 64)) return VIMSCAN_ERR_SHAPE;
+    if (!g->x || !g->r || !g->i || !g->lam || !y || (nslots > 0 && !state)) return VIMSCAN_ERR_NULL;
+    const size_t e = io_bytes(l);
+    const void* io[] = {g->x, g->r, g->i, y};
+    for (const void* q : io)
+        if (!is_aligned(q, e)) return VIMSCAN_ERR_ALIGN;
+    const void* w4[] = {g->lam, state, slots_in, slots_out};
+    for (const void* q : w4)
+        if (!is_aligned(q, 4)) return VIMSCAN_ERR_ALIGN;
+    const Span ins[] = {rows_span(g->x, n, g->ld_x, d, e), rows_span(g->r, n, g->ld_r, d, e),
+                        rows_span(g->i, n, g->ld_i, d, e), dense_span(g->lam, 1, d, 4),
+                        dense_span(slots_in, n, 1, 4),     dense_span(slots_out, n, 1, 4)};
+    const Span outs[] = {dense_span(y, n, d, e), dense_span(state, nslots, d, 4)};
+    return any_meet(outs, ins) || meet(outs[0], outs[1]) ? VIMSCAN_ERR_ALIAS : VIMSCAN_OK;
+}
+
+int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p) {
+    const int rc = check_launch(l, 0, VIMSCAN_FLAG_GATE_AFTER);
+    if (rc != VIMSCAN_OK) return rc;
+    if (l->d_inner > kNormMaxWidth) return VIMSCAN_ERR_SHAPE;
+    std::memset(p, 0, sizeof(*p));
+    p->rows = l->batch * l->seqlen;
+    p->D = l->d_inner;
+    if (p->rows == 0 || p->D == 0) return VIMSCAN_OK;
+    p->wgs = p->rows < 512 ? p->rows : 512;
+    p->rows_per_wg = (p->rows + p->wgs - 1) / p->wgs;
+    if (backward) p->ws = up256(static_cast<size_t>(p->wgs) * 3 * p->D * sizeof(float));
+    return VIMSCAN_OK;
+}
+
+int check_norm_call(const vimscan_norm* n, const void* sum, const void* out, const vimscan_norm_grad* g,
+                    const vimscan_launch* l, const NormPlan& p) {
+    const int64_t rows = p.rows, d = l->d_inner;
+    const size_t e = io_bytes(l);
+    if (n->res_dtype != VIMSCAN_F32 && n->res_dtype != l->io_dtype) return VIMSCAN_ERR_DTYPE;
+    const size_t re = n->res_dtype == VIMSCAN_F32 ? 4 : 2;
+    if (!positive(n->eps)) return VIMSCAN_ERR_PARAM;
+    if (!good_stride(n->ld_x, d) || (n->z && !good_stride(n->ld_z, d))) return VIMSCAN_ERR_PARAM;
+    if (rows == 0 || d == 0) {  // pointers may be NULL; an empty backward pass still zeroes weight gradients
+        if (!g || d == 0) return VIMSCAN_OK;
+    } else if (!n->x) {
+        return VIMSCAN_ERR_NULL;
+    }
+    if ((l->flags & VIMSCAN_FLAG_GATE_AFTER) && rows > 0 && (!n->z || !n->w_post)) return VIMSCAN_ERR_PARAM;
+    if (!g) {
+        if ((out != nullptr) != (n->w_pre != nullptr)) return VIMSCAN_ERR_PARAM;
+        if (!sum && !out) return VIMSCAN_ERR_NULL;
+    } else {
+        if ((g->dn && !n->w_pre) || (g->dw_pre && !n->w_pre) || (g->dgamma && !n->gamma) || (g->dw_post && !n->w_post))
+            return VIMSCAN_ERR_PARAM;
+        if (rows > 0 && ((g->dz && !n->z) || (g->dresidual && !n->residual))) return VIMSCAN_ERR_PARAM;
+        if ((g->dx && !good_stride(g->ld_dx, d)) || (g->dz && !good_stride(g->ld_dz, d))) return VIMSCAN_ERR_PARAM;
+    }
+    const void* io[] = {n->x, n->z, out, g ? g->dn : nullptr, g ? g->dx : nullptr, g ? g->dz : nullptr};
+    for (const void* q : io)
+        if (!is_aligned(q, e)) return VIMSCAN_ERR_ALIGN;
+    const void* rs[] = {n->residual, sum, g ? g->dsum : nullptr, g ? g->dresidual : nullptr};
+    for (const void* q : rs)
+        if (!is_aligned(q, re)) return VIMSCAN_ERR_ALIGN;
+    const void* w4[] = {n->w_post, n->gamma, n->w_pre, g ? g->dw_post : nullptr, g ? g->dgamma : nullptr,
+                        g ? g->dw_pre : nullptr};
+    for (const void* q : w4)
+        if (!is_aligned(q, 4)) return VIMSCAN_ERR_ALIGN;
+    const Span none = {nullptr, 0};
+    const Span res = dense_span(n->residual, rows, d, re);
+    const Span ins[] = {rows_span(n->x, rows, n->ld_x, d, e), rows_span(n->z, rows, n->ld_z, d, e),
+                        dense_span(n->w_post, 1, d, 4), dense_span(n->gamma, 1, d, 4), dense_span(n->w_pre, 1, d, 4),
+                        g ? dense_span(g->dn, rows, d, e) : none};
+    if (!g) {
+        const Span outs[] = {dense_span(sum, rows, d, re), dense_span(out, rows, d, e)};
+        if (any_meet(outs, ins) || meet(outs[0], outs[1]) || meet(outs[1], res)) return VIMSCAN_ERR_ALIAS;
+        if (sum != n->residual && meet(outs[0], res)) return VIMSCAN_ERR_ALIAS;
+        return VIMSCAN_OK;
+    }
+    const Span dsum = dense_span(g->dsum, rows, d, re), dres = dense_span(g->dresidual, rows, d, re);
+    const Span rin[] = {res, dsum};
+    const Span outs[] = {rows_span(g->dx, rows, g->ld_dx, d, e), rows_span(g->dz, rows, g->ld_dz, d, e),
+                         dense_span(g->dw_post, 1, d, 4), dense_span(g->dgamma, 1, d, 4), dense_span(g->dw_pre, 1, d, 4)};
+    const Span rout[] = {dres};
+    if (any_meet(outs, ins) || any_meet(outs, rin) || any_meet(outs, rout) || any_meet(rout, ins) || meet(dres, res))
+        return VIMSCAN_ERR_ALIAS;
+    if (g->dresidual != g->dsum && meet(dres, dsum)) return VIMSCAN_ERR_ALIAS;
+    if (outs[0].p && outs[0].p == outs[1].p) return VIMSCAN_ERR_ALIAS;
+    for (int k = 2; k < 5; ++k)
+        for (int j = 0; j < k; ++j)
+            if (meet(outs[k], outs[j])) return VIMSCAN_ERR_ALIAS;
+    if (!g->dw_post && !g->dgamma && !g->dw_pre) return VIMSCAN_OK;
+    const int rc = check_workspace(l, p.ws, ins, outs);
+    if (rc != VIMSCAN_OK || p.ws == 0) return rc;
+    const Span w[] = {{l->workspace, p.ws}};
+    return any_meet(w, rin) || any_meet(w, rout) ? VIMSCAN_ERR_ALIAS : VIMSCAN_OK;
+}
+
+}  // namespace vimscan_host
+
+using namespace vimscan_host;
+
+extern "C" {
+
+int vimscan_gated_plan(const vimscan_launch* launch, int64_t seg_len, int packed, int64_t nseq, int backward,
+                       vimscan_plan* plan) {
+    if (!plan) return VIMSCAN_ERR_NULL;
+    GatedPlan p;
+    const int rc = make_gated_plan(launch, seg_len, packed != 0, nseq, backward != 0, &p);
+    if (rc != VIMSCAN_OK) return rc;
+    std::memset(plan, 0, sizeof(*plan));
+    plan->sequences = p.nseq;
+    plan->seq_tokens = p.Lp;
+    plan->chunk_len = p.Lp;
+    plan->chunks = 1;
+    plan->workgroups = p.wgs;
+    plan->kernels = p.wgs == 0 ? 0 : (backward ? 2 : 1);
+    plan->workspace_bytes = p.ws;
+    return VIMSCAN_OK;
+}
+
+int vimscan_norm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan) {
+    if (!plan) return VIMSCAN_ERR_NULL;
+    NormPlan p;
+    const int rc = make_norm_plan(launch, backward != 0, &p);
+    if (rc != VIMSCAN_OK) return rc;
+    std::memset(plan, 0, sizeof(*plan));
+    plan->sequences = p.rows;
+    plan->seq_tokens = p.rows > 0 ? 1 : 0;
+    plan->chunk_len = p.rows_per_wg;
+    plan->chunks = p.rows > 0 ? 1 : 0;
+    plan->workgroups = p.wgs;
+    plan->kernels = p.wgs == 0 ? 0 : (backward ? 2 : 1);
+    plan->workspace_bytes = p.ws;
+    return VIMSCAN_OK;
+}
+
+}  // extern "C"

@@ -116,13 +116,15 @@ const char* const kStatusText[] = {
     "bad seg_len: must be 0 or a positive divisor of seqlen",
     "bad io_dtype: must be VIMSCAN_F32 or VIMSCAN_BF16",
     "misaligned pointer",
-    "y overlaps an input",
+    "an output overlaps an input or another output",
     "workspace missing or too small",
     "HIP kernel launch failed",
     "bad chunk_len: must be >= 0",
     "unknown flag bits",
     "bad convolution: k must be 1..4",
     "the call needs more scratch than the allocation-free entry point's static array holds (96 MiB)",
+    "bad parameter: c or eps not positive and finite, a row stride below d_inner or at least 2^24, or arguments that "
+    "exclude each other",
 };
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

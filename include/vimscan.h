@@ -1,7 +1,9 @@
 /*
  * vimscan.h -- C ABI of the bidirectional selective scan on AMD MI355X (gfx950), with its
  * variants (directional convolution in front, forward only with the auxiliary swap, a given token
- * order) and the NC-SSD global-state form (declared further down).
+ * order) and the NC-SSD global-state form (declared further down), and of two operators of the
+ * blocks around such scans, each with its backward pass: the gated linear recurrence
+ * (vimscan_gated_*) and the block norm (vimscan_norm_*), also declared further down.
  *
  * The operation (Vision Mamba page, section 2.2 "bidirectional state-space modelling": a
  * forward path over the tokens in raster order and a backward path over them in reverse, the
@@ -67,8 +69,12 @@ enum vimscan_status {
     VIMSCAN_ERR_CHUNK = -9,     /* chunk_len < 0 */
     VIMSCAN_ERR_FLAGS = -10,    /* unknown bits in flags */
     VIMSCAN_ERR_CONV = -11,     /* vimscan_conv.k outside 1..4 */
-    VIMSCAN_ERR_SCRATCH = -12   /* vimscan_bidir_fwd_noalloc: the call needs more scratch than
+    VIMSCAN_ERR_SCRATCH = -12,  /* vimscan_bidir_fwd_noalloc: the call needs more scratch than
                                    VIMSCAN_NOALLOC_SCRATCH_BYTES */
+    VIMSCAN_ERR_PARAM = -13     /* gated recurrence, block norm: c or eps is not positive and
+                                   finite, a row stride is below d_inner or at least 2^24, or
+                                   arguments that exclude each other (each entry point names its
+                                   own) */
 };
 
 /* dtype of x, dt, z, B_*, C_* and y. */
@@ -90,13 +96,20 @@ enum vimscan_io_dtype { VIMSCAN_F32 = 0, VIMSCAN_BF16 = 1 };
    functions need it to size the forward-only plan; vimscan_bidir_fwd, vimscan_bidir_conv_fwd and
    vimscan_bidir_order_fwd reject it (VIMSCAN_ERR_FLAGS). */
 #define VIMSCAN_FLAG_FORWARD_ONLY 4
+/* vimscan_gated_fwd and vimscan_gated_bwd: every sequence is walked from its last token to its
+   first (nothing is flipped or copied). Only for them. */
+#define VIMSCAN_FLAG_REVERSE 8
+/* vimscan_norm_fwd and vimscan_norm_bwd: the gate silu(z) multiplies the post-norm's output
+   instead of its input. Only for them. */
+#define VIMSCAN_FLAG_GATE_AFTER 16
 
 /* Shape and launch description, passed by pointer to every entry point. */
 typedef struct vimscan_launch {
     int64_t batch;          /* B >= 0 */
     int64_t seqlen;         /* L >= 0 (the folded stream length when seg_len > 0) */
     int64_t d_inner;        /* Di >= 0 */
-    int64_t d_state;        /* N; 16 for the scans; 16, 32 or 64 for vimscan_ncssd_fwd */
+    int64_t d_state;        /* N; 16 for the scans; 16, 32 or 64 for vimscan_ncssd_fwd; 1 for the
+                               gated recurrence; 0 for the block norm */
     int32_t io_dtype;       /* enum vimscan_io_dtype */
     int32_t flags;          /* VIMSCAN_FLAG_* bits */
     int64_t chunk_len;      /* 0: the library picks; > 0: tokens per chunk of the chunked scan,
@@ -283,6 +296,162 @@ int vimscan_bidir_fwd_noalloc(const void* x, const void* dt, const void* z, cons
                               const float* dt_bias_f, const float* dt_bias_b, int64_t seg_len, void* y,
                               const vimscan_launch* launch);
 
+/*
+ * Gated linear recurrence: one fp32 state per channel, decayed and fed through two gates. For every
+ * sequence and channel d, over the sequence's tokens t in walking order (memory order, or from the
+ * last token to the first with VIMSCAN_FLAG_REVERSE):
+ *   s_t = sigmoid(r[t,d]),  g_t = sigmoid(i[t,d]),  u_t = -c * softplus(lam[d]) * s_t
+ *   a_t = exp(u_t),  m_t = sqrt(1 - a_t^2)        (1 - a_t^2 formed without cancellation)
+ *   h_t = a_t h_{t-1} + m_t g_t x[t,d],   h before the first token = h0[seq][d] (0 without h0)
+ *   y[t,d] = h_t;   h_last[seq][d] = h after the sequence's last token
+ * The tokens are the launch's batch * seqlen rows in memory order. They are cut into sequences in
+ * one of two ways:
+ *   offsets NULL: every seg_len tokens (seqlen when seg_len is 0) are a sequence; nseq is ignored;
+ *   offsets set:  device int32 [nseq + 1], offsets[0] = 0, non-decreasing, offsets[nseq] = batch *
+ *                 seqlen: sequence q is the tokens offsets[q] .. offsets[q+1] - 1, possibly none
+ *                 (seg_len must be 0: VIMSCAN_ERR_PARAM). Offsets that break these rules give
+ *                 unspecified outputs, but no access outside the arrays.
+ * An empty sequence has h_last = h0 (0 without h0). Nothing of a sequence, NaN and infinities
+ * included, reaches another sequence.
+ *
+ * Rows of x, r and i are ld_* elements apart (>= d_inner, < 2^24), so they may be slices of one
+ * projection's output; a row's channels are contiguous. h0, h_last and lam are dense fp32.
+ * launch->d_state must be 1 and chunk_len 0 (VIMSCAN_ERR_CHUNK); flags: VIMSCAN_FLAG_REVERSE only.
+ * tokens = batch * seqlen < 2^31; there is no limit on tokens * d_inner short of 2^24 workgroups
+ * (vimscan_gated_plan: VIMSCAN_ERR_SHAPE past it).
+ */
+typedef struct vimscan_gated {
+    const void* x;          /* [tokens][d_inner] io dtype, rows ld_x elements apart */
+    const void* r;          /* decay gate before the sigmoid, rows ld_r apart */
+    const void* i;          /* input gate before the sigmoid, rows ld_i apart */
+    int64_t ld_x, ld_r, ld_i;
+    const float* lam;       /* [d_inner] */
+    const float* h0;        /* [sequences][d_inner] or NULL */
+    const int32_t* offsets; /* [nseq + 1] or NULL */
+    int64_t nseq;           /* sequences when offsets is set, 0 <= nseq < 2^31 */
+    float c;                /* > 0, finite (VIMSCAN_ERR_PARAM) */
+} vimscan_gated;
+
+/* Tokens between two saved states (the states array of vimscan_gated_fwd and _bwd). */
+#define VIMSCAN_GATED_STRIDE 64
+
+/*
+ * Forward pass: y [tokens][d_inner] io dtype, dense; h_last [sequences][d_inner] fp32 or NULL;
+ * states: NULL, or fp32 [ceil(tokens / VIMSCAN_GATED_STRIDE)][d_inner], which the backward pass
+ * needs: row k receives the state entering the k-th group of VIMSCAN_GATED_STRIDE tokens in walking
+ * order (unspecified where a sequence starts there). y, h_last and states must not overlap an input,
+ * each other or the workspace (of strided rows the whole extent counts). Pointers are aligned to
+ * their element size. An empty call (no tokens) only writes h_last.
+ */
+int vimscan_gated_fwd(const vimscan_gated* g, int64_t seg_len, void* y, float* h_last, float* states,
+                      const vimscan_launch* launch);
+
+/* Gradients of vimscan_gated_fwd: dy and dh_last are those of y and h_last (either may be NULL:
+   zero); dx, dr, di [tokens][d_inner] io dtype with their own row strides; dlam [d_inner] and dh0
+   [sequences][d_inner] fp32. dr .. dh0 may be NULL (not wanted); dx may not. */
+typedef struct vimscan_gated_grad {
+    const void* dy;         /* rows ld_dy apart, io dtype */
+    const float* dh_last;
+    const float* states;    /* of vimscan_gated_fwd on the same arguments */
+    void* dx;
+    void* dr;
+    void* di;
+    int64_t ld_dy, ld_dx, ld_dr, ld_di;
+    float* dlam;            /* sum over every token: a fixed order, the same bits on every run */
+    float* dh0;
+} vimscan_gated_grad;
+
+/*
+ * Backward pass. With d_t = dy_t + e_{t+1}, e_t = a_t d_t (e after the last token = dh_last):
+ *   dx = d m g,  di = d m x g (1 - g),  dh0 = e at the first token,
+ *   w = d (u a h_{t-1} - g x a^2 u / m),  dr = w (1 - s),  dlam = sum w * sigmoid(lam) / softplus(lam)
+ * (w is u dL/du, which stays finite as u goes to 0; u / m is taken as 0 there). Arguments as the
+ * forward pass; the outputs must not overlap an input or the workspace, but dx, dr and di may be
+ * slices of one array. Needs a workspace (vimscan_gated_plan).
+ */
+int vimscan_gated_bwd(const vimscan_gated* g, int64_t seg_len, const vimscan_gated_grad* grad,
+                      const vimscan_launch* launch);
+
+/*
+ * One token of launch->batch independent streams (launch->seqlen must be 1): row b takes its state
+ * from state[slots_in[b]], applies one step of the recurrence and writes the new state to
+ * state[slots_out[b]] and y [batch][d_inner] (io dtype, dense). state is a pool of nslots fp32 rows
+ * of d_inner; slots_in and slots_out are device int32 [batch]. slots_in NULL: row b uses slot b;
+ * slots_out NULL: the state goes back to the slot it came from. A row whose slot (either one) is
+ * outside 0..nslots-1 is skipped: its y is zero and no state is written. A slot that a row writes
+ * must not be read or written by another row. h0, offsets and nseq of *g are ignored; flags must
+ * be 0; no workspace.
+ */
+int vimscan_gated_step(const vimscan_gated* g, float* state, int64_t nslots, const int32_t* slots_in,
+                       const int32_t* slots_out, void* y, const vimscan_launch* launch);
+
+/* Plan of a vimscan_gated_fwd (backward 0) or vimscan_gated_bwd (backward 1) call: sequences;
+   seq_tokens (0 with offsets); chunk_len = tokens per workgroup, chunks = workgroups over the
+   tokens of one channel block; workgroups; kernels; workspace_bytes. packed: 1 when offsets are set
+   (nseq is then their count). Host only. */
+int vimscan_gated_plan(const vimscan_launch* launch, int64_t seg_len, int packed, int64_t nseq, int backward,
+                       vimscan_plan* plan);
+
+/*
+ * Block norm: what stands between two blocks, fused. Per row (token) of d_inner channels, each
+ * stage present when its pointer is:
+ *   v = x * silu(z)                                         (z; else v = x)
+ *   p = v * w_post / sqrt(mean(v^2) + eps)                  (w_post; else p = v)
+ *   s = residual + gamma * p                                (residual, gamma)
+ *   n = s * w_pre / sqrt(mean(s^2) + eps)                   (w_pre)
+ * With VIMSCAN_FLAG_GATE_AFTER (needs z and w_post: VIMSCAN_ERR_PARAM) the gate comes after the
+ * norm instead: v = x, p = v * w_post / sqrt(mean(v^2) + eps) * silu(z). All in fp32, rounded once
+ * at the outputs (n is formed from s before its rounding). So a gated norm is (x, z, w_post), a
+ * pre-norm (x, w_pre), a residual add with the next block's norm (x, residual, gamma, w_pre).
+ *
+ * Rows: launch->batch * seqlen; width d_inner <= 32768 (VIMSCAN_ERR_SHAPE); d_state must be 0,
+ * chunk_len 0, flags VIMSCAN_FLAG_GATE_AFTER only. x and z rows are ld_x, ld_z elements apart;
+ * residual, sum and n are dense. residual and sum have res_dtype (VIMSCAN_F32, or io_dtype:
+ * VIMSCAN_ERR_DTYPE otherwise), n io_dtype; weights are fp32 [d_inner].
+ */
+typedef struct vimscan_norm {
+    const void* x;
+    const void* z;
+    int64_t ld_x, ld_z;     /* ld_z is read only with z */
+    const float* w_post;
+    const void* residual;
+    const float* gamma;
+    const float* w_pre;
+    float eps;              /* > 0, finite */
+    int32_t res_dtype;
+} vimscan_norm;
+
+/* Forward pass: writes s to sum (may be NULL when n is wanted alone) and n (non-NULL exactly with
+   w_pre: VIMSCAN_ERR_PARAM). sum may be the residual's own memory; any other overlap with an
+   input, or of sum with n, is VIMSCAN_ERR_ALIAS. One kernel, no workspace. */
+int vimscan_norm_fwd(const vimscan_norm* p, void* sum, void* n, const vimscan_launch* launch);
+
+/* Gradients of vimscan_norm_fwd. dsum (res_dtype, dense) and dn (io dtype, dense; only with w_pre:
+   VIMSCAN_ERR_PARAM) are those of its outputs, either may be NULL (zero). dx and dz (io dtype,
+   own row strides), dresidual (res_dtype, dense), dw_post, dgamma, dw_pre (fp32 [d_inner], sums over
+   the rows in a fixed order) may each be NULL (not wanted); one whose input is absent must be
+   NULL (VIMSCAN_ERR_PARAM). */
+typedef struct vimscan_norm_grad {
+    const void* dsum;
+    const void* dn;
+    void* dx;
+    void* dz;
+    int64_t ld_dx, ld_dz;
+    void* dresidual;
+    float* dw_post;
+    float* dgamma;
+    float* dw_pre;
+} vimscan_norm_grad;
+
+/* Backward pass, recomputing the row's norms from x, z and residual. dresidual may be dsum's own
+   memory. Needs a workspace when a weight gradient is wanted (vimscan_norm_plan). */
+int vimscan_norm_bwd(const vimscan_norm* p, const vimscan_norm_grad* grad, const vimscan_launch* launch);
+
+/* Plan of a vimscan_norm_fwd (backward 0) or vimscan_norm_bwd (backward 1) call: sequences = rows,
+   seq_tokens = 1, chunk_len = rows per workgroup, chunks 1, workgroups, kernels (with every weight
+   gradient wanted), workspace_bytes. Host only. */
+int vimscan_norm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan);
+
 /* Fills *plan for a call with this launch and seg_len (workspace fields of launch are
    ignored). Host only; no HIP call. Returns VIMSCAN_OK or the error the call would return. */
 int vimscan_plan_launch(const vimscan_launch* launch, int64_t seg_len, vimscan_plan* plan);
@@ -298,7 +467,8 @@ const char* vimscan_status_string(int status);
 const char* vimscan_version(void);
 
 /*
- * Diagnostics of the one-kernel chunked scans (plans of 2..16 chunks): *count = the number of
+ * Diagnostics of the one-kernel chunked scans (plans of 2..16 chunks) and of the gated
+ * recurrence (whose workgroups hand their states on in the same way): *count = the number of
  * waves on the current HIP device, since the library was loaded, whose wait for the chunk
  * aggregates of the earlier chunks of their sequence gave up after its bound (about a second);
  * their calls' outputs are unspecified. The hardware starts the workgroups of every XCD in
