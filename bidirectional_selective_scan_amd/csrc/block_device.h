@@ -16,6 +16,7 @@ struct Bf16 {};  // tag for bf16 io
 template <typename IO> struct IoOf;
 template <> struct IoOf<float> { using elem = float; };
 template <> struct IoOf<Bf16> { using elem = uint16_t; };
+template <typename IO> using IoElem = typename IoOf<IO>::elem;
 
 __device__ __forceinline__ float fast_exp2(float v) { return __builtin_amdgcn_exp2f(v); }
 __device__ __forceinline__ float fast_log2(float v) { return __builtin_amdgcn_logf(v); }

@@ -87,13 +87,23 @@ int make_gated_plan(const vimscan_launch* l, int64_t seg_len, bool packed, int64
     // uniform sequences of no tokens: one per batch row
     p->nseq = packed ? nseq : (p->tokens > 0 ? p->tokens / p->Lp : l->batch);
     if (l->d_inner == 0 || p->nseq == 0) return VIMSCAN_OK;
-    p->ncb = (l->d_inner + 63) / 64;
-    if (p->nseq > kMaxGatedWgs / p->ncb) return VIMSCAN_ERR_SHAPE;
-    p->wgs = p->nseq * p->ncb;
-    if (backward) {
-        p->off_dlam = 0;
-        p->ws = up256(static_cast<size_t>(p->nseq) * l->d_inner * sizeof(float));
+    p->ncb = (l->d_inner + kGatedBlock - 1) / kGatedBlock;
+    p->tile = backward ? kGatedBwdTile : kGatedFwdTile;
+    // a call without tokens still writes the states of its empty sequences
+    p->tiles = p->tokens > 0 ? (p->tokens + p->tile - 1) / p->tile : 1;
+    if (p->tiles > kMaxGatedWgs / p->ncb) return VIMSCAN_ERR_SHAPE;
+    p->wgs = p->tiles * p->ncb;
+    p->groups = (p->tiles + kGatedGroup - 1) / kGatedGroup;
+    // no sequence crosses a tile boundary: nothing to hand on
+    p->chain = p->tiles > 1 && (packed || p->tile % p->Lp != 0);
+    const size_t width = static_cast<size_t>(p->ncb) * kGatedBlock;
+    if (p->chain) {
+        p->off_inc = up256(static_cast<size_t>(p->tiles) * width * 2 * sizeof(float));
+        p->off_tags = p->off_inc + up256(static_cast<size_t>(p->groups) * width * sizeof(float));
+        p->off_part = p->off_tags + up256(static_cast<size_t>(p->tiles + p->groups) * p->ncb * sizeof(uint64_t));
+        p->ws = p->off_part;
     }
+    if (backward && p->tokens > 0) p->ws += up256(static_cast<size_t>(p->tiles) * width * sizeof(float));
     return VIMSCAN_OK;
 }
 
@@ -266,8 +276,8 @@ int vimscan_gated_plan(const vimscan_launch* launch, int64_t seg_len, int packed
     std::memset(plan, 0, sizeof(*plan));
     plan->sequences = p.nseq;
     plan->seq_tokens = p.Lp;
-    plan->chunk_len = p.Lp;
-    plan->chunks = 1;
+    plan->chunk_len = p.tile;
+    plan->chunks = p.tiles;
     plan->workgroups = p.wgs;
     plan->kernels = p.wgs == 0 ? 0 : (backward ? 2 : 1);
     plan->workspace_bytes = p.ws;

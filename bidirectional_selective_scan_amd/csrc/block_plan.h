@@ -11,16 +11,30 @@
 namespace vimscan_host {
 
 constexpr int kGatedStride = VIMSCAN_GATED_STRIDE;
-constexpr int64_t kMaxRowStride = int64_t(1) << 24;
+// Rows of a tile (128 at most) lie within the 2^31 bytes that one buffer resource's offsets span.
+constexpr int64_t kMaxRowStride = int64_t(1) << 22;
 constexpr int64_t kMaxGatedWgs = int64_t(1) << 24;  // x 256 threads: a grid's limit of 2^32 threads
 constexpr int64_t kNormMaxWidth = 32768;
 
+// Tiling of the gated recurrence: a workgroup of 256 threads takes kGatedBlock channels of a tile of
+// tokens, each thread tile * kGatedBlock / 256 elements.
+constexpr int kGatedBlock = 64;
+constexpr int kGatedFwdTile = 128;
+constexpr int kGatedBwdTile = 64;
+// Tiles per group of the hand-over: a tile folds the aggregates of the tiles before it in its group
+// onto the state that the group before left.
+constexpr int kGatedGroup = 32;
+static_assert(kGatedBwdTile == kGatedStride, "the backward pass starts each tile from a saved state");
+
 // Plan of a gated recurrence over whole sequences.
 struct GatedPlan {
-    int64_t tokens, nseq, Lp;  // Lp: tokens per sequence, 0 when packed
+    int64_t tokens, nseq, Lp;      // Lp: tokens per sequence, 0 when packed
+    int64_t tile, tiles, groups;   // tokens per workgroup, workgroups along the tokens, hand-over groups
     int64_t ncb, wgs;
     bool packed;
-    size_t off_dlam, ws;
+    bool chain;                    // tiles hand states on to each other
+    // workspace: aggregates, group states and tags of the hand-over, partial sums of dlam
+    size_t off_inc, off_tags, off_part, ws;
 };
 
 int make_gated_plan(const vimscan_launch* l, int64_t seg_len, bool packed, int64_t nseq, bool backward, GatedPlan* p);
@@ -30,6 +44,9 @@ int check_gated_call(const vimscan_gated* g, const void* y, const float* h_last,
                      const vimscan_gated_grad* grad, const vimscan_launch* l, const GatedPlan& p);
 int check_gated_step(const vimscan_gated* g, const float* state, int64_t nslots, const int32_t* slots_in,
                      const int32_t* slots_out, const void* y, const vimscan_launch* l);
+
+// Waits of the gated recurrence's hand-over that gave up (gated.hip).
+int gated_wait_timeouts(uint64_t* count);
 
 // Plan of a block norm: how a row is spread over lanes.
 struct NormPlan {

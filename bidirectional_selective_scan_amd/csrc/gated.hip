@@ -2,6 +2,30 @@
 // backward pass and the single-token form (include/vimscan.h, vimscan_gated_*).
 //
 // Per channel: u = -c softplus(lam) sigmoid(r), a = e^u, m = sqrt(1 - a^2), h' = a h + m sigmoid(i) x.
+//
+// Execution design (gfx950, wave64). The tokens of a call are one stream of positions in walking
+// order, whatever sequences they belong to; where a sequence starts, the state is replaced instead
+// of carried over. A workgroup of 256 threads takes a tile of positions x 64 channels and reads it
+// once: every thread holds the transitions and inputs of a few consecutive positions in registers,
+// reduces them to the map h -> A h + H of its positions, the maps are composed across the rows of a
+// wave (lane swaps), the waves (LDS) and the tiles (through the workspace, see below), and each
+// thread then walks its positions from the state that enters them. So every element is read once and
+// written once at any shape: one long sequence fills the chip as well as many short ones.
+//  * Layout: V consecutive channels per lane (8 or 16 bytes), 64 / V lanes over the channels (rows of
+//    128 or 256 bytes), the other lanes and waves over the positions.
+//  * A map whose positions contain a sequence start does not depend on the entering state: it is
+//    marked by A < 0 (a is never negative) and composed with selects, not with a factor 0, so that NaN
+//    or infinity in one sequence never reaches the next.
+//  * Between tiles: a tile publishes its map before it waits for anything, then composes the maps of
+//    the tiles before it in its group of kGatedGroup onto the state that the group before left, always
+//    in this order (the same bits on every run); a group's last tile publishes the state it leaves.
+//    Tiles wait only for tiles of lower workgroup ids, and the hardware starts the workgroups of each
+//    XCD in increasing id order: the lowest unfinished id has nothing unfinished to wait for and
+//    nothing of a higher id in its way, so every wait ends. Waits are bounded all the same
+//    (kSpinLimit) and counted (vimscan_wait_timeouts).
+//  * Backward: the same with the positions' gradients walked the other way; the state before every
+//    position is walked again from the states that the forward pass saved at every tile's first
+//    position.
 
 #include <hip/hip_runtime.h>
 
@@ -10,12 +34,17 @@
 
 #include "block_device.h"
 #include "block_plan.h"
+#include "handover.h"
 #include "vimscan.h"
 
 namespace {
 
 using namespace vimscan_dev;
 using vimscan_host::GatedPlan;
+using vimscan_host::kGatedBlock;
+using vimscan_host::kGatedBwdTile;
+using vimscan_host::kGatedFwdTile;
+using vimscan_host::kGatedGroup;
 using vimscan_host::kGatedStride;
 
 struct GatedArgs {
@@ -27,9 +56,9 @@ struct GatedArgs {
     const float* h0;
     const int32_t* offsets;  // NULL: sequences of Lp tokens
     float c;
-    int64_t N;               // tokens
-    int64_t Lp;
-    int32_t D, nseq, ncb;
+    int32_t N;               // tokens
+    int32_t Lp;
+    int32_t D, nseq, ncb, tiles;
     int32_t rev;             // walk from the last token to the first
     void* y;
     float* h_last;
@@ -44,20 +73,83 @@ struct GatedArgs {
     int64_t ld_dy, ld_dx, ld_dr, ld_di;
     float* dlam;
     float* dh0;
-    float* part;             // [nseq][D] partial sums of dlam
+    // workspace
+    float2* agg;             // [tile][width] maps (A, H), width = 64 ncb
+    float* inc;              // [group][width] the state a group leaves
+    uint64_t* tags;          // [tile][ncb], then [group][ncb]
+    float* part;             // [tile][width] partial sums of dlam
 };
 
 // Walking positions: position p of the call is token p, or N - 1 - p walked from the end; sequence
 // q in walking order is sequence q or nseq - 1 - q of the caller.
-__device__ __forceinline__ int64_t token_of(const GatedArgs& a, int64_t p) { return a.rev ? a.N - 1 - p : p; }
-__device__ __forceinline__ int64_t seq_of(const GatedArgs& a, int64_t q) { return a.rev ? a.nseq - 1 - q : q; }
+__device__ __forceinline__ int64_t seq_of(const GatedArgs& a, int q) { return a.rev ? a.nseq - 1 - q : q; }
 
 // First position of sequence q in walking order (q = nseq: the end), inside 0..N whatever the
 // offsets hold.
-__device__ __forceinline__ int64_t bound_of(const GatedArgs& a, int64_t q) {
+__device__ __forceinline__ int bound_of(const GatedArgs& a, int q) {
     if (!a.offsets) return q * a.Lp;
-    const int64_t o = a.rev ? a.N - a.offsets[a.nseq - q] : a.offsets[q];
-    return o < 0 ? 0 : o > a.N ? a.N : o;
+    const int o = a.rev ? a.offsets[a.nseq - q] : a.offsets[q];
+    const int in = o < 0 ? 0 : o > a.N ? a.N : o;
+    return a.rev ? a.N - in : in;
+}
+
+// The last sequence of lo..hi that starts at or before position p (lo when none does): the one that
+// holds p, empty ones being passed over.
+__device__ __forceinline__ int seq_at(const GatedArgs& a, int p, int lo, int hi) {
+    if (!a.offsets) return p / a.Lp;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (bound_of(a, mid) <= p) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The same over all sequences, for a position that the whole wave shares: 64 probes a round.
+__device__ __forceinline__ int seq_at_wave(const GatedArgs& a, int p, int lane) {
+    if (!a.offsets) return p / a.Lp;
+    int lo = 0, n = a.nseq;  // the answer is in lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int64_t probe = static_cast<int64_t>(lane + 1) * step;
+        const bool before = probe < n && bound_of(a, lo + static_cast<int>(probe)) <= p;
+        const int k = __popcll(__ballot(before)) * step;
+        lo += k;
+        n = n - k < step ? n - k : step;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// The sequence boundaries among a thread's positions p .. p + T - 1 of the stream: bit k of starts
+// (ends) is set where position p + k is the first (last) of its sequence. No bit is set for a position
+// past the stream's end.
+struct Cuts {
+    uint32_t starts, ends;
+};
+template <int T>
+__device__ __forceinline__ Cuts cuts_of(const GatedArgs& a, int p, int qlo, int qhi) {
+    uint64_t m = 0;  // bit k: p + k is a boundary, the stream's end included
+    const int n = min(T, a.N - p);
+    if (n <= 0) return {0, 0};
+    if (!a.offsets) {
+        const int rem = p % a.Lp;
+        for (int64_t o = rem ? a.Lp - rem : 0; o <= n; o += a.Lp) m |= uint64_t(1) << o;
+    } else {
+        int q = seq_at(a, p, qlo, qhi);
+        if (bound_of(a, q) == p) m = 1;
+        while (q < a.nseq) {
+            const int o = bound_of(a, q + 1) - p;
+            if (o > n || o <= 0) break;
+            m |= uint64_t(1) << o;
+            if (o == n) break;
+            const int next = seq_at(a, p + o, q + 1, qhi);
+            if (next <= q) break;
+            q = next;
+        }
+        if (p + n == a.N) m |= uint64_t(1) << n;
+    }
+    const uint64_t in = (uint64_t(1) << n) - 1;
+    return {static_cast<uint32_t>(m & in), static_cast<uint32_t>((m >> 1) & in)};
 }
 
 // -c softplus(lam) log2(e), so that a = 2^(k2 sigmoid(r)). softplus in log2 units is
@@ -106,97 +198,607 @@ __device__ __forceinline__ Gates gates(float r, float i, float k2) {
     return o;
 }
 
+// The rows of a tile of one tensor as a buffer resource, rows in walking order. A position past the
+// end of the stream, or a channel past the row's, takes an offset outside the resource: the hardware
+// gives 0 for such a load and drops such a store.
+constexpr uint32_t kOutside = 0x80000000u;
+
+struct TileRows {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t row_bytes;
+    uint32_t vo;         // the thread's first row (in memory order) and channel
+
+    // A tile of tile positions from p0, of which the thread takes T from tg * T on.
+    template <typename IO, int T>
+    __device__ __forceinline__ void init(const GatedArgs& a, const void* base, int64_t ld, int p0, int tile, int tg, int c0) {
+        const int64_t first = a.rev ? static_cast<int64_t>(a.N) - p0 - tile : p0;  // the tile's lowest row
+        const uint64_t at = reinterpret_cast<uint64_t>(base) + first * ld * static_cast<int64_t>(sizeof(IoElem<IO>));
+        const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
+        const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0,
+                                                 0x7fffffff, 0x00020000);
+        row_bytes = static_cast<uint32_t>(ld) * sizeof(IoElem<IO>);
+        const int row = (a.rev ? tile / T - 1 - tg : tg) * T;
+        vo = row * row_bytes + c0 * static_cast<uint32_t>(sizeof(IoElem<IO>));
+    }
+    __device__ __forceinline__ uint32_t so(const GatedArgs& a, int k, int T) const {
+        return (a.rev ? T - 1 - k : k) * row_bytes;
+    }
+};
+
+template <typename IO, int V>
+__device__ __forceinline__ Raw<IO, V> ld_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so) {
+    Raw<IO, V> o;
+    if constexpr (sizeof(o) == 2) {
+        const uint16_t w = __builtin_amdgcn_raw_buffer_load_b16(r, vo, so, 0);
+        __builtin_memcpy(&o, &w, 2);
+    } else if constexpr (sizeof(o) == 4) {
+        const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
+        __builtin_memcpy(&o, &w, 4);
+    } else if constexpr (sizeof(o) == 8) {
+        const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, vo, so, 0);
+        __builtin_memcpy(&o, &w, 8);
+    } else {
+        const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, vo, so, 0);
+        __builtin_memcpy(&o, &w, 16);
+    }
+    return o;
+}
+using U2 = uint32_t __attribute__((vector_size(8)));
+using U4 = uint32_t __attribute__((vector_size(16)));
+template <typename IO, int V>
+__device__ __forceinline__ void st_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so, const float* v) {
+    Raw<IO, V> o;
+    o.set(v);
+    if constexpr (sizeof(o) == 2) {
+        uint16_t w;
+        __builtin_memcpy(&w, &o, 2);
+        __builtin_amdgcn_raw_buffer_store_b16(w, r, vo, so, 0);
+    } else if constexpr (sizeof(o) == 4) {
+        uint32_t w;
+        __builtin_memcpy(&w, &o, 4);
+        __builtin_amdgcn_raw_buffer_store_b32(w, r, vo, so, 0);
+    } else if constexpr (sizeof(o) == 8) {
+        U2 w;
+        __builtin_memcpy(&w, &o, 8);
+        __builtin_amdgcn_raw_buffer_store_b64(w, r, vo, so, 0);
+    } else {
+        U4 w;
+        __builtin_memcpy(&w, &o, 16);
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, vo, so, 0);
+    }
+}
+
+// The map h -> A h + H of some consecutive positions; A < 0: h -> H whatever h is.
+struct Map {
+    float A, H;
+    __device__ __forceinline__ float operator()(float h) const { return A < 0.0f ? H : fmaf(A, h, H); }
+};
+__device__ __forceinline__ Map identity() { return {1.0f, 0.0f}; }
+// f, then g.
+__device__ __forceinline__ Map then(const Map& f, const Map& g) {
+    return {g.A < 0.0f || f.A < 0.0f ? -1.0f : f.A * g.A, g(f.H)};
+}
+__device__ __forceinline__ Map pick(bool c, const Map& f, const Map& g) { return {c ? f.A : g.A, c ? f.H : g.H}; }
+
+// Every lane's pair: the values of the even and the odd row of 16 lanes, or of the lower and the
+// upper 32 lanes.
+__device__ __forceinline__ void swap16(float v, float* even, float* odd) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    *even = __uint_as_float(r[0]);
+    *odd = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap32(float v, float* lo, float* hi) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    *lo = __uint_as_float(r[0]);
+    *hi = __uint_as_float(r[1]);
+}
+
+// Composes the maps of a wave's position groups (64 / CL of them, CL lanes each): total of the wave,
+// and before: the map of the groups before this lane's in walking order, or after it with kBack.
+template <int CL, bool kBack>
+__device__ __forceinline__ void scan_rows(const Map& f, int lane, Map* total, Map* before) {
+    static_assert(CL == 16 || CL == 64, "one or four position groups in a wave");
+    if constexpr (CL == 64) {
+        *total = f;
+        *before = identity();
+    } else {
+        Map e, o, lo, hi;
+        swap16(f.A, &e.A, &o.A);
+        swap16(f.H, &e.H, &o.H);
+        const Map pair = kBack ? then(o, e) : then(e, o);
+        swap32(pair.A, &lo.A, &hi.A);
+        swap32(pair.H, &lo.H, &hi.H);
+        const bool odd = lane & 16, upper = lane & 32;
+        if constexpr (kBack) {
+            const Map b = pick(odd, identity(), o);
+            *total = then(hi, lo);
+            *before = pick(upper, b, then(hi, b));
+        } else {
+            const Map b = pick(odd, e, identity());
+            *total = then(lo, hi);
+            *before = pick(upper, then(lo, b), b);
+        }
+    }
+}
+
+// Waits of this file's hand-over on this GPU that gave up after kSpinLimit reads.
+__device__ unsigned long long g_wait_timeouts;
+
+__device__ __forceinline__ void publish(uint64_t* word, uint64_t tag, int lane) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the values' stores have completed
+    if (lane == 0) __hip_atomic_store(word, tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// LDS of the hand-over.
+struct ChainLds {
+    float2 wave[4][kGatedBlock];   // the maps of the waves
+    float2 part[4][kGatedBlock];   // the maps of the tiles before this one, a quarter each
+    float inc[kGatedBlock];        // the state that the group before left
+};
+
+// Hand-over along the chain: workgroup j of channel block cb publishes its tile's map (every one but
+// the last, whatever the sequences: no wait depends on what the offsets hold) and gathers what comes in from tile first on (first == j: nothing comes in). Called
+// by all threads between the barrier that completes l.wave and one that completes l.part and l.inc.
+// kBack: the waves' maps compose from the last wave to the first.
+template <bool kBack>
+__device__ __forceinline__ Map tile_map(const ChainLds& l, int lane) {
+    Map f = identity();
+    for (int k = 0; k < 4; ++k) {
+        const float2 w = l.wave[kBack ? 3 - k : k][lane];
+        f = then(f, Map{w.x, w.y});
+    }
+    return f;
+}
+template <bool kBack>
+__device__ __forceinline__ void chain_gather(const GatedArgs& a, ChainLds& l, int j, int cb, int first, uint64_t tag,
+                                             int wave, int lane) {
+    const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
+    const int ch = cb * kGatedBlock + lane;
+    if (wave == 0 && j + 1 < a.tiles) {
+        const Map f = tile_map<kBack>(l, lane);
+        const uint64_t v = __float_as_uint(f.A) | (static_cast<uint64_t>(__float_as_uint(f.H)) << 32);
+        __hip_atomic_store(reinterpret_cast<uint64_t*>(a.agg + j * width + ch), v, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+        publish(a.tags + static_cast<int64_t>(j) * a.ncb + cb, tag, lane);
+    }
+    const int group = j / kGatedGroup, g0 = group * kGatedGroup;
+    const bool from_group = first < g0;
+    const int lo = (from_group ? g0 : first) + wave * (kGatedGroup / 4);   // this wave's tiles: lo .. lo + n - 1
+    const int n = min(j - lo, kGatedGroup / 4);
+    const bool inc = from_group && wave == 0;
+    const uint64_t* word = a.tags + static_cast<int64_t>(lo + lane) * a.ncb + cb;
+    const bool is_inc = inc && lane == 63;
+    if (is_inc) word = a.tags + (static_cast<int64_t>(a.tiles) + group - 1) * a.ncb + cb;
+    const bool mine = lane < n || is_inc;
+    bool done = n <= 0 && !inc;
+    for (int it = 0; it < kSpinLimit && !done; ++it) {
+        const bool ready = !mine || __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == tag;
+        done = __all(ready);
+        if (!done) __builtin_amdgcn_s_sleep(1);
+    }
+    if (!done && lane == 0)
+        __hip_atomic_fetch_add(&g_wait_timeouts, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::: "memory");  // the loads of the values stay after the wait
+    Map f = identity();
+    if (n > 0) {
+        uint64_t v[kGatedGroup / 4];
+#pragma unroll
+        for (int k = 0; k < kGatedGroup / 4; ++k) {
+            const int t = lo + (k < n ? k : n - 1);
+            v[k] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(a.agg + t * width + ch), __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int k = 0; k < kGatedGroup / 4; ++k) {
+            const Map g = {__uint_as_float(static_cast<uint32_t>(v[k])), __uint_as_float(static_cast<uint32_t>(v[k] >> 32))};
+            if (k < n) f = then(f, g);
+        }
+    }
+    l.part[wave][lane] = make_float2(f.A, f.H);
+    if (wave == 0) {
+        l.inc[lane] = inc ? __hip_atomic_load(a.inc + (group - 1) * width + ch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                          : 0.0f;
+    }
+}
+// What enters the tile in channel ch of the block (0 when nothing does).
+__device__ __forceinline__ float chain_carry(const ChainLds& l, int ch) {
+    float h = l.inc[ch];
+    for (int k = 0; k < 4; ++k) h = Map{l.part[k][ch].x, l.part[k][ch].y}(h);
+    return h;
+}
+// A group's last tile publishes the state it leaves.
+template <bool kBack>
+__device__ __forceinline__ void chain_leave(const GatedArgs& a, const ChainLds& l, int j, int cb, uint64_t tag, int wave,
+                                            int lane) {
+    if (wave != 0 || j + 1 >= a.tiles || j % kGatedGroup != kGatedGroup - 1) return;
+    const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
+    const int group = j / kGatedGroup;
+    const float h = tile_map<kBack>(l, lane)(chain_carry(l, lane));
+    __hip_atomic_store(a.inc + group * width + cb * kGatedBlock + lane, h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    publish(a.tags + (static_cast<int64_t>(a.tiles) + group) * a.ncb + cb, tag, lane);
+}
+
+// Sequences without tokens: what comes out is what went in (0 without it). Shared out over the tiles.
+__device__ __forceinline__ void pass_empty(const GatedArgs& a, const float* in, float* out, int j, int cb) {
+    if (!out || (!a.offsets && a.N > 0)) return;
+    const int ch = cb * kGatedBlock + (static_cast<int>(threadIdx.x) & 63);
+    if (ch >= a.D) return;
+    for (int64_t q = j * 4 + (threadIdx.x >> 6); q < a.nseq; q += static_cast<int64_t>(a.tiles) * 4) {
+        const int k = static_cast<int>(q);
+        if (a.N > 0 && bound_of(a, k + 1) > bound_of(a, k)) continue;
+        const int64_t slot = seq_of(a, k) * a.D + ch;
+        out[slot] = in ? in[slot] : 0.0f;
+    }
+}
+
+// Forward pass: a tile of kGatedFwdTile positions x 64 channels.
+template <typename IO, int V, bool kChain>
+__global__ __launch_bounds__(256) void k_gated_fwd(GatedArgs a) {
+    constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedFwdTile / TG;
+    __shared__ ChainLds lds;
+    const int j = static_cast<int>(blockIdx.x) / a.ncb, cb = static_cast<int>(blockIdx.x) % a.ncb;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    pass_empty(a, a.h0, a.h_last, j, cb);
+    if (a.N == 0) return;
+    const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
+    const bool live = c0 < a.D;
+    const int p0 = j * kGatedFwdTile, pt = p0 + tg * T;
+
+    Raw<IO, V> xr[T], rr[T], ir[T];
+    {
+        TileRows x, r, i;
+        x.init<IO, T>(a, a.x, a.ld_x, p0, kGatedFwdTile, tg, c0);
+        r.init<IO, T>(a, a.r, a.ld_r, p0, kGatedFwdTile, tg, c0);
+        i.init<IO, T>(a, a.i, a.ld_i, p0, kGatedFwdTile, tg, c0);
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            const bool in = live && pt + k < a.N;
+            rr[k] = ld_tile<IO, V>(r.rsrc, in ? r.vo : kOutside, r.so(a, k, T));
+            ir[k] = ld_tile<IO, V>(i.rsrc, in ? i.vo : kOutside, i.so(a, k, T));
+            xr[k] = ld_tile<IO, V>(x.rsrc, in ? x.vo : kOutside, x.so(a, k, T));
+        }
+    }
+    float k2[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) k2[v] = decay_rate(live ? a.lam[c0 + v] : 0.0f, a.c);
+
+    // the sequences around: where they start, and from which tile on a state comes in
+    const int p1 = min(p0 + kGatedFwdTile, a.N);
+    const int qlo = seq_at_wave(a, p0, lane);
+    const int qhi = a.offsets ? seq_at_wave(a, p1 - 1, lane) : 0;
+    const Cuts cut = cuts_of<T>(a, pt, qlo, qhi);
+    const bool starts = __any(cut.starts != 0), ends = __any(cut.ends != 0);
+
+    float av[T][V], bv[T][V];
+    Map f[V], before[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = identity();
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Gates o = gates(rr[k].get(v), ir[k].get(v), k2[v]);
+            av[k][v] = o.a;
+            bv[k][v] = o.m * o.g * xr[k].get(v);
+        }
+        const bool start = starts && (cut.starts >> k & 1);
+        if (start) {
+            if (a.h0) {
+                const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (live) bv[k][v] = fmaf(av[k][v], a.h0[slot + v], bv[k][v]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = {-1.0f, bv[k][v]};
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                f[v].H = fmaf(av[k][v], f[v].H, bv[k][v]);
+                f[v].A = f[v].A < 0.0f ? f[v].A : f[v].A * av[k][v];
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        Map total;
+        scan_rows<CL, false>(f[v], lane, &total, &before[v]);
+        if (lane < CL) lds.wave[wave][lane * V + v] = make_float2(total.A, total.H);
+    }
+    __syncthreads();
+    float h[V];
+    if constexpr (kChain) {
+        const uint64_t tag = dispatch_tag();
+        const int start = bound_of(a, qlo);
+        const int first = start >= p0 ? j : start / kGatedFwdTile;
+        chain_gather<false>(a, lds, j, cb, first, tag, wave, lane);
+        __syncthreads();
+        chain_leave<false>(a, lds, j, cb, tag, wave, lane);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = chain_carry(lds, cl * V + v);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = 0.0f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        for (int w = 0; w < wave; ++w) h[v] = Map{lds.wave[w][cl * V + v].x, lds.wave[w][cl * V + v].y}(h[v]);
+        h[v] = before[v](h[v]);
+    }
+    if (a.states && live && pt < a.N && pt % kGatedStride == 0) {
+        float* dst = a.states + static_cast<int64_t>(pt / kGatedStride) * a.D + c0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) dst[v] = h[v];
+    }
+    TileRows y;
+    y.init<IO, T>(a, a.y, a.D, p0, kGatedFwdTile, tg, c0);
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        const bool start = starts && (cut.starts >> k & 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = start ? bv[k][v] : fmaf(av[k][v], h[v], bv[k][v]);
+        st_tile<IO, V>(y.rsrc, live && pt + k < a.N ? y.vo : kOutside, y.so(a, k, T), h);
+        if (ends && (cut.ends >> k & 1) && a.h_last && live) {
+            const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.h_last[slot + v] = h[v];
+        }
+    }
+}
+
+// Backward pass: a tile of kGatedBwdTile positions x 64 channels; workgroups take the tiles from the
+// last to the first.
+template <typename IO, int V, bool kChain>
+__global__ __launch_bounds__(256) void k_gated_bwd(GatedArgs a) {
+    constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedBwdTile / TG;
+    __shared__ ChainLds lds;
+    __shared__ float2 fwd[4][kGatedBlock];
+    const int j = static_cast<int>(blockIdx.x) / a.ncb, cb = static_cast<int>(blockIdx.x) % a.ncb;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    pass_empty(a, a.dh_last, a.dh0, j, cb);
+    if (a.N == 0) return;
+    const int tile = a.tiles - 1 - j;
+    const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
+    const bool live = c0 < a.D;
+    const int p0 = tile * kGatedBwdTile, pt = p0 + tg * T;
+
+    Raw<IO, V> xr[T], rr[T], ir[T], gr[T];
+    {
+        TileRows x, r, i, g;
+        x.init<IO, T>(a, a.x, a.ld_x, p0, kGatedBwdTile, tg, c0);
+        r.init<IO, T>(a, a.r, a.ld_r, p0, kGatedBwdTile, tg, c0);
+        i.init<IO, T>(a, a.i, a.ld_i, p0, kGatedBwdTile, tg, c0);
+        g.init<IO, T>(a, a.dy, a.ld_dy, p0, kGatedBwdTile, tg, c0);
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            const bool in = live && pt + k < a.N;
+            rr[k] = ld_tile<IO, V>(r.rsrc, in ? r.vo : kOutside, r.so(a, k, T));
+            ir[k] = ld_tile<IO, V>(i.rsrc, in ? i.vo : kOutside, i.so(a, k, T));
+            xr[k] = ld_tile<IO, V>(x.rsrc, in ? x.vo : kOutside, x.so(a, k, T));
+            gr[k] = ld_tile<IO, V>(g.rsrc, in && a.dy ? g.vo : kOutside, g.so(a, k, T));
+        }
+    }
+    float k2[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) k2[v] = decay_rate(live ? a.lam[c0 + v] : 0.0f, a.c);
+    const int p1 = min(p0 + kGatedBwdTile, a.N);
+    const int qlo = seq_at_wave(a, p0, lane);
+    const int qhi = a.offsets ? seq_at_wave(a, p1 - 1, lane) : 0;
+    const Cuts cut = cuts_of<T>(a, pt, qlo, qhi);
+    const bool starts = __any(cut.starts != 0), ends = __any(cut.ends != 0);
+
+    // per element: a; m g (of dx); u a and g x a^2 u / m (of w); the gates' complements
+    float av[T][V], mg[T][V], ua[T][V], gm[T][V], ns[T][V], ng[T][V];
+    Map f[V], e[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = e[v] = identity();
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        float in[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Gates o = gates(rr[k].get(v), ir[k].get(v), k2[v]);
+            const float u = o.q * kLn2;
+            const float um = o.m > 0.0f ? u * fast_rcp(o.m) : 0.0f;
+            const float gx = o.g * xr[k].get(v);
+            av[k][v] = o.a;
+            mg[k][v] = o.m * o.g;
+            ua[k][v] = u * o.a;
+            gm[k][v] = gx * o.a * o.a * um;
+            ns[k][v] = o.ns;
+            ng[k][v] = o.ng;
+            in[v] = o.m * gx;
+        }
+        const bool start = starts && (cut.starts >> k & 1);
+        if (start) {
+            if (a.h0) {
+                const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (live) in[v] = fmaf(av[k][v], a.h0[slot + v], in[v]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = {-1.0f, in[v]};
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                f[v].H = fmaf(av[k][v], f[v].H, in[v]);
+                f[v].A = f[v].A < 0.0f ? f[v].A : f[v].A * av[k][v];
+            }
+        }
+    }
+    // gradient of a sequence's last state, added where the sequence ends
+    float last[V];
+    auto end_grad = [&](int k) {
+        const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) last[v] = live && a.dh_last ? a.dh_last[slot + v] : 0.0f;
+    };
+#pragma unroll
+    for (int k = T - 1; k >= 0; --k) {
+        if (ends && (cut.ends >> k & 1)) {
+            end_grad(k);
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v] = {-1.0f, av[k][v] * (gr[k].get(v) + last[v])};
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                e[v].H = av[k][v] * (gr[k].get(v) + e[v].H);
+                e[v].A = e[v].A < 0.0f ? e[v].A : e[v].A * av[k][v];
+            }
+        }
+    }
+    Map fb[V], eb[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        Map total;
+        scan_rows<CL, false>(f[v], lane, &total, &fb[v]);
+        if (lane < CL) fwd[wave][lane * V + v] = make_float2(total.A, total.H);
+        scan_rows<CL, true>(e[v], lane, &total, &eb[v]);
+        if (lane < CL) lds.wave[wave][lane * V + v] = make_float2(total.A, total.H);
+    }
+    __syncthreads();
+    const uint64_t tag = kChain ? dispatch_tag() : 0;
+    if constexpr (kChain) {
+        // what comes in comes from the tiles up to the end of the sequence that goes on behind this one
+        const int next = p0 + kGatedBwdTile;
+        int first = j;
+        if (next < a.N) {
+            const int q = seq_at_wave(a, next, lane);
+            if (bound_of(a, q) != next) first = a.tiles - 1 - (bound_of(a, q + 1) - 1) / kGatedBwdTile;
+        }
+        chain_gather<true>(a, lds, j, cb, min(max(first, 0), j), tag, wave, lane);
+    }
+    // the state before every position, meanwhile
+    {
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = live ? a.states_in[static_cast<int64_t>(tile) * a.D + c0 + v] : 0.0f;
+            for (int w = 0; w < wave; ++w) h[v] = Map{fwd[w][cl * V + v].x, fwd[w][cl * V + v].y}(h[v]);
+            h[v] = fb[v](h[v]);
+        }
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            if (starts && (cut.starts >> k & 1)) {
+                const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = live && a.h0 ? a.h0[slot + v] : 0.0f;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float w = fmaf(ua[k][v], h[v], -gm[k][v]);
+                h[v] = fmaf(av[k][v], h[v], mg[k][v] * xr[k].get(v));
+                ua[k][v] = w;
+            }
+        }
+    }
+    float d[V];
+    if constexpr (kChain) {
+        __syncthreads();
+        chain_leave<true>(a, lds, j, cb, tag, wave, lane);
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = chain_carry(lds, cl * V + v);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = 0.0f;
+    }
+    TileRows dx, dr, di;
+    dx.init<IO, T>(a, a.dx, a.ld_dx, p0, kGatedBwdTile, tg, c0);
+    dr.init<IO, T>(a, a.dr, a.ld_dr, p0, kGatedBwdTile, tg, c0);
+    di.init<IO, T>(a, a.di, a.ld_di, p0, kGatedBwdTile, tg, c0);
+    float sum[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        for (int w = 3; w > wave; --w) d[v] = Map{lds.wave[w][cl * V + v].x, lds.wave[w][cl * V + v].y}(d[v]);
+        d[v] = eb[v](d[v]);
+        sum[v] = 0.0f;
+    }
+#pragma unroll
+    for (int k = T - 1; k >= 0; --k) {
+        if (ends && (cut.ends >> k & 1)) {
+            end_grad(k);
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] = last[v];
+        }
+        float ox[V], orr[V], oi[V];
+        const bool in = live && pt + k < a.N;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float del = gr[k].get(v) + d[v];
+            const float w = del * ua[k][v];
+            ox[v] = del * mg[k][v];
+            oi[v] = ox[v] * xr[k].get(v) * ng[k][v];
+            orr[v] = w * ns[k][v];
+            sum[v] += in ? w : 0.0f;
+            d[v] = av[k][v] * del;
+        }
+        st_tile<IO, V>(dx.rsrc, in ? dx.vo : kOutside, dx.so(a, k, T), ox);
+        st_tile<IO, V>(dr.rsrc, in && a.dr ? dr.vo : kOutside, dr.so(a, k, T), orr);
+        st_tile<IO, V>(di.rsrc, in && a.di ? di.vo : kOutside, di.so(a, k, T), oi);
+        if (starts && (cut.starts >> k & 1) && a.dh0 && live) {
+            const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.dh0[slot + v] = d[v];
+        }
+    }
+    if (!a.dlam) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if constexpr (CL == 16) {
+            float p, q;
+            swap16(sum[v], &p, &q);
+            swap32(p + q, &p, &q);
+            sum[v] = p + q;
+        }
+    }
+    __syncthreads();
+    if (lane < CL) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) fwd[wave][lane * V + v].x = sum[v];
+    }
+    __syncthreads();
+    if (wave == 0)
+        a.part[static_cast<int64_t>(tile) * a.ncb * kGatedBlock + cb * kGatedBlock + lane] =
+            (fwd[0][lane].x + fwd[1][lane].x) + (fwd[2][lane].x + fwd[3][lane].x);
+}
+
+// dlam = sigmoid(lam) / softplus(lam) * the sum of the tiles' partial sums, in a fixed order: 16 waves
+// take every 16th tile each.
+__global__ __launch_bounds__(1024) void k_gated_dlam(GatedArgs a, int parts) {
+    __shared__ float lds[16][64];
+    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
+    const int d = static_cast<int>(blockIdx.x) * 64 + lane;
+    const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int k = wave; k < parts; k += 16) sum += a.part[k * width + d];
+    lds[wave][lane] = sum;
+    __syncthreads();
+    if (wave != 0 || d >= a.D) return;
+    sum = 0.0f;
+    for (int k = 0; k < 16; ++k) sum += lds[k][lane];
+    const float lam = a.lam[d];
+    const float sp = decay_rate(lam, -kLn2);  // softplus(lam)
+    // both tend to e^lam as lam goes to -infinity, where the ratio goes to 1
+    const float ratio = sp > 0.0f ? fast_rcp(1.0f + fast_exp2(-lam * kLog2e)) / sp : 1.0f;
+    a.dlam[d] = sum * ratio;
+}
+
 template <typename IO>
 __device__ __forceinline__ float ld(const void* p, int64_t k) {
     Raw<IO, 1> w;
-    w.load(static_cast<const typename IoOf<IO>::elem*>(p) + k);
+    w.load(static_cast<const IoElem<IO>*>(p) + k);
     return w.get(0);
 }
 template <typename IO>
 __device__ __forceinline__ void st(void* p, int64_t k, float v) {
     Raw<IO, 1> w;
     w.set(&v);
-    w.store(static_cast<typename IoOf<IO>::elem*>(p) + k);
-}
-
-// One wave per sequence and block of 64 channels, token by token.
-template <typename IO>
-__global__ __launch_bounds__(64) void k_gated_fwd(GatedArgs a) {
-    const int64_t q = blockIdx.x / a.ncb;
-    const int d = static_cast<int>(blockIdx.x % a.ncb) * 64 + static_cast<int>(threadIdx.x);
-    if (d >= a.D) return;
-    const int64_t slot = seq_of(a, q) * a.D + d;
-    const int64_t p0 = bound_of(a, q), p1 = bound_of(a, q + 1);
-    float h = a.h0 ? a.h0[slot] : 0.0f;
-    if (p1 > p0) {
-        const float k2 = decay_rate(a.lam[d], a.c);
-        for (int64_t p = p0; p < p1; ++p) {
-            const int64_t t = token_of(a, p);
-            if (a.states && p % kGatedStride == 0) a.states[p / kGatedStride * a.D + d] = h;
-            const Gates o = gates(ld<IO>(a.r, t * a.ld_r + d), ld<IO>(a.i, t * a.ld_i + d), k2);
-            h = fmaf(o.a, h, o.m * o.g * ld<IO>(a.x, t * a.ld_x + d));
-            st<IO>(a.y, t * a.D + d, h);
-        }
-    }
-    if (a.h_last) a.h_last[slot] = h;
-}
-
-// The same division of the work, from the last group of kGatedStride positions to the first: the
-// group's states are walked forward again from the saved one, then the gradient backward.
-template <typename IO>
-__global__ __launch_bounds__(64) void k_gated_bwd(GatedArgs a) {
-    const int64_t q = blockIdx.x / a.ncb;
-    const int d = static_cast<int>(blockIdx.x % a.ncb) * 64 + static_cast<int>(threadIdx.x);
-    if (d >= a.D) return;
-    const int64_t slot = seq_of(a, q) * a.D + d;
-    const int64_t p0 = bound_of(a, q), p1 = bound_of(a, q + 1);
-    float e = a.dh_last ? a.dh_last[slot] : 0.0f;
-    float sum = 0.0f;
-    if (p1 > p0) {
-        const float k2 = decay_rate(a.lam[d], a.c);
-        float before[kGatedStride];
-        for (int64_t grp = (p1 - 1) / kGatedStride; grp >= p0 / kGatedStride; --grp) {
-            const int64_t g0 = grp * kGatedStride;
-            const int64_t lo = g0 > p0 ? g0 : p0, hi = g0 + kGatedStride < p1 ? g0 + kGatedStride : p1;
-            float h = lo == p0 ? (a.h0 ? a.h0[slot] : 0.0f) : a.states_in[grp * a.D + d];
-            for (int64_t p = lo; p < hi; ++p) {
-                const int64_t t = token_of(a, p);
-                before[p - g0] = h;
-                const Gates o = gates(ld<IO>(a.r, t * a.ld_r + d), ld<IO>(a.i, t * a.ld_i + d), k2);
-                h = fmaf(o.a, h, o.m * o.g * ld<IO>(a.x, t * a.ld_x + d));
-            }
-            for (int64_t p = hi - 1; p >= lo; --p) {
-                const int64_t t = token_of(a, p);
-                const Gates o = gates(ld<IO>(a.r, t * a.ld_r + d), ld<IO>(a.i, t * a.ld_i + d), k2);
-                const float x = ld<IO>(a.x, t * a.ld_x + d);
-                const float del = e + (a.dy ? ld<IO>(a.dy, t * a.ld_dy + d) : 0.0f);
-                const float u = o.q * kLn2;
-                const float um = o.m > 0.0f ? u * fast_rcp(o.m) : 0.0f;
-                const float dx = del * o.m * o.g;
-                const float w = del * (u * o.a * before[p - g0] - o.g * x * o.a * o.a * um);
-                st<IO>(a.dx, t * a.ld_dx + d, dx);
-                if (a.di) st<IO>(a.di, t * a.ld_di + d, dx * x * o.ng);
-                if (a.dr) st<IO>(a.dr, t * a.ld_dr + d, w * o.ns);
-                sum += w;
-                e = o.a * del;
-            }
-        }
-    }
-    if (a.dh0) a.dh0[slot] = e;
-    a.part[q * a.D + d] = sum;
-}
-
-// dlam = sigmoid(lam) / softplus(lam) * the sum of the partial sums, in their order.
-__global__ __launch_bounds__(64) void k_gated_dlam(GatedArgs a, int64_t parts) {
-    const int d = static_cast<int>(blockIdx.x) * 64 + static_cast<int>(threadIdx.x);
-    if (d >= a.D) return;
-    float sum = 0.0f;
-    for (int64_t k = 0; k < parts; ++k) sum += a.part[k * a.D + d];
-    const float lam = a.lam[d];
-    const float sp = decay_rate(lam, -kLn2);  // softplus(lam)
-    // both tend to e^lam as lam goes to -infinity, where the ratio goes to 1
-    const float ratio = sp > 0.0f ? fast_rcp(1.0f + fast_exp2(-lam * kLog2e)) / sp : 1.0f;
-    a.dlam[d] = sum * ratio;
+    w.store(static_cast<IoElem<IO>*>(p) + k);
 }
 
 struct StepArgs {
@@ -244,11 +846,19 @@ GatedArgs common_args(const vimscan_gated* g, const vimscan_launch* l, const Gat
     a.h0 = g->h0;
     a.offsets = g->offsets;
     a.c = g->c;
-    a.N = p.tokens;
-    a.Lp = p.Lp;
+    a.N = static_cast<int32_t>(p.tokens);
+    a.Lp = static_cast<int32_t>(p.Lp);
     a.D = static_cast<int32_t>(l->d_inner);
     a.nseq = static_cast<int32_t>(p.nseq);
     a.ncb = static_cast<int32_t>(p.ncb);
+    a.tiles = static_cast<int32_t>(p.tiles);
+    char* ws = static_cast<char*>(l->workspace);
+    if (p.chain) {
+        a.agg = reinterpret_cast<float2*>(ws);
+        a.inc = reinterpret_cast<float*>(ws + p.off_inc);
+        a.tags = reinterpret_cast<uint64_t*>(ws + p.off_tags);
+    }
+    a.part = p.ws > p.off_part ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
     a.rev = (l->flags & VIMSCAN_FLAG_REVERSE) ? 1 : 0;
     return a;
 }
@@ -259,7 +869,43 @@ bool record(const vimscan_launch* l, int k) {
     return hipEventRecord(static_cast<hipEvent_t>(l->scan_events[k]), static_cast<hipStream_t>(l->stream)) == hipSuccess;
 }
 
+// Four channels per lane where every row of every tensor is aligned to four elements.
+bool by_four(const vimscan_gated* g, int64_t d, size_t e, const void* const* more, const int64_t* lds, int n) {
+    auto ok = [&](const void* p, int64_t ld) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % (4 * e) == 0 && ld % 4 == 0);
+    };
+    bool r = d % 4 == 0 && ok(g->x, g->ld_x) && ok(g->r, g->ld_r) && ok(g->i, g->ld_i);
+    for (int k = 0; k < n; ++k) r = r && ok(more[k], lds[k]);
+    return r;
+}
+
+template <typename IO, int V>
+void launch_fwd(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.wgs));
+    if (p.chain) hipLaunchKernelGGL((k_gated_fwd<IO, V, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_gated_fwd<IO, V, false>), grid, dim3(256), 0, s, a);
+}
+
+template <typename IO, int V>
+void launch_bwd(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.wgs));
+    if (p.chain) hipLaunchKernelGGL((k_gated_bwd<IO, V, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_gated_bwd<IO, V, false>), grid, dim3(256), 0, s, a);
+}
+
 }  // namespace
+
+namespace vimscan_host {
+
+int gated_wait_timeouts(uint64_t* count) {
+    unsigned long long v = 0;
+    if (hipMemcpyFromSymbol(&v, HIP_SYMBOL(g_wait_timeouts), sizeof(v), 0, hipMemcpyDeviceToHost) != hipSuccess)
+        return VIMSCAN_ERR_HIP;
+    *count = static_cast<uint64_t>(v);
+    return VIMSCAN_OK;
+}
+
+}  // namespace vimscan_host
 
 extern "C" {
 
@@ -278,9 +924,16 @@ int vimscan_gated_fwd(const vimscan_gated* g, int64_t seg_len, void* y, float* h
     a.states = states;
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
-    const dim3 grid(static_cast<unsigned>(p.wgs));
-    if (launch->io_dtype == VIMSCAN_F32) hipLaunchKernelGGL(k_gated_fwd<float>, grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL(k_gated_fwd<Bf16>, grid, dim3(64), 0, s, a);
+    const void* out[] = {y};
+    const int64_t out_ld[] = {launch->d_inner};
+    const bool f32 = launch->io_dtype == VIMSCAN_F32;
+    if (by_four(g, launch->d_inner, f32 ? 4 : 2, out, out_ld, 1)) {
+        if (f32) launch_fwd<float, 4>(a, p, s);
+        else launch_fwd<Bf16, 4>(a, p, s);
+    } else {
+        if (f32) launch_fwd<float, 1>(a, p, s);
+        else launch_fwd<Bf16, 1>(a, p, s);
+    }
     if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
     return VIMSCAN_OK;
 }
@@ -307,17 +960,25 @@ int vimscan_gated_bwd(const vimscan_gated* g, int64_t seg_len, const vimscan_gat
     a.ld_di = grad->ld_di;
     a.dlam = grad->dlam;
     a.dh0 = grad->dh0;
-    a.part = static_cast<float*>(launch->workspace);
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
     if (p.wgs > 0) {
-        const dim3 grid(static_cast<unsigned>(p.wgs));
-        if (launch->io_dtype == VIMSCAN_F32) hipLaunchKernelGGL(k_gated_bwd<float>, grid, dim3(64), 0, s, a);
-        else hipLaunchKernelGGL(k_gated_bwd<Bf16>, grid, dim3(64), 0, s, a);
+        const void* more[] = {grad->dy, grad->dx, grad->dr, grad->di};
+        const int64_t lds[] = {grad->ld_dy, grad->ld_dx, grad->ld_dr, grad->ld_di};
+        const bool f32 = launch->io_dtype == VIMSCAN_F32;
+        if (by_four(g, launch->d_inner, f32 ? 4 : 2, more, lds, 4)) {
+            if (f32) launch_bwd<float, 4>(a, p, s);
+            else launch_bwd<Bf16, 4>(a, p, s);
+        } else {
+            if (f32) launch_bwd<float, 1>(a, p, s);
+            else launch_bwd<Bf16, 1>(a, p, s);
+        }
     }
     if (a.dlam) {
         const unsigned blocks = static_cast<unsigned>((launch->d_inner + 63) / 64);
-        hipLaunchKernelGGL(k_gated_dlam, dim3(blocks), dim3(64), 0, s, a, p.nseq);
+        const int parts = p.tokens > 0 && p.wgs > 0 ? static_cast<int>(p.tiles) : 0;
+        a.ncb = static_cast<int32_t>(blocks);
+        hipLaunchKernelGGL(k_gated_dlam, dim3(blocks), dim3(1024), 0, s, a, parts);
     }
     if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
     return VIMSCAN_OK;

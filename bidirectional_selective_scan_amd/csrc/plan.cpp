@@ -123,7 +123,7 @@ const char* const kStatusText[] = {
     "unknown flag bits",
     "bad convolution: k must be 1..4",
     "the call needs more scratch than the allocation-free entry point's static array holds (96 MiB)",
-    "bad parameter: c or eps not positive and finite, a row stride below d_inner or at least 2^24, or arguments that "
+    "bad parameter: c or eps not positive and finite, a row stride below d_inner or at least 2^22, or arguments that "
     "exclude each other",
 };
 

@@ -61,11 +61,15 @@
 #include <cstring>
 #include <mutex>
 
+#include "block_plan.h"
+#include "handover.h"
 #include "plan.h"
 #include "vimscan.h"
 
 namespace {
 
+using vimscan_dev::dispatch_tag;
+using vimscan_dev::kSpinLimit;
 using vimscan_host::kFoldMaxChunks;
 using vimscan_host::kMaxTaps;
 using vimscan_host::kN;
@@ -1078,26 +1082,9 @@ __global__ __launch_bounds__(256) void k_chunk_aggregate(ScanArgs a) {
 // and complete, and so on group by group. The wait is bounded all the same (kSpinLimit reads,
 // about a second): past it the wave goes on, its output is unspecified, and it counts itself in
 // g_wait_timeouts (vimscan_wait_timeouts).
-constexpr int kSpinLimit = 1 << 20;
-
 // Waits of the one-kernel chunked scans on this GPU that ran past kSpinLimit since the library was
 // loaded (none is expected: see the progress argument above).
 __device__ unsigned long long g_wait_timeouts;
-
-// llvm.amdgcn.dispatch.id: the dispatch packet's index in its queue, which the command processor
-// writes into two SGPRs of every wave it launches.
-extern "C" __device__ uint64_t vimscan_dispatch_id() __asm("llvm.amdgcn.dispatch.id");
-
-// A tag unique to this kernel dispatch: the packet index and the queue's address, through the
-// splitmix64 finaliser (a bijection), so that tags of neighbouring dispatches differ in every bit
-// position; never zero.
-__device__ __forceinline__ uint64_t dispatch_tag() {
-    uint64_t v = vimscan_dispatch_id() ^
-                 (reinterpret_cast<uint64_t>(__builtin_amdgcn_queue_ptr()) * 0x9E3779B97F4A7C15ull);
-    v = (v ^ (v >> 30)) * 0xBF58476D1CE4E5B9ull;
-    v = (v ^ (v >> 27)) * 0x94D049BB133111EBull;
-    return (v ^ (v >> 31)) | 1u;
-}
 
 // The tag word of the aggregate of (dir, seq, chunk) for channel block cb.
 __device__ __forceinline__ uint64_t* tag_word(const ScanArgs& a, int dir, int seq, int chunk, int cb) {
@@ -1489,7 +1476,9 @@ int vimscan_wait_timeouts(uint64_t* count) {
     unsigned long long v = 0;
     if (hipMemcpyFromSymbol(&v, HIP_SYMBOL(g_wait_timeouts), sizeof(v), 0, hipMemcpyDeviceToHost) != hipSuccess)
         return VIMSCAN_ERR_HIP;
-    *count = static_cast<uint64_t>(v);
+    uint64_t gated = 0;
+    if (vimscan_host::gated_wait_timeouts(&gated) != VIMSCAN_OK) return VIMSCAN_ERR_HIP;
+    *count = static_cast<uint64_t>(v) + gated;
     return VIMSCAN_OK;
 }
 

@@ -72,7 +72,7 @@ enum vimscan_status {
     VIMSCAN_ERR_SCRATCH = -12,  /* vimscan_bidir_fwd_noalloc: the call needs more scratch than
                                    VIMSCAN_NOALLOC_SCRATCH_BYTES */
     VIMSCAN_ERR_PARAM = -13     /* gated recurrence, block norm: c or eps is not positive and
-                                   finite, a row stride is below d_inner or at least 2^24, or
+                                   finite, a row stride is below d_inner or at least 2^22, or
                                    arguments that exclude each other (each entry point names its
                                    own) */
 };
@@ -314,7 +314,7 @@ int vimscan_bidir_fwd_noalloc(const void* x, const void* dt, const void* z, cons
  * An empty sequence has h_last = h0 (0 without h0). Nothing of a sequence, NaN and infinities
  * included, reaches another sequence.
  *
- * Rows of x, r and i are ld_* elements apart (>= d_inner, < 2^24), so they may be slices of one
+ * Rows of x, r and i are ld_* elements apart (>= d_inner, < 2^22), so they may be slices of one
  * projection's output; a row's channels are contiguous. h0, h_last and lam are dense fp32.
  * launch->d_state must be 1 and chunk_len 0 (VIMSCAN_ERR_CHUNK); flags: VIMSCAN_FLAG_REVERSE only.
  * tokens = batch * seqlen < 2^31; there is no limit on tokens * d_inner short of 2^24 workgroups

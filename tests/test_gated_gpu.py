@@ -413,3 +413,20 @@ def test_refusals():
         state = torch.zeros(2, 16, device=DEV)
         PreparedGatedStep(x[:, 0], r[:, 0], i[:, 0], lam, state, out=state)()
     assert e.value.status == -6
+
+
+@pytest.mark.parametrize("seqlen,seg", [(2, 0), (3, 0), (7, 0), (1, 0), (130, 13), (66, 1), (66, 2)])
+@pytest.mark.parametrize("d", [68, 5])
+def test_nothing_is_written_past_the_last_sequence(seqlen, seg, d):
+    """Streams that end inside a thread's positions: rows around y and h_last stay as they are."""
+    p = Problem(3, seqlen, d, "f32", seg_len=seg, seed=seqlen)
+    nseq = len(p.bounds)
+    hbuf = torch.full((nseq + 8, d), 7.0, device=DEV)
+    ybuf = torch.full((3 * seqlen + 200, d), 7.0, device=DEV)
+    y, h = ybuf[100:100 + 3 * seqlen].view(3, seqlen, d), hbuf[4:4 + nseq]
+    PreparedGated(p.inputs(), None, None, None, out=y, h_last=h)()
+    want = p.reference(False)
+    ref.check(y, want["y"])
+    ref.check(h, want["h_last"])
+    assert bool((hbuf[:4] == 7).all()) and bool((hbuf[4 + nseq:] == 7).all())
+    assert bool((ybuf[:100] == 7).all()) and bool((ybuf[100 + 3 * seqlen:] == 7).all())
