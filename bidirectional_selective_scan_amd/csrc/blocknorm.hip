@@ -39,174 +39,378 @@ struct NormArgs {
     float* part;    // [workgroup][3][D] partial weight gradients, NULL when none is wanted
 };
 
-template <typename IO>
-__device__ __forceinline__ float ld(const void* p, int64_t k) {
-    Raw<IO, 1> w;
-    w.load(static_cast<const typename IoOf<IO>::elem*>(p) + k);
-    return w.get(0);
+// Sum over a wave, on the vector unit alone: within rows of 16 lanes by lane permutations of a quad and
+// mirrors, across rows by lane swaps. Every lane gets the same bits.
+template <int kCtrl>
+__device__ __forceinline__ float add_dpp(float v) {
+    return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), kCtrl, 0xf, 0xf, false));
 }
-template <typename IO>
-__device__ __forceinline__ void st(void* p, int64_t k, float v) {
-    Raw<IO, 1> w;
-    w.set(&v);
-    w.store(static_cast<typename IoOf<IO>::elem*>(p) + k);
-}
-template <typename IO>
-__device__ __forceinline__ float ld_res(const NormArgs& a, const void* p, int64_t k) {
-    return a.res_f32 ? ld<float>(p, k) : ld<IO>(p, k);
-}
-template <typename IO>
-__device__ __forceinline__ void st_res(const NormArgs& a, void* p, int64_t k, float v) {
-    if (a.res_f32) st<float>(p, k, v);
-    else st<IO>(p, k, v);
+__device__ __forceinline__ float wave_sum(float v) {
+    v = add_dpp<0xB1>(v);   // lane ^ 1
+    v = add_dpp<0x4E>(v);   // lane ^ 2
+    v = add_dpp<0x141>(v);  // half row mirrored
+    v = add_dpp<0x140>(v);  // row mirrored
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
-// Sum over the 256 threads of a workgroup, in a fixed order.
-__device__ __forceinline__ float wg_sum(float v, float* lds) {
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+// Sums of two values over the W waves of a row, in the waves' order. Calls alternate between two slots:
+// a slot is written again only after the barrier of the call between, which every wave reaches after
+// its reads of that slot, so one barrier a call is enough.
+template <int W>
+__device__ __forceinline__ void row_sum(float* u, float* v, float2 (*lds)[W], int& slot, int wave) {
+    *u = wave_sum(*u);
+    *v = wave_sum(*v);
+    if constexpr (W > 1) {
+        slot ^= 1;
+        if ((threadIdx.x & 63) == 0) lds[slot][wave] = make_float2(*u, *v);
+        __syncthreads();
+        float su = 0.0f, sv = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            su += lds[slot][k].x;
+            sv += lds[slot][k].y;
+        }
+        *u = su;
+        *v = sv;
+    }
 }
 
 __device__ __forceinline__ float sigmoid(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
 
-// One channel's way through the row: what the later stages need of it.
-struct Chan {
-    float x, gate, v, q, p, s;
+// How a row is spread: W waves, each lane NV vectors of V consecutive channels.
+template <int V, int NV, int W> struct Spread {
+    static constexpr int kThreads = W > 4 ? 64 * W : 256;
+    static constexpr int kRows = kThreads / (64 * W);  // rows a workgroup works on at once
+    __device__ __forceinline__ static int channel(int wave, int lane, int k) { return ((k * W + wave) * 64 + lane) * V; }
 };
-template <typename IO>
-__device__ __forceinline__ void stage_v(const NormArgs& a, int64_t row, int c, Chan& o) {
-    o.x = ld<IO>(a.x, row * a.ld_x + c);
-    o.gate = 1.0f;
-    if (a.z) {
-        const float z = ld<IO>(a.z, row * a.ld_z + c);
-        o.gate = z * sigmoid(z);
+
+template <typename T, int V, int NV, typename S>
+__device__ __forceinline__ void ld_row(const void* base, int64_t at, bool there, int D, int wave, int lane, Raw<T, V> (&o)[NV]) {
+    const IoElem<T>* p = static_cast<const IoElem<T>*>(base) + at;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = S::channel(wave, lane, k);
+        if (there && c < D) o[k].load(p + c);
+        else o[k].zero();
     }
-    o.v = a.after ? o.x : o.x * o.gate;
 }
-template <typename IO>
-__device__ __forceinline__ void stage_s(const NormArgs& a, int64_t row, int c, float rho1, Chan& o) {
-    o.q = a.w_post ? o.v * rho1 * a.w_post[c] : o.v;
-    o.p = a.after ? o.q * o.gate : o.q;
-    o.s = a.gamma ? o.p * a.gamma[c] : o.p;
-    if (a.residual) o.s += ld_res<IO>(a, a.residual, row * a.D + c);
+template <typename T, int V, int NV, typename S>
+__device__ __forceinline__ void st_row(void* base, int64_t at, int D, int wave, int lane, const float (&v)[NV][V]) {
+    IoElem<T>* p = static_cast<IoElem<T>*>(base) + at;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = S::channel(wave, lane, k);
+        if (c < D) {
+            Raw<T, V> o;
+            o.set(v[k]);
+            o.store(p + c);
+        }
+    }
+}
+// A weight's channels (1 where the weight is absent).
+template <int V, int NV, typename S>
+__device__ __forceinline__ void ld_weight(const float* w, int D, int wave, int lane, float (&o)[NV][V]) {
+    Raw<float, V> r[NV];
+    ld_row<float, V, NV, S>(w, 0, w != nullptr, D, wave, lane, r);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[k][v] = w ? r[k].get(v) : 1.0f;
 }
 
-// A workgroup per row; every stage reads the row again.
-template <typename IO>
-__global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
-    __shared__ float lds[4];
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        Chan o;
-        float rho1 = 1.0f, rho2 = 0.0f;
+// Forward: a row stays in registers from its one read to its one write.
+template <typename IO, typename RES, int V, int NV, int W>
+__global__ __launch_bounds__((Spread<V, NV, W>::kThreads)) void k_norm_fwd(NormArgs a) {
+    using S = Spread<V, NV, W>;
+    __shared__ float2 lds[2][W];
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6), wave = w % W;
+    float wp[NV][V], ga[NV][V], wn[NV][V];
+    ld_weight<V, NV, S>(a.w_post, a.D, wave, lane, wp);
+    ld_weight<V, NV, S>(a.gamma, a.D, wave, lane, ga);
+    ld_weight<V, NV, S>(a.w_pre, a.D, wave, lane, wn);
+    int slot = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * S::kRows + w / W; row < a.rows;
+         row += static_cast<int64_t>(gridDim.x) * S::kRows) {
+        Raw<IO, V> x[NV], z[NV];
+        Raw<RES, V> r[NV];
+        ld_row<IO, V, NV, S>(a.x, row * a.ld_x, true, a.D, wave, lane, x);
+        ld_row<IO, V, NV, S>(a.z, row * a.ld_z, a.z != nullptr, a.D, wave, lane, z);
+        ld_row<RES, V, NV, S>(a.residual, row * a.D, a.residual != nullptr, a.D, wave, lane, r);
+        float s[NV][V];
+        float ss = 0.0f, none = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[k][v] = x[k].get(v);
+                if (a.z && !a.after) {
+                    const float zv = z[k].get(v);
+                    s[k][v] *= zv * sigmoid(zv);
+                }
+                ss = fmaf(s[k][v], s[k][v], ss);
+            }
+        float rho = 1.0f;
         if (a.w_post) {
-            float s = 0.0f;
-            for (int c = threadIdx.x; c < a.D; c += 256) {
-                stage_v<IO>(a, row, c, o);
-                s = fmaf(o.v, o.v, s);
+            row_sum<W>(&ss, &none, lds, slot, wave);
+            rho = fast_rsq(fmaf(ss, a.inv_d, a.eps));
+        }
+        ss = none = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[k][v] *= rho * wp[k][v];
+                if (a.after) {
+                    const float zv = z[k].get(v);
+                    s[k][v] *= zv * sigmoid(zv);
+                }
+                s[k][v] = fmaf(s[k][v], ga[k][v], r[k].get(v));
+                ss = fmaf(s[k][v], s[k][v], ss);
             }
-            rho1 = fast_rsq(fmaf(wg_sum(s, lds), a.inv_d, a.eps));
-        }
-        if (a.w_pre) {
-            float s = 0.0f;
-            for (int c = threadIdx.x; c < a.D; c += 256) {
-                stage_v<IO>(a, row, c, o);
-                stage_s<IO>(a, row, c, rho1, o);
-                s = fmaf(o.s, o.s, s);
-            }
-            rho2 = fast_rsq(fmaf(wg_sum(s, lds), a.inv_d, a.eps));
-        }
-        for (int c = threadIdx.x; c < a.D; c += 256) {
-            stage_v<IO>(a, row, c, o);
-            stage_s<IO>(a, row, c, rho1, o);
-            if (a.sum) st_res<IO>(a, a.sum, row * a.D + c, o.s);
-            if (a.w_pre) st<IO>(a.n, row * a.D + c, o.s * rho2 * a.w_pre[c]);
-        }
+        if (a.sum) st_row<RES, V, NV, S>(a.sum, row * a.D, a.D, wave, lane, s);
+        if (!a.w_pre) continue;
+        row_sum<W>(&ss, &none, lds, slot, wave);
+        rho = fast_rsq(fmaf(ss, a.inv_d, a.eps));
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[k][v] *= rho * wn[k][v];
+        st_row<IO, V, NV, S>(a.n, row * a.D, a.D, wave, lane, s);
     }
 }
 
-template <typename IO>
-__global__ __launch_bounds__(256) void k_norm_bwd(NormArgs a) {
-    __shared__ float lds[4];
-    float* part = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.D : nullptr;
-    if (part)
-        for (int c = threadIdx.x; c < 3 * a.D; c += 256) part[c] = 0.0f;
-    __syncthreads();
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        Chan o;
+// Backward: the row's stages again from its inputs, then the gradients against them; the weights'
+// gradients of a wave's rows stay in registers, are added up over the workgroup's waves at the end and
+// left for k_norm_cols.
+template <typename IO, typename RES, int V, int NV, int W>
+__global__ __launch_bounds__((Spread<V, NV, W>::kThreads)) void k_norm_bwd(NormArgs a) {
+    using S = Spread<V, NV, W>;
+    __shared__ float2 lds[2][W];
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6), wave = w % W;
+    float wp[NV][V], ga[NV][V], wn[NV][V];
+    ld_weight<V, NV, S>(a.w_post, a.D, wave, lane, wp);
+    ld_weight<V, NV, S>(a.gamma, a.D, wave, lane, ga);
+    ld_weight<V, NV, S>(a.w_pre, a.D, wave, lane, wn);
+    float dwp[NV][V], dga[NV][V], dwn[NV][V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) dwp[k][v] = dga[k][v] = dwn[k][v] = 0.0f;
+    int slot = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * S::kRows + w / W; row < a.rows;
+         row += static_cast<int64_t>(gridDim.x) * S::kRows) {
+        Raw<IO, V> x[NV], z[NV], dn[NV];
+        Raw<RES, V> r[NV], ds[NV];
+        ld_row<IO, V, NV, S>(a.x, row * a.ld_x, true, a.D, wave, lane, x);
+        ld_row<IO, V, NV, S>(a.z, row * a.ld_z, a.z != nullptr, a.D, wave, lane, z);
+        ld_row<RES, V, NV, S>(a.residual, row * a.D, a.residual != nullptr, a.D, wave, lane, r);
+        ld_row<IO, V, NV, S>(a.dn, row * a.D, a.dn != nullptr, a.D, wave, lane, dn);
+        ld_row<RES, V, NV, S>(a.dsum, row * a.D, a.dsum != nullptr, a.D, wave, lane, ds);
+        // val: the post-norm's input; s: the sum
+        float val[NV][V], s[NV][V];
+        float u = 0.0f, t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                val[k][v] = x[k].get(v);
+                if (a.z && !a.after) {
+                    const float zv = z[k].get(v);
+                    val[k][v] *= zv * sigmoid(zv);
+                }
+                u = fmaf(val[k][v], val[k][v], u);
+            }
         float rho1 = 1.0f, rho2 = 0.0f, k2 = 0.0f;
         if (a.w_post) {
-            float s = 0.0f;
-            for (int c = threadIdx.x; c < a.D; c += 256) {
-                stage_v<IO>(a, row, c, o);
-                s = fmaf(o.v, o.v, s);
-            }
-            rho1 = fast_rsq(fmaf(wg_sum(s, lds), a.inv_d, a.eps));
+            row_sum<W>(&u, &t, lds, slot, wave);
+            rho1 = fast_rsq(fmaf(u, a.inv_d, a.eps));
         }
+        u = t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float p = val[k][v] * rho1 * wp[k][v];
+                if (a.after) {
+                    const float zv = z[k].get(v);
+                    p *= zv * sigmoid(zv);
+                }
+                s[k][v] = fmaf(p, ga[k][v], r[k].get(v));
+                u = fmaf(s[k][v], s[k][v], u);
+                t = fmaf(dn[k].get(v) * wn[k][v], s[k][v], t);
+            }
         if (a.dn) {
-            float s = 0.0f, t = 0.0f;
-            for (int c = threadIdx.x; c < a.D; c += 256) {
-                stage_v<IO>(a, row, c, o);
-                stage_s<IO>(a, row, c, rho1, o);
-                s = fmaf(o.s, o.s, s);
-                t = fmaf(ld<IO>(a.dn, row * a.D + c) * a.w_pre[c], o.s, t);
-            }
-            rho2 = fast_rsq(fmaf(wg_sum(s, lds), a.inv_d, a.eps));
-            k2 = wg_sum(t, lds) * a.inv_d * rho2 * rho2 * rho2;
+            row_sum<W>(&u, &t, lds, slot, wave);
+            rho2 = fast_rsq(fmaf(u, a.inv_d, a.eps));
+            k2 = t * a.inv_d * rho2 * rho2 * rho2;
         }
-        // gradient of s, then of q (the post-norm's output)
-        auto grads = [&](int c, float& ds, float& dp, float& dq) {
-            stage_v<IO>(a, row, c, o);
-            stage_s<IO>(a, row, c, rho1, o);
-            ds = a.dsum ? ld_res<IO>(a, a.dsum, row * a.D + c) : 0.0f;
-            if (a.dn) ds += rho2 * ld<IO>(a.dn, row * a.D + c) * a.w_pre[c] - o.s * k2;
-            dp = a.gamma ? ds * a.gamma[c] : ds;
-            dq = a.after ? dp * o.gate : dp;
-        };
+        // from here s is the gradient of the sum
+        u = t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float g = dn[k].get(v);
+                dwn[k][v] = fmaf(g, s[k][v] * rho2, dwn[k][v]);
+                s[k][v] = ds[k].get(v) + fmaf(rho2 * g, wn[k][v], -s[k][v] * k2);
+                const float q = val[k][v] * rho1 * wp[k][v], dp = s[k][v] * ga[k][v];
+                float p = q, dq = dp;
+                if (a.after) {
+                    const float zv = z[k].get(v), gate = zv * sigmoid(zv);
+                    p *= gate;
+                    dq *= gate;
+                }
+                dga[k][v] = fmaf(p, s[k][v], dga[k][v]);
+                dwp[k][v] = fmaf(dq, val[k][v] * rho1, dwp[k][v]);
+                u = fmaf(dq * wp[k][v], val[k][v], u);
+            }
+        if (a.dres) st_row<RES, V, NV, S>(a.dres, row * a.D, a.D, wave, lane, s);
         float k1 = 0.0f;
         if (a.w_post) {
-            float t = 0.0f;
-            for (int c = threadIdx.x; c < a.D; c += 256) {
-                float ds, dp, dq;
-                grads(c, ds, dp, dq);
-                t = fmaf(dq * a.w_post[c], o.v, t);
-            }
-            k1 = wg_sum(t, lds) * a.inv_d * rho1 * rho1 * rho1;
+            row_sum<W>(&u, &t, lds, slot, wave);
+            k1 = u * a.inv_d * rho1 * rho1 * rho1;
         }
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.D; c += 256) {
-            float ds, dp, dq;
-            grads(c, ds, dp, dq);
-            const float dn = a.dn ? ld<IO>(a.dn, row * a.D + c) : 0.0f;
-            const float dv = a.w_post ? rho1 * dq * a.w_post[c] - o.v * k1 : dq;
-            const float zv = a.z ? ld<IO>(a.z, row * a.ld_z + c) : 0.0f;
-            if (a.dres) st_res<IO>(a, a.dres, row * a.D + c, ds);
-            if (a.dx) st<IO>(a.dx, row * a.ld_dx + c, a.after ? dv : dv * o.gate);
-            if (a.dz) {
-                const float sg = sigmoid(zv);
-                const float slope = sg * fmaf(zv, 1.0f - sg, 1.0f);
-                st<IO>(a.dz, row * a.ld_dz + c, (a.after ? dp * o.q : dv * o.x) * slope);
+        float dz[NV][V];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float dp = s[k][v] * ga[k][v];
+                float gate = 1.0f, slope = 0.0f;
+                if (a.z) {
+                    const float zv = z[k].get(v), sg = sigmoid(zv);
+                    gate = zv * sg;
+                    slope = sg * fmaf(zv, 1.0f - sg, 1.0f);
+                }
+                const float dq = a.after ? dp * gate : dp;
+                const float dv = fmaf(rho1 * dq, wp[k][v], -val[k][v] * k1);
+                const float q = val[k][v] * rho1 * wp[k][v];
+                dz[k][v] = (a.after ? dp * q : dv * x[k].get(v)) * slope;
+                s[k][v] = a.after ? dv : dv * gate;
             }
-            if (part) {
-                part[c] += dq * o.v * rho1;
-                part[a.D + c] += o.p * ds;
-                part[2 * a.D + c] += dn * o.s * rho2;
+        if (a.dx) st_row<IO, V, NV, S>(a.dx, row * a.ld_dx, a.D, wave, lane, s);
+        if (a.dz) st_row<IO, V, NV, S>(a.dz, row * a.ld_dz, a.D, wave, lane, dz);
+    }
+    if (!a.part) return;
+    float* part = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.D;
+    if constexpr (S::kRows == 1) {
+        st_row<float, V, NV, S>(part, 0, a.D, wave, lane, dwp);
+        st_row<float, V, NV, S>(part, a.D, a.D, wave, lane, dga);
+        st_row<float, V, NV, S>(part, 2 * a.D, a.D, wave, lane, dwn);
+    } else {
+        // the workgroup's waves in their order, one weight at a time
+        __shared__ float col[NV * 64 * V];
+        auto add_up = [&](float (&g)[NV][V], int which) {
+            for (int turn = 0; turn < S::kRows; ++turn) {
+                if (w == turn) {
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            float* p = col + (k * V + v) * 64 + lane;
+                            if (turn > 0) g[k][v] += *p;
+                            *p = g[k][v];
+                        }
+                    if (turn == S::kRows - 1) st_row<float, V, NV, S>(part, which * a.D, a.D, wave, lane, g);
+                }
+                __syncthreads();
             }
-        }
-        __syncthreads();
+        };
+        add_up(dwp, 0);
+        add_up(dga, 1);
+        add_up(dwn, 2);
     }
 }
 
-// The weight gradients: the workgroups' partial sums in their order.
-__global__ __launch_bounds__(64) void k_norm_cols(NormArgs a, int parts) {
-    const int c = static_cast<int>(blockIdx.x) * 64 + static_cast<int>(threadIdx.x);
+// The weight gradients: the workgroups' partial sums, 16 waves taking every 16th each, then the waves in
+// their order.
+__global__ __launch_bounds__(1024) void k_norm_cols(NormArgs a, int parts) {
+    __shared__ float lds[16][64];
+    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
+    const int c = static_cast<int>(blockIdx.x) * 64 + lane;
     float* dst = a.dw[blockIdx.y];
-    if (c >= a.D || !dst) return;
+    if (!dst) return;
     float s = 0.0f;
-    for (int k = 0; k < parts; ++k) s += a.part[(static_cast<int64_t>(k) * 3 + blockIdx.y) * a.D + c];
+    if (c < a.D) {
+#pragma unroll 8
+        for (int k = wave; k < parts; k += 16) s += a.part[(static_cast<int64_t>(k) * 3 + blockIdx.y) * a.D + c];
+    }
+    lds[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= a.D) return;
+    s = 0.0f;
+    for (int k = 0; k < 16; ++k) s += lds[k][lane];
     dst[c] = s;
+}
+
+// Wide loads where every row of every tensor, and every weight, is aligned to them.
+bool by_four(const NormArgs& a, size_t e, size_t re) {
+    auto ok = [](const void* p, int64_t ld, size_t size) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && ld % 4 == 0);
+    };
+    const int64_t d = a.D;
+    bool r = d % 4 == 0 && ok(a.x, a.ld_x, e) && ok(a.z, a.ld_z, e) && ok(a.n, d, e) && ok(a.dn, d, e) &&
+             ok(a.dx, a.ld_dx, e) && ok(a.dz, a.ld_dz, e);
+    const void* rs[] = {a.residual, a.sum, a.dsum, a.dres};
+    for (const void* p : rs) r = r && ok(p, d, re);
+    const void* ws[] = {a.w_post, a.gamma, a.w_pre};
+    for (const void* p : ws) r = r && ok(p, d, 4);
+    return r;
+}
+
+template <typename IO, typename RES, int V, int NV, int W>
+void launch(const NormArgs& a, const NormPlan& p, bool back, hipStream_t s) {
+    using S = Spread<V, NV, W>;
+    const int64_t full = (a.rows + S::kRows - 1) / S::kRows;
+    const dim3 grid(static_cast<unsigned>(full < p.wgs ? full : p.wgs)), block(S::kThreads);
+    if (back) hipLaunchKernelGGL((k_norm_bwd<IO, RES, V, NV, W>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_norm_fwd<IO, RES, V, NV, W>), grid, block, 0, s, a);
+    if (back && a.part)
+        hipLaunchKernelGGL(k_norm_cols, dim3(static_cast<unsigned>((a.D + 63) / 64), 3), dim3(1024), 0, s, a,
+                           static_cast<int>(grid.x));
+}
+
+// The narrowest spread that holds the row.
+template <typename IO, typename RES>
+void launch_any(const NormArgs& a, const NormPlan& p, bool back, hipStream_t s) {
+    const int d = a.D;
+    if (by_four(a, sizeof(IoElem<IO>), sizeof(IoElem<RES>))) {
+        if (d <= 256) launch<IO, RES, 4, 1, 1>(a, p, back, s);
+        else if (d <= 512) launch<IO, RES, 4, 2, 1>(a, p, back, s);
+        else if (d <= 768) launch<IO, RES, 4, 3, 1>(a, p, back, s);
+        else if (d <= 1024) launch<IO, RES, 4, 4, 1>(a, p, back, s);
+        else if (d <= 2048) launch<IO, RES, 4, 2, 4>(a, p, back, s);
+        else if (d <= 4096) launch<IO, RES, 4, 4, 4>(a, p, back, s);
+        else if (d <= 8192) launch<IO, RES, 4, 4, 8>(a, p, back, s);
+        else if (d <= 16384) launch<IO, RES, 4, 4, 16>(a, p, back, s);
+        else launch<IO, RES, 4, 8, 16>(a, p, back, s);
+    } else {
+        if (d <= 256) launch<IO, RES, 1, 4, 1>(a, p, back, s);
+        else if (d <= 512) launch<IO, RES, 1, 8, 1>(a, p, back, s);
+        else if (d <= 1024) launch<IO, RES, 1, 4, 4>(a, p, back, s);
+        else if (d <= 2048) launch<IO, RES, 1, 8, 4>(a, p, back, s);
+        else if (d <= 4096) launch<IO, RES, 1, 16, 4>(a, p, back, s);
+        else if (d <= 8192) launch<IO, RES, 1, 16, 8>(a, p, back, s);
+        else if (d <= 16384) launch<IO, RES, 1, 16, 16>(a, p, back, s);
+        else launch<IO, RES, 1, 32, 16>(a, p, back, s);
+    }
+}
+
+void launch_typed(const NormArgs& a, const NormPlan& p, int io, bool back, hipStream_t s) {
+    if (io == VIMSCAN_F32) launch_any<float, float>(a, p, back, s);
+    else if (a.res_f32) launch_any<Bf16, float>(a, p, back, s);
+    else launch_any<Bf16, Bf16>(a, p, back, s);
+}
+
+// An empty backward pass: weight gradients of zero.
+__global__ __launch_bounds__(64) void k_norm_zero(NormArgs a) {
+    const int c = static_cast<int>(blockIdx.x) * 64 + static_cast<int>(threadIdx.x);
+    if (c < a.D && a.dw[blockIdx.y]) a.dw[blockIdx.y][c] = 0.0f;
 }
 
 NormArgs common_args(const vimscan_norm* n, const vimscan_launch* l, const NormPlan& p) {
@@ -250,9 +454,7 @@ int vimscan_norm_fwd(const vimscan_norm* n, void* sum, void* out, const vimscan_
     a.n = out;
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
-    const dim3 grid(static_cast<unsigned>(p.wgs));
-    if (launch->io_dtype == VIMSCAN_F32) hipLaunchKernelGGL(k_norm_fwd<float>, grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(k_norm_fwd<Bf16>, grid, dim3(256), 0, s, a);
+    launch_typed(a, p, launch->io_dtype, false, s);
     if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
     return VIMSCAN_OK;
 }
@@ -279,15 +481,9 @@ int vimscan_norm_bwd(const vimscan_norm* n, const vimscan_norm_grad* grad, const
     a.part = weights ? static_cast<float*>(launch->workspace) : nullptr;
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
-    if (p.wgs > 0) {
-        const dim3 grid(static_cast<unsigned>(p.wgs));
-        if (launch->io_dtype == VIMSCAN_F32) hipLaunchKernelGGL(k_norm_bwd<float>, grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(k_norm_bwd<Bf16>, grid, dim3(256), 0, s, a);
-    }
-    if (weights) {
-        const dim3 grid(static_cast<unsigned>((p.D + 63) / 64), 3);
-        hipLaunchKernelGGL(k_norm_cols, grid, dim3(64), 0, s, a, static_cast<int>(p.wgs));
-    }
+    if (p.wgs > 0) launch_typed(a, p, launch->io_dtype, true, s);
+    else if (weights)
+        hipLaunchKernelGGL(k_norm_zero, dim3(static_cast<unsigned>((p.D + 63) / 64), 3), dim3(64), 0, s, a);
     if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
     return VIMSCAN_OK;
 }
