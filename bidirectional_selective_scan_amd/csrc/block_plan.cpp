@@ -98,9 +98,8 @@ int make_gated_plan(const vimscan_launch* l, int64_t seg_len, bool packed, int64
     p->chain = p->tiles > 1 && (packed || p->tile % p->Lp != 0);
     const size_t width = static_cast<size_t>(p->ncb) * kGatedBlock;
     if (p->chain) {
-        p->off_inc = up256(static_cast<size_t>(p->tiles) * width * 2 * sizeof(float));
-        p->off_tags = p->off_inc + up256(static_cast<size_t>(p->groups) * width * sizeof(float));
-        p->off_part = p->off_tags + up256(static_cast<size_t>(p->tiles + p->groups) * p->ncb * sizeof(uint64_t));
+        p->off_inc = up256(static_cast<size_t>(p->tiles) * width * 2 * sizeof(uint64_t));
+        p->off_part = p->off_inc + up256(static_cast<size_t>(p->groups) * width * 2 * sizeof(uint64_t));
         p->ws = p->off_part;
     }
     if (backward && p->tokens > 0) p->ws += up256(static_cast<size_t>(p->tiles) * width * sizeof(float));

@@ -23,7 +23,7 @@ constexpr int kGatedFwdTile = 128;
 constexpr int kGatedBwdTile = 64;
 // Tiles per group of the hand-over: a tile folds the aggregates of the tiles before it in its group
 // onto the state that the group before left.
-constexpr int kGatedGroup = 32;
+constexpr int kGatedGroup = 16;
 static_assert(kGatedBwdTile == kGatedStride, "the backward pass starts each tile from a saved state");
 
 // Plan of a gated recurrence over whole sequences.
@@ -33,8 +33,8 @@ struct GatedPlan {
     int64_t ncb, wgs;
     bool packed;
     bool chain;                    // tiles hand states on to each other
-    // workspace: aggregates, group states and tags of the hand-over, partial sums of dlam
-    size_t off_inc, off_tags, off_part, ws;
+    // workspace: tile maps and group states of the hand-over, partial sums of dlam
+    size_t off_inc, off_part, ws;
 };
 
 int make_gated_plan(const vimscan_launch* l, int64_t seg_len, bool packed, int64_t nseq, bool backward, GatedPlan* p);

@@ -58,6 +58,7 @@ struct GatedArgs {
     float c;
     int32_t N;               // tokens
     int32_t Lp;
+    uint32_t lp_mul, lp_shift;  // position / Lp = position * lp_mul >> lp_shift (Lp > 0)
     int32_t D, nseq, ncb, tiles;
     int32_t rev;             // walk from the last token to the first
     void* y;
@@ -74,9 +75,8 @@ struct GatedArgs {
     float* dlam;
     float* dh0;
     // workspace
-    float2* agg;             // [tile][width] maps (A, H), width = 64 ncb
-    float* inc;              // [group][width] the state a group leaves
-    uint64_t* tags;          // [tile][ncb], then [group][ncb]
+    uint64_t* agg;           // [tile][width][2] maps handed over, width = 64 ncb
+    uint64_t* inc;           // [group][width][2] the state a group leaves
     float* part;             // [tile][width] partial sums of dlam
 };
 
@@ -93,10 +93,14 @@ __device__ __forceinline__ int bound_of(const GatedArgs& a, int q) {
     return a.rev ? a.N - in : in;
 }
 
+__device__ __forceinline__ int uniform_seq(const GatedArgs& a, int p) {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(p)) * a.lp_mul >> a.lp_shift);
+}
+
 // The last sequence of lo..hi that starts at or before position p (lo when none does): the one that
 // holds p, empty ones being passed over.
 __device__ __forceinline__ int seq_at(const GatedArgs& a, int p, int lo, int hi) {
-    if (!a.offsets) return p / a.Lp;
+    if (!a.offsets) return uniform_seq(a, p);
     while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
         if (bound_of(a, mid) <= p) lo = mid;
@@ -107,7 +111,7 @@ __device__ __forceinline__ int seq_at(const GatedArgs& a, int p, int lo, int hi)
 
 // The same over all sequences, for a position that the whole wave shares: 64 probes a round.
 __device__ __forceinline__ int seq_at_wave(const GatedArgs& a, int p, int lane) {
-    if (!a.offsets) return p / a.Lp;
+    if (!a.offsets) return uniform_seq(a, p);
     int lo = 0, n = a.nseq;  // the answer is in lo .. lo + n - 1
     while (n > 1) {
         const int step = (n + 63) / 64;
@@ -120,6 +124,19 @@ __device__ __forceinline__ int seq_at_wave(const GatedArgs& a, int p, int lane) 
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// The sequences around a tile of positions p0 .. p1 - 1 (the same for every lane).
+struct TileSeqs {
+    int lo, hi;    // the sequences that hold the first and the last position
+    int start;     // first position of sequence lo
+    bool any;      // a sequence starts at p0, or ends inside the tile
+    __device__ __forceinline__ void init(const GatedArgs& a, int p0, int p1, int lane) {
+        lo = seq_at_wave(a, p0, lane);
+        start = bound_of(a, lo);
+        any = start == p0 || bound_of(a, lo + 1) <= p1;
+        hi = a.offsets && any ? seq_at_wave(a, p1 - 1, lane) : lo;
+    }
+};
+
 // The sequence boundaries among a thread's positions p .. p + T - 1 of the stream: bit k of starts
 // (ends) is set where position p + k is the first (last) of its sequence. No bit is set for a position
 // past the stream's end.
@@ -127,22 +144,22 @@ struct Cuts {
     uint32_t starts, ends;
 };
 template <int T>
-__device__ __forceinline__ Cuts cuts_of(const GatedArgs& a, int p, int qlo, int qhi) {
+__device__ __forceinline__ Cuts cuts_of(const GatedArgs& a, int p, const TileSeqs& ts) {
     uint64_t m = 0;  // bit k: p + k is a boundary, the stream's end included
     const int n = min(T, a.N - p);
-    if (n <= 0) return {0, 0};
+    if (!ts.any || n <= 0) return {0, 0};
     if (!a.offsets) {
-        const int rem = p % a.Lp;
+        const int rem = p - uniform_seq(a, p) * a.Lp;
         for (int64_t o = rem ? a.Lp - rem : 0; o <= n; o += a.Lp) m |= uint64_t(1) << o;
     } else {
-        int q = seq_at(a, p, qlo, qhi);
+        int q = seq_at(a, p, ts.lo, ts.hi);
         if (bound_of(a, q) == p) m = 1;
         while (q < a.nseq) {
             const int o = bound_of(a, q + 1) - p;
             if (o > n || o <= 0) break;
             m |= uint64_t(1) << o;
             if (o == n) break;
-            const int next = seq_at(a, p + o, q + 1, qhi);
+            const int next = seq_at(a, p + o, q + 1, ts.hi);
             if (next <= q) break;
             q = next;
         }
@@ -164,38 +181,35 @@ __device__ __forceinline__ float decay_rate(float lam, float c) {
 }
 
 // 1 - a^2 with a = 2^q, q <= 0: 1 - e^-t with t = -2 q ln 2. Small t by its series (the sixth power
-// at t = 1/4 is 5e-8 of the result), larger t from a itself.
+// at t = 1/4 is 5e-8 of the result), written in q; larger t from a itself.
 __device__ __forceinline__ float one_minus_sq(float q, float a) {
-    const float t = -2.0f * kLn2 * q;
-    float s = fmaf(t, -1.0f / 720.0f, 1.0f / 120.0f);
-    s = fmaf(t, -s, 1.0f / 24.0f);
-    s = fmaf(t, -s, 1.0f / 6.0f);
-    s = fmaf(t, -s, 0.5f);
-    s = fmaf(t, -s, 1.0f);
-    return t < 0.25f ? t * s : fmaf(-a, a, 1.0f);
+    constexpr double z = -2.0 * 0.693147180559945309417;
+    constexpr float c1 = float(z), c2 = float(-z * z / 2), c3 = float(z * z * z / 6), c4 = float(-z * z * z * z / 24),
+                    c5 = float(z * z * z * z * z / 120), c6 = float(-z * z * z * z * z * z / 720);
+    float s = fmaf(q, c6, c5);
+    s = fmaf(q, s, c4);
+    s = fmaf(q, s, c3);
+    s = fmaf(q, s, c2);
+    s = fmaf(q, s, c1);
+    return q > float(0.25 / z) ? q * s : fmaf(-a, a, 1.0f);
 }
 
-struct Gates {
-    float s, ns;   // sigmoid(r) and 1 - sigmoid(r)
-    float g, ng;   // sigmoid(i) and 1 - sigmoid(i)
-    float q, a, m; // u log2(e), exp(u), sqrt(1 - a^2)
-};
+// sigmoid(v) = 1 / (1 + e^-v)
+__device__ __forceinline__ float sigmoid(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
 
-// sigmoid(v) = 1 / (1 + e), 1 - sigmoid(v) = e / (1 + e) with e = e^-v held below 2^126.
-__device__ __forceinline__ void sigmoid2(float v, float* s, float* ns) {
+// The same and 1 - sigmoid(v) = e / (1 + e), e = e^-v held below 2^126.
+__device__ __forceinline__ float sigmoid2(float v, float* ns) {
     const float e = fast_exp2(fminf(-v * kLog2e, 126.0f));
-    *s = fast_rcp(1.0f + e);
-    *ns = e * *s;
+    const float s = fast_rcp(1.0f + e);
+    *ns = e * s;
+    return s;
 }
 
-__device__ __forceinline__ Gates gates(float r, float i, float k2) {
-    Gates o;
-    sigmoid2(r, &o.s, &o.ns);
-    sigmoid2(i, &o.g, &o.ng);
-    o.q = k2 * o.s;
-    o.a = fast_exp2(o.q);
-    o.m = fast_sqrt(one_minus_sq(o.q, o.a));
-    return o;
+// Transition a and input gate m sigmoid(i) of a position.
+__device__ __forceinline__ void gates(float r, float i, float k2, float* a, float* mg) {
+    const float q = k2 * sigmoid(r);
+    *a = fast_exp2(q);
+    *mg = fast_sqrt(one_minus_sq(q, *a)) * sigmoid(i);
 }
 
 // The rows of a tile of one tensor as a buffer resource, rows in walking order. A position past the
@@ -203,27 +217,27 @@ __device__ __forceinline__ Gates gates(float r, float i, float k2) {
 // gives 0 for such a load and drops such a store.
 constexpr uint32_t kOutside = 0x80000000u;
 
+// The thread's T positions from tg * T on of a tile of TILE positions from p0.
+template <typename IO, int TILE, int T>
 struct TileRows {
     __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t row_bytes;
-    uint32_t vo;         // the thread's first row (in memory order) and channel
+    uint32_t vo;             // the thread's lowest row in memory, and its channel
+    uint32_t so, step;       // scalar offset of its first position, and from one to the next
 
-    // A tile of tile positions from p0, of which the thread takes T from tg * T on.
-    template <typename IO, int T>
-    __device__ __forceinline__ void init(const GatedArgs& a, const void* base, int64_t ld, int p0, int tile, int tg, int c0) {
-        const int64_t first = a.rev ? static_cast<int64_t>(a.N) - p0 - tile : p0;  // the tile's lowest row
+    __device__ __forceinline__ void init(const GatedArgs& a, const void* base, int64_t ld, int p0, int tg, int c0) {
+        const int64_t first = a.rev ? static_cast<int64_t>(a.N) - p0 - TILE : p0;  // the tile's lowest row
         const uint64_t at = reinterpret_cast<uint64_t>(base) + first * ld * static_cast<int64_t>(sizeof(IoElem<IO>));
         const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
         const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
         rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0,
                                                  0x7fffffff, 0x00020000);
-        row_bytes = static_cast<uint32_t>(ld) * sizeof(IoElem<IO>);
-        const int row = (a.rev ? tile / T - 1 - tg : tg) * T;
-        vo = row * row_bytes + c0 * static_cast<uint32_t>(sizeof(IoElem<IO>));
+        const uint32_t row_bytes = static_cast<uint32_t>(ld) * sizeof(IoElem<IO>);
+        const int row = (a.rev ? TILE / T - 1 - tg : tg) * T;
+        vo = c0 < a.D && base ? row * row_bytes + c0 * static_cast<uint32_t>(sizeof(IoElem<IO>)) : kOutside;
+        so = a.rev ? (T - 1) * row_bytes : 0;
+        step = a.rev ? 0u - row_bytes : row_bytes;
     }
-    __device__ __forceinline__ uint32_t so(const GatedArgs& a, int k, int T) const {
-        return (a.rev ? T - 1 - k : k) * row_bytes;
-    }
+    __device__ __forceinline__ uint32_t at(bool in) const { return in ? vo : kOutside; }
 };
 
 template <typename IO, int V>
@@ -298,10 +312,17 @@ __device__ __forceinline__ void swap32(float v, float* lo, float* hi) {
 // and before: the map of the groups before this lane's in walking order, or after it with kBack.
 template <int CL, bool kBack>
 __device__ __forceinline__ void scan_rows(const Map& f, int lane, Map* total, Map* before) {
-    static_assert(CL == 16 || CL == 64, "one or four position groups in a wave");
+    static_assert(CL == 16 || CL == 32 || CL == 64, "one, two or four position groups in a wave");
     if constexpr (CL == 64) {
         *total = f;
         *before = identity();
+    } else if constexpr (CL == 32) {
+        Map lo, hi;
+        swap32(f.A, &lo.A, &hi.A);
+        swap32(f.H, &lo.H, &hi.H);
+        const bool upper = lane & 32;
+        *total = kBack ? then(hi, lo) : then(lo, hi);
+        *before = kBack ? pick(upper, identity(), hi) : pick(upper, lo, identity());
     } else {
         Map e, o, lo, hi;
         swap16(f.A, &e.A, &o.A);
@@ -325,11 +346,6 @@ __device__ __forceinline__ void scan_rows(const Map& f, int lane, Map* total, Ma
 // Waits of this file's hand-over on this GPU that gave up after kSpinLimit reads.
 __device__ unsigned long long g_wait_timeouts;
 
-__device__ __forceinline__ void publish(uint64_t* word, uint64_t tag, int lane) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the values' stores have completed
-    if (lane == 0) __hip_atomic_store(word, tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
 // LDS of the hand-over.
 struct ChainLds {
     float2 wave[4][kGatedBlock];   // the maps of the waves
@@ -337,13 +353,36 @@ struct ChainLds {
     float inc[kGatedBlock];        // the state that the group before left
 };
 
+// A value handed over: two 64-bit words, the value and the value xor the dispatch's tag, each stored and
+// loaded on its own (device-coherent, no order between them). A reader takes the value when the two
+// differ by exactly this dispatch's tag, so words of earlier dispatches, arbitrary bytes and half a
+// value never pass, the memory needs no clearing, and neither side waits for one access before the
+// next: a value costs its reader one trip to memory after it was stored.
+__device__ __forceinline__ void hand_over(uint64_t* w, uint64_t tag, float x, float y) {
+    const uint64_t v = __float_as_uint(x) | (static_cast<uint64_t>(__float_as_uint(y)) << 32);
+    __hip_atomic_store(w, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(w + 1, v ^ tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+struct Handed {
+    uint64_t v, c;
+    __device__ __forceinline__ void load(const uint64_t* w) {
+        v = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        c = __hip_atomic_load(w + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ bool there(uint64_t tag) const { return (v ^ c) == tag; }
+    __device__ __forceinline__ float x() const { return __uint_as_float(static_cast<uint32_t>(v)); }
+    __device__ __forceinline__ float y() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+};
+
 // Hand-over along the chain: workgroup j of channel block cb publishes its tile's map (every one but
-// the last, whatever the sequences: no wait depends on what the offsets hold) and gathers what comes in from tile first on (first == j: nothing comes in). Called
-// by all threads between the barrier that completes l.wave and one that completes l.part and l.inc.
-// kBack: the waves' maps compose from the last wave to the first.
+// the last, whatever the sequences: no wait depends on what the offsets hold) and gathers what comes
+// in from tile first on (first == j: nothing comes in). Called by all threads between the barrier that
+// completes l.wave and one that completes l.part and l.inc. kBack: the waves' maps compose from the
+// last wave to the first.
 template <bool kBack>
 __device__ __forceinline__ Map tile_map(const ChainLds& l, int lane) {
     Map f = identity();
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float2 w = l.wave[kBack ? 3 - k : k][lane];
         f = then(f, Map{w.x, w.y});
@@ -353,57 +392,46 @@ __device__ __forceinline__ Map tile_map(const ChainLds& l, int lane) {
 template <bool kBack>
 __device__ __forceinline__ void chain_gather(const GatedArgs& a, ChainLds& l, int j, int cb, int first, uint64_t tag,
                                              int wave, int lane) {
+    constexpr int kEach = kGatedGroup / 4;
     const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
     const int ch = cb * kGatedBlock + lane;
-    if (wave == 0 && j + 1 < a.tiles) {
+    if (wave == 3 && j + 1 < a.tiles) {
         const Map f = tile_map<kBack>(l, lane);
-        const uint64_t v = __float_as_uint(f.A) | (static_cast<uint64_t>(__float_as_uint(f.H)) << 32);
-        __hip_atomic_store(reinterpret_cast<uint64_t*>(a.agg + j * width + ch), v, __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
-        publish(a.tags + static_cast<int64_t>(j) * a.ncb + cb, tag, lane);
+        hand_over(a.agg + 2 * (j * width + ch), tag, f.A, f.H);
     }
     const int group = j / kGatedGroup, g0 = group * kGatedGroup;
     const bool from_group = first < g0;
-    const int lo = (from_group ? g0 : first) + wave * (kGatedGroup / 4);   // this wave's tiles: lo .. lo + n - 1
-    const int n = min(j - lo, kGatedGroup / 4);
+    const int lo = (from_group ? g0 : first) + wave * kEach;   // this wave's tiles: lo .. lo + n - 1
+    const int n = min(j - lo, kEach);
     const bool inc = from_group && wave == 0;
-    const uint64_t* word = a.tags + static_cast<int64_t>(lo + lane) * a.ncb + cb;
-    const bool is_inc = inc && lane == 63;
-    if (is_inc) word = a.tags + (static_cast<int64_t>(a.tiles) + group - 1) * a.ncb + cb;
-    const bool mine = lane < n || is_inc;
-    bool done = n <= 0 && !inc;
-    for (int it = 0; it < kSpinLimit && !done; ++it) {
-        const bool ready = !mine || __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == tag;
-        done = __all(ready);
-        if (!done) __builtin_amdgcn_s_sleep(1);
+    Handed v[kEach], vi;
+    int todo = 0;  // bit k: tile lo + k is still awaited; bit kEach: the group's state
+    if (n > 0) todo = (1 << n) - 1;
+    if (inc) todo |= 1 << kEach;
+    for (int it = 0; todo && it < kSpinLimit; ++it) {
+        if (it > 0) __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (todo >> k & 1) v[k].load(a.agg + 2 * ((lo + k) * width + ch));
+        if (todo >> kEach) vi.load(a.inc + 2 * ((group - 1) * width + ch));
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if ((todo >> k & 1) && __all(v[k].there(tag))) todo &= ~(1 << k);
+        if ((todo >> kEach) && __all(vi.there(tag))) todo &= ~(1 << kEach);
     }
-    if (!done && lane == 0)
+    if (todo && lane == 0)
         __hip_atomic_fetch_add(&g_wait_timeouts, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    asm volatile("" ::: "memory");  // the loads of the values stay after the wait
     Map f = identity();
-    if (n > 0) {
-        uint64_t v[kGatedGroup / 4];
 #pragma unroll
-        for (int k = 0; k < kGatedGroup / 4; ++k) {
-            const int t = lo + (k < n ? k : n - 1);
-            v[k] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(a.agg + t * width + ch), __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
-        }
-#pragma unroll
-        for (int k = 0; k < kGatedGroup / 4; ++k) {
-            const Map g = {__uint_as_float(static_cast<uint32_t>(v[k])), __uint_as_float(static_cast<uint32_t>(v[k] >> 32))};
-            if (k < n) f = then(f, g);
-        }
-    }
+    for (int k = 0; k < kEach; ++k)
+        if (k < n) f = then(f, Map{v[k].x(), v[k].y()});
     l.part[wave][lane] = make_float2(f.A, f.H);
-    if (wave == 0) {
-        l.inc[lane] = inc ? __hip_atomic_load(a.inc + (group - 1) * width + ch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                          : 0.0f;
-    }
+    if (wave == 0) l.inc[lane] = inc ? vi.x() : 0.0f;
 }
 // What enters the tile in channel ch of the block (0 when nothing does).
 __device__ __forceinline__ float chain_carry(const ChainLds& l, int ch) {
     float h = l.inc[ch];
+#pragma unroll
     for (int k = 0; k < 4; ++k) h = Map{l.part[k][ch].x, l.part[k][ch].y}(h);
     return h;
 }
@@ -413,10 +441,8 @@ __device__ __forceinline__ void chain_leave(const GatedArgs& a, const ChainLds& 
                                             int lane) {
     if (wave != 0 || j + 1 >= a.tiles || j % kGatedGroup != kGatedGroup - 1) return;
     const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
-    const int group = j / kGatedGroup;
     const float h = tile_map<kBack>(l, lane)(chain_carry(l, lane));
-    __hip_atomic_store(a.inc + group * width + cb * kGatedBlock + lane, h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    publish(a.tags + (static_cast<int64_t>(a.tiles) + group) * a.ncb + cb, tag, lane);
+    hand_over(a.inc + 2 * (j / kGatedGroup * width + cb * kGatedBlock + lane), tag, h, 0.0f);
 }
 
 // Sequences without tokens: what comes out is what went in (0 without it). Shared out over the tiles.
@@ -432,74 +458,115 @@ __device__ __forceinline__ void pass_empty(const GatedArgs& a, const float* in, 
     }
 }
 
+// v[k] of the thread's positions for a k that differs between lanes.
+template <int T, int V>
+__device__ __forceinline__ void at_position(const float (&v)[T][V], int k, float (&o)[V]) {
+#pragma unroll
+    for (int n = 0; n < T; ++n)
+#pragma unroll
+        for (int c = 0; c < V; ++c) o[c] = n == 0 || n == k ? v[n][c] : o[c];
+}
+
+// The caller's row of the sequence that holds position p, first of the thread's channels.
+__device__ __forceinline__ int64_t seq_row(const GatedArgs& a, int p, const TileSeqs& ts, int c0) {
+    return seq_of(a, seq_at(a, p, ts.lo, ts.hi)) * a.D + c0;
+}
+
+// A sequence that starts among the thread's positions brings its initial state in: added to that
+// position's input.
+template <int T, int V>
+__device__ __forceinline__ void add_h0(const GatedArgs& a, uint32_t starts, int pt, const TileSeqs& ts, int c0,
+                                       const float (&av)[T][V], float (&bv)[T][V]) {
+    if (!a.h0 || c0 >= a.D) return;
+    for (; starts; starts &= starts - 1) {
+        const int k = __builtin_ctz(starts);
+        const float* h0 = a.h0 + seq_row(a, pt + k, ts, c0);
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = h0[v];
+#pragma unroll
+        for (int n = 0; n < T; ++n)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (n == k) bv[n][v] = fmaf(av[n][v], h[v], bv[n][v]);
+    }
+}
+
+// The map of the thread's positions, from the first to the last. kCut: some lane of the wave has a
+// sequence start among them.
+template <bool kCut, int T, int V>
+__device__ __forceinline__ void thread_map(uint32_t starts, const float (&av)[T][V], const float (&bv)[T][V], Map (&f)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = {av[0][v], bv[0][v]};
+#pragma unroll
+    for (int k = 1; k < T; ++k) {
+        const bool start = kCut && (starts >> k & 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float h = fmaf(av[k][v], f[v].H, bv[k][v]);
+            f[v].H = start ? bv[k][v] : h;
+            f[v].A *= av[k][v];
+        }
+    }
+    if constexpr (kCut) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v].A = starts ? -1.0f : f[v].A;
+    }
+}
+
 // Forward pass: a tile of kGatedFwdTile positions x 64 channels.
 template <typename IO, int V, bool kChain>
-__global__ __launch_bounds__(256) void k_gated_fwd(GatedArgs a) {
+__global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 ? 4 : 3) void k_gated_fwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedFwdTile / TG;
     __shared__ ChainLds lds;
     const int j = static_cast<int>(blockIdx.x) / a.ncb, cb = static_cast<int>(blockIdx.x) % a.ncb;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    pass_empty(a, a.h0, a.h_last, j, cb);
-    if (a.N == 0) return;
+    if (a.N == 0) return pass_empty(a, a.h0, a.h_last, j, cb);
     const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
     const bool live = c0 < a.D;
-    const int p0 = j * kGatedFwdTile, pt = p0 + tg * T;
+    const int p0 = j * kGatedFwdTile, pt = p0 + tg * T, p1 = min(p0 + kGatedFwdTile, a.N);
+    const bool full = p0 + kGatedFwdTile <= a.N;
 
-    Raw<IO, V> xr[T], rr[T], ir[T];
-    {
-        TileRows x, r, i;
-        x.init<IO, T>(a, a.x, a.ld_x, p0, kGatedFwdTile, tg, c0);
-        r.init<IO, T>(a, a.r, a.ld_r, p0, kGatedFwdTile, tg, c0);
-        i.init<IO, T>(a, a.i, a.ld_i, p0, kGatedFwdTile, tg, c0);
-#pragma unroll
-        for (int k = 0; k < T; ++k) {
-            const bool in = live && pt + k < a.N;
-            rr[k] = ld_tile<IO, V>(r.rsrc, in ? r.vo : kOutside, r.so(a, k, T));
-            ir[k] = ld_tile<IO, V>(i.rsrc, in ? i.vo : kOutside, i.so(a, k, T));
-            xr[k] = ld_tile<IO, V>(x.rsrc, in ? x.vo : kOutside, x.so(a, k, T));
-        }
-    }
     float k2[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) k2[v] = decay_rate(live ? a.lam[c0 + v] : 0.0f, a.c);
-
-    // the sequences around: where they start, and from which tile on a state comes in
-    const int p1 = min(p0 + kGatedFwdTile, a.N);
-    const int qlo = seq_at_wave(a, p0, lane);
-    const int qhi = a.offsets ? seq_at_wave(a, p1 - 1, lane) : 0;
-    const Cuts cut = cuts_of<T>(a, pt, qlo, qhi);
-    const bool starts = __any(cut.starts != 0), ends = __any(cut.ends != 0);
+    for (int v = 0; v < V; ++v) k2[v] = a.lam[live ? c0 + v : 0];
+    Raw<IO, V> xr[T], rr[T], ir[T];
+    {
+        TileRows<IO, kGatedFwdTile, T> x, r, i;
+        r.init(a, a.r, a.ld_r, p0, tg, c0);
+        i.init(a, a.i, a.ld_i, p0, tg, c0);
+        x.init(a, a.x, a.ld_x, p0, tg, c0);
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            const bool in = full || pt + k < a.N;
+            rr[k] = ld_tile<IO, V>(r.rsrc, r.at(in), r.so + k * r.step);
+            ir[k] = ld_tile<IO, V>(i.rsrc, i.at(in), i.so + k * i.step);
+            xr[k] = ld_tile<IO, V>(x.rsrc, x.at(in), x.so + k * x.step);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) k2[v] = decay_rate(k2[v], a.c);
+    TileSeqs ts;
+    ts.init(a, p0, p1, lane);
+    const Cuts cut = cuts_of<T>(a, pt, ts);
+    const bool starts = __any(cut.starts != 0);
 
     float av[T][V], bv[T][V];
     Map f[V], before[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = identity();
-#pragma unroll
-    for (int k = 0; k < T; ++k) {
+    for (int k = 0; k < T; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const Gates o = gates(rr[k].get(v), ir[k].get(v), k2[v]);
-            av[k][v] = o.a;
-            bv[k][v] = o.m * o.g * xr[k].get(v);
+            float mg;
+            gates(rr[k].get(v), ir[k].get(v), k2[v], &av[k][v], &mg);
+            bv[k][v] = mg * xr[k].get(v);
         }
-        const bool start = starts && (cut.starts >> k & 1);
-        if (start) {
-            if (a.h0) {
-                const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (live) bv[k][v] = fmaf(av[k][v], a.h0[slot + v], bv[k][v]);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = {-1.0f, bv[k][v]};
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                f[v].H = fmaf(av[k][v], f[v].H, bv[k][v]);
-                f[v].A = f[v].A < 0.0f ? f[v].A : f[v].A * av[k][v];
-            }
-        }
+    if (starts) {
+        add_h0(a, cut.starts, pt, ts, c0, av, bv);
+        thread_map<true>(cut.starts, av, bv, f);
+    } else {
+        thread_map<false>(0, av, bv, f);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -511,8 +578,7 @@ __global__ __launch_bounds__(256) void k_gated_fwd(GatedArgs a) {
     float h[V];
     if constexpr (kChain) {
         const uint64_t tag = dispatch_tag();
-        const int start = bound_of(a, qlo);
-        const int first = start >= p0 ? j : start / kGatedFwdTile;
+        const int first = ts.start >= p0 ? j : ts.start / kGatedFwdTile;
         chain_gather<false>(a, lds, j, cb, first, tag, wave, lane);
         __syncthreads();
         chain_leave<false>(a, lds, j, cb, tag, wave, lane);
@@ -532,128 +598,166 @@ __global__ __launch_bounds__(256) void k_gated_fwd(GatedArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) dst[v] = h[v];
     }
-    TileRows y;
-    y.init<IO, T>(a, a.y, a.D, p0, kGatedFwdTile, tg, c0);
+    TileRows<IO, kGatedFwdTile, T> y;
+    y.init(a, a.y, a.D, p0, tg, c0);
+    // from here bv is the state after each position
+    if (starts) {
 #pragma unroll
-    for (int k = 0; k < T; ++k) {
-        const bool start = starts && (cut.starts >> k & 1);
+        for (int k = 0; k < T; ++k)
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = start ? bv[k][v] : fmaf(av[k][v], h[v], bv[k][v]);
-        st_tile<IO, V>(y.rsrc, live && pt + k < a.N ? y.vo : kOutside, y.so(a, k, T), h);
-        if (ends && (cut.ends >> k & 1) && a.h_last && live) {
-            const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+            for (int v = 0; v < V; ++v) {
+                const float n = fmaf(av[k][v], h[v], bv[k][v]);
+                bv[k][v] = h[v] = cut.starts >> k & 1 ? bv[k][v] : n;
+            }
+    } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.h_last[slot + v] = h[v];
-        }
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) bv[k][v] = h[v] = fmaf(av[k][v], h[v], bv[k][v]);
     }
+#pragma unroll
+    for (int k = 0; k < T; ++k) st_tile<IO, V>(y.rsrc, y.at(full || pt + k < a.N), y.so + k * y.step, bv[k]);
+    if (a.h_last && live)
+        for (uint32_t m = cut.ends; m; m &= m - 1) {
+            const int k = __builtin_ctz(m);
+            float* dst = a.h_last + seq_row(a, pt + k, ts, c0);
+            at_position(bv, k, h);
+#pragma unroll
+            for (int v = 0; v < V; ++v) dst[v] = h[v];
+        }
+    pass_empty(a, a.h0, a.h_last, j, cb);
 }
 
 // Backward pass: a tile of kGatedBwdTile positions x 64 channels; workgroups take the tiles from the
-// last to the first.
+// last to the first. With e the gradient that comes in behind a position (dh_last behind a sequence's
+// last one), d = dy + e is the state's and a d goes on to the position before.
 template <typename IO, int V, bool kChain>
-__global__ __launch_bounds__(256) void k_gated_bwd(GatedArgs a) {
+__global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedBwdTile / TG;
     __shared__ ChainLds lds;
     __shared__ float2 fwd[4][kGatedBlock];
+    __shared__ __align__(16) float park[2 * T][256 * V];
     const int j = static_cast<int>(blockIdx.x) / a.ncb, cb = static_cast<int>(blockIdx.x) % a.ncb;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    pass_empty(a, a.dh_last, a.dh0, j, cb);
-    if (a.N == 0) return;
+    if (a.N == 0) return pass_empty(a, a.dh_last, a.dh0, j, cb);
     const int tile = a.tiles - 1 - j;
     const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
     const bool live = c0 < a.D;
-    const int p0 = tile * kGatedBwdTile, pt = p0 + tg * T;
+    const int p0 = tile * kGatedBwdTile, pt = p0 + tg * T, p1 = min(p0 + kGatedBwdTile, a.N);
+    const bool full = p0 + kGatedBwdTile <= a.N;
 
+    float k2[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        k2[v] = a.lam[live ? c0 + v : 0];
+        h[v] = a.states_in[static_cast<int64_t>(tile) * a.D + (live ? c0 + v : 0)];
+    }
     Raw<IO, V> xr[T], rr[T], ir[T], gr[T];
     {
-        TileRows x, r, i, g;
-        x.init<IO, T>(a, a.x, a.ld_x, p0, kGatedBwdTile, tg, c0);
-        r.init<IO, T>(a, a.r, a.ld_r, p0, kGatedBwdTile, tg, c0);
-        i.init<IO, T>(a, a.i, a.ld_i, p0, kGatedBwdTile, tg, c0);
-        g.init<IO, T>(a, a.dy, a.ld_dy, p0, kGatedBwdTile, tg, c0);
+        TileRows<IO, kGatedBwdTile, T> x, r, i, g;
+        r.init(a, a.r, a.ld_r, p0, tg, c0);
+        i.init(a, a.i, a.ld_i, p0, tg, c0);
+        x.init(a, a.x, a.ld_x, p0, tg, c0);
+        g.init(a, a.dy, a.ld_dy, p0, tg, c0);
 #pragma unroll
         for (int k = 0; k < T; ++k) {
-            const bool in = live && pt + k < a.N;
-            rr[k] = ld_tile<IO, V>(r.rsrc, in ? r.vo : kOutside, r.so(a, k, T));
-            ir[k] = ld_tile<IO, V>(i.rsrc, in ? i.vo : kOutside, i.so(a, k, T));
-            xr[k] = ld_tile<IO, V>(x.rsrc, in ? x.vo : kOutside, x.so(a, k, T));
-            gr[k] = ld_tile<IO, V>(g.rsrc, in && a.dy ? g.vo : kOutside, g.so(a, k, T));
+            const bool in = full || pt + k < a.N;
+            rr[k] = ld_tile<IO, V>(r.rsrc, r.at(in), r.so + k * r.step);
+            ir[k] = ld_tile<IO, V>(i.rsrc, i.at(in), i.so + k * i.step);
+            xr[k] = ld_tile<IO, V>(x.rsrc, x.at(in), x.so + k * x.step);
+            gr[k] = ld_tile<IO, V>(g.rsrc, g.at(in), g.so + k * g.step);
         }
     }
-    float k2[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) k2[v] = decay_rate(live ? a.lam[c0 + v] : 0.0f, a.c);
-    const int p1 = min(p0 + kGatedBwdTile, a.N);
-    const int qlo = seq_at_wave(a, p0, lane);
-    const int qhi = a.offsets ? seq_at_wave(a, p1 - 1, lane) : 0;
-    const Cuts cut = cuts_of<T>(a, pt, qlo, qhi);
+    for (int v = 0; v < V; ++v) k2[v] = decay_rate(k2[v], a.c);
+    TileSeqs ts;
+    ts.init(a, p0, p1, lane);
+    const Cuts cut = cuts_of<T>(a, pt, ts);
     const bool starts = __any(cut.starts != 0), ends = __any(cut.ends != 0);
 
-    // per element: a; m g (of dx); u a and g x a^2 u / m (of w); the gates' complements
-    float av[T][V], mg[T][V], ua[T][V], gm[T][V], ns[T][V], ng[T][V];
-    Map f[V], e[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = e[v] = identity();
+    // per position: a; m g (of dx); u a and g x a^2 u / m (of w); the state's input. 1 - sigmoid(r) and
+    // 1 - sigmoid(i), wanted at the end only, wait in LDS
+    float av[T][V], mg[T][V], ua[T][V], gm[T][V], bv[T][V];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        float in[V];
+        float ns[V], ng[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const Gates o = gates(rr[k].get(v), ir[k].get(v), k2[v]);
-            const float u = o.q * kLn2;
-            const float um = o.m > 0.0f ? u * fast_rcp(o.m) : 0.0f;
-            const float gx = o.g * xr[k].get(v);
-            av[k][v] = o.a;
-            mg[k][v] = o.m * o.g;
-            ua[k][v] = u * o.a;
-            gm[k][v] = gx * o.a * o.a * um;
-            ns[k][v] = o.ns;
-            ng[k][v] = o.ng;
-            in[v] = o.m * gx;
+            const float q = k2[v] * sigmoid2(rr[k].get(v), &ns[v]);
+            const float gx = sigmoid2(ir[k].get(v), &ng[v]);
+            const float at = fast_exp2(q), m2 = one_minus_sq(q, at), u = q * kLn2;
+            const float im = m2 > 0.0f ? fast_rsq(m2) : 0.0f;  // 1 / m; where m is 0 its terms are taken as 0
+            const float b = m2 * im * gx;
+            av[k][v] = at;
+            mg[k][v] = b;
+            ua[k][v] = u * at;
+            gm[k][v] = gx * xr[k].get(v) * (ua[k][v] * at) * im;
+            bv[k][v] = b * xr[k].get(v);
         }
-        const bool start = starts && (cut.starts >> k & 1);
-        if (start) {
-            if (a.h0) {
-                const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
+        Raw<float, V> w;
+        w.set(ns);
+        w.store(&park[2 * k][tid * V]);
+        w.set(ng);
+        w.store(&park[2 * k + 1][tid * V]);
+    }
+    Map f[V], e[V];
+    if (starts) {
+        // an initial state comes in through the input, and through gm into w (the walk below takes the
+        // state before such a position as 0)
+        if (a.h0 && live)
+            for (uint32_t m = cut.starts; m; m &= m - 1) {
+                const int k = __builtin_ctz(m);
+                const float* h0 = a.h0 + seq_row(a, pt + k, ts, c0);
+                float g[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) g[v] = h0[v];
+#pragma unroll
+                for (int n = 0; n < T; ++n)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (n == k) {
+                            bv[n][v] = fmaf(av[n][v], g[v], bv[n][v]);
+                            gm[n][v] = fmaf(-ua[n][v], g[v], gm[n][v]);
+                        }
+            }
+        thread_map<true>(cut.starts, av, bv, f);
+    } else {
+        thread_map<false>(0, av, bv, f);
+    }
+    // what is added to dy: the gradient of a sequence's last state at its last position
+    float gv[T][V];
+#pragma unroll
+    for (int k = 0; k < T; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) gv[k][v] = gr[k].get(v);
+    if (ends && a.dh_last && live)
+        for (uint32_t m = cut.ends; m; m &= m - 1) {
+            const int k = __builtin_ctz(m);
+            const float* last = a.dh_last + seq_row(a, pt + k, ts, c0);
+            float g[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[v] = last[v];
+#pragma unroll
+            for (int n = 0; n < T; ++n)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (live) in[v] = fmaf(av[k][v], a.h0[slot + v], in[v]);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = {-1.0f, in[v]};
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                f[v].H = fmaf(av[k][v], f[v].H, in[v]);
-                f[v].A = f[v].A < 0.0f ? f[v].A : f[v].A * av[k][v];
-            }
+                    if (n == k) gv[n][v] += g[v];
         }
-    }
-    // gradient of a sequence's last state, added where the sequence ends
-    float last[V];
-    auto end_grad = [&](int k) {
-        const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) last[v] = live && a.dh_last ? a.dh_last[slot + v] : 0.0f;
-    };
+    for (int v = 0; v < V; ++v) e[v] = {av[T - 1][v], av[T - 1][v] * gv[T - 1][v]};
 #pragma unroll
-    for (int k = T - 1; k >= 0; --k) {
-        if (ends && (cut.ends >> k & 1)) {
-            end_grad(k);
+    for (int k = T - 2; k >= 0; --k)
 #pragma unroll
-            for (int v = 0; v < V; ++v) e[v] = {-1.0f, av[k][v] * (gr[k].get(v) + last[v])};
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                e[v].H = av[k][v] * (gr[k].get(v) + e[v].H);
-                e[v].A = e[v].A < 0.0f ? e[v].A : e[v].A * av[k][v];
-            }
+        for (int v = 0; v < V; ++v) {
+            const float in = ends && (cut.ends >> k & 1) ? 0.0f : e[v].H;
+            e[v].H = av[k][v] * (gv[k][v] + in);
+            e[v].A *= av[k][v];
         }
-    }
     Map fb[V], eb[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+        if (ends) e[v].A = cut.ends ? -1.0f : e[v].A;
         Map total;
         scan_rows<CL, false>(f[v], lane, &total, &fb[v]);
         if (lane < CL) fwd[wave][lane * V + v] = make_float2(total.A, total.H);
@@ -672,31 +776,21 @@ __global__ __launch_bounds__(256) void k_gated_bwd(GatedArgs a) {
         }
         chain_gather<true>(a, lds, j, cb, min(max(first, 0), j), tag, wave, lane);
     }
-    // the state before every position, meanwhile
-    {
-        float h[V];
+    // the state before every position, meanwhile: ua becomes w / d
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        for (int w = 0; w < wave; ++w) h[v] = Map{fwd[w][cl * V + v].x, fwd[w][cl * V + v].y}(h[v]);
+        h[v] = fb[v](h[v]);
+    }
+#pragma unroll
+    for (int k = 0; k < T; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            h[v] = live ? a.states_in[static_cast<int64_t>(tile) * a.D + c0 + v] : 0.0f;
-            for (int w = 0; w < wave; ++w) h[v] = Map{fwd[w][cl * V + v].x, fwd[w][cl * V + v].y}(h[v]);
-            h[v] = fb[v](h[v]);
+            if (starts) h[v] = cut.starts >> k & 1 ? 0.0f : h[v];
+            ua[k][v] = fmaf(ua[k][v], h[v], -gm[k][v]);
+            h[v] = fmaf(av[k][v], h[v], bv[k][v]);
         }
-#pragma unroll
-        for (int k = 0; k < T; ++k) {
-            if (starts && (cut.starts >> k & 1)) {
-                const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = live && a.h0 ? a.h0[slot + v] : 0.0f;
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float w = fmaf(ua[k][v], h[v], -gm[k][v]);
-                h[v] = fmaf(av[k][v], h[v], mg[k][v] * xr[k].get(v));
-                ua[k][v] = w;
-            }
-        }
-    }
-    float d[V];
+    float d[V], sum[V];
     if constexpr (kChain) {
         __syncthreads();
         chain_leave<true>(a, lds, j, cb, tag, wave, lane);
@@ -706,52 +800,57 @@ __global__ __launch_bounds__(256) void k_gated_bwd(GatedArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = 0.0f;
     }
-    TileRows dx, dr, di;
-    dx.init<IO, T>(a, a.dx, a.ld_dx, p0, kGatedBwdTile, tg, c0);
-    dr.init<IO, T>(a, a.dr, a.ld_dr, p0, kGatedBwdTile, tg, c0);
-    di.init<IO, T>(a, a.di, a.ld_di, p0, kGatedBwdTile, tg, c0);
-    float sum[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         for (int w = 3; w > wave; --w) d[v] = Map{lds.wave[w][cl * V + v].x, lds.wave[w][cl * V + v].y}(d[v]);
         d[v] = eb[v](d[v]);
         sum[v] = 0.0f;
     }
+    TileRows<IO, kGatedBwdTile, T> dx, dr, di;
+    dx.init(a, a.dx, a.ld_dx, p0, tg, c0);
+    dr.init(a, a.dr, a.ld_dr, p0, tg, c0);
+    di.init(a, a.di, a.ld_di, p0, tg, c0);
 #pragma unroll
     for (int k = T - 1; k >= 0; --k) {
-        if (ends && (cut.ends >> k & 1)) {
-            end_grad(k);
-#pragma unroll
-            for (int v = 0; v < V; ++v) d[v] = last[v];
-        }
         float ox[V], orr[V], oi[V];
-        const bool in = live && pt + k < a.N;
+        const bool in = full || pt + k < a.N;
+        Raw<float, V> ns, ng;
+        ns.load(&park[2 * k][tid * V]);
+        ng.load(&park[2 * k + 1][tid * V]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float del = gr[k].get(v) + d[v];
+            if (ends) d[v] = cut.ends >> k & 1 ? 0.0f : d[v];
+            const float del = gv[k][v] + d[v];
             const float w = del * ua[k][v];
             ox[v] = del * mg[k][v];
-            oi[v] = ox[v] * xr[k].get(v) * ng[k][v];
-            orr[v] = w * ns[k][v];
+            oi[v] = ox[v] * xr[k].get(v) * ng.get(v);
+            orr[v] = w * ns.get(v);
             sum[v] += in ? w : 0.0f;
-            d[v] = av[k][v] * del;
+            bv[k][v] = d[v] = av[k][v] * del;
         }
-        st_tile<IO, V>(dx.rsrc, in ? dx.vo : kOutside, dx.so(a, k, T), ox);
-        st_tile<IO, V>(dr.rsrc, in && a.dr ? dr.vo : kOutside, dr.so(a, k, T), orr);
-        st_tile<IO, V>(di.rsrc, in && a.di ? di.vo : kOutside, di.so(a, k, T), oi);
-        if (starts && (cut.starts >> k & 1) && a.dh0 && live) {
-            const int64_t slot = seq_of(a, seq_at(a, pt + k, qlo, qhi)) * a.D + c0;
-#pragma unroll
-            for (int v = 0; v < V; ++v) a.dh0[slot + v] = d[v];
-        }
+        st_tile<IO, V>(dx.rsrc, dx.at(in), dx.so + k * dx.step, ox);
+        st_tile<IO, V>(dr.rsrc, dr.at(in), dr.so + k * dr.step, orr);
+        st_tile<IO, V>(di.rsrc, di.at(in), di.so + k * di.step, oi);
     }
+    if (starts && a.dh0 && live)
+        for (uint32_t m = cut.starts; m; m &= m - 1) {
+            const int k = __builtin_ctz(m);
+            float* dst = a.dh0 + seq_row(a, pt + k, ts, c0);
+            at_position(bv, k, d);
+#pragma unroll
+            for (int v = 0; v < V; ++v) dst[v] = d[v];
+        }
+    pass_empty(a, a.dh_last, a.dh0, j, cb);
     if (!a.dlam) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+        float p, q;
         if constexpr (CL == 16) {
-            float p, q;
             swap16(sum[v], &p, &q);
-            swap32(p + q, &p, &q);
+            sum[v] = p + q;
+        }
+        if constexpr (CL < 64) {
+            swap32(sum[v], &p, &q);
             sum[v] = p + q;
         }
     }
@@ -826,8 +925,9 @@ __global__ __launch_bounds__(64) void k_gated_step(StepArgs a) {
     const int64_t to = a.slots_out ? a.slots_out[b] : from;
     float h = 0.0f;
     if (from >= 0 && from < a.nslots && to >= 0 && to < a.nslots) {
-        const Gates o = gates(ld<IO>(a.r, b * a.ld_r + d), ld<IO>(a.i, b * a.ld_i + d), decay_rate(a.lam[d], a.c));
-        h = fmaf(o.a, a.state[from * a.D + d], o.m * o.g * ld<IO>(a.x, b * a.ld_x + d));
+        float at, mg;
+        gates(ld<IO>(a.r, b * a.ld_r + d), ld<IO>(a.i, b * a.ld_i + d), decay_rate(a.lam[d], a.c), &at, &mg);
+        h = fmaf(at, a.state[from * a.D + d], mg * ld<IO>(a.x, b * a.ld_x + d));
         a.state[to * a.D + d] = h;
     }
     st<IO>(a.y, b * a.D + d, h);
@@ -848,15 +948,21 @@ GatedArgs common_args(const vimscan_gated* g, const vimscan_launch* l, const Gat
     a.c = g->c;
     a.N = static_cast<int32_t>(p.tokens);
     a.Lp = static_cast<int32_t>(p.Lp);
+    if (p.Lp > 0) {
+        // exact for positions below 2^31: lp_mul = floor(2^(31 + s) / Lp) + 1 with 2^(s - 1) < Lp <= 2^s
+        int s = 0;
+        while ((int64_t(1) << s) < p.Lp) ++s;
+        a.lp_mul = static_cast<uint32_t>((uint64_t(1) << (31 + s)) / static_cast<uint64_t>(p.Lp) + 1);
+        a.lp_shift = static_cast<uint32_t>(31 + s);
+    }
     a.D = static_cast<int32_t>(l->d_inner);
     a.nseq = static_cast<int32_t>(p.nseq);
     a.ncb = static_cast<int32_t>(p.ncb);
     a.tiles = static_cast<int32_t>(p.tiles);
     char* ws = static_cast<char*>(l->workspace);
     if (p.chain) {
-        a.agg = reinterpret_cast<float2*>(ws);
-        a.inc = reinterpret_cast<float*>(ws + p.off_inc);
-        a.tags = reinterpret_cast<uint64_t*>(ws + p.off_tags);
+        a.agg = reinterpret_cast<uint64_t*>(ws);
+        a.inc = reinterpret_cast<uint64_t*>(ws + p.off_inc);
     }
     a.part = p.ws > p.off_part ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
     a.rev = (l->flags & VIMSCAN_FLAG_REVERSE) ? 1 : 0;
@@ -869,12 +975,15 @@ bool record(const vimscan_launch* l, int k) {
     return hipEventRecord(static_cast<hipEvent_t>(l->scan_events[k]), static_cast<hipStream_t>(l->stream)) == hipSuccess;
 }
 
-// Four channels per lane where every row of every tensor is aligned to four elements.
-bool by_four(const vimscan_gated* g, int64_t d, size_t e, const void* const* more, const int64_t* lds, int n) {
+// VEC channels per lane where every row of every tensor is aligned to them.
+#ifndef VEC
+#define VEC 2
+#endif
+bool by_vec(const vimscan_gated* g, int64_t d, size_t e, const void* const* more, const int64_t* lds, int n) {
     auto ok = [&](const void* p, int64_t ld) {
-        return !p || (reinterpret_cast<uintptr_t>(p) % (4 * e) == 0 && ld % 4 == 0);
+        return !p || (reinterpret_cast<uintptr_t>(p) % (VEC * e) == 0 && ld % VEC == 0);
     };
-    bool r = d % 4 == 0 && ok(g->x, g->ld_x) && ok(g->r, g->ld_r) && ok(g->i, g->ld_i);
+    bool r = d % VEC == 0 && ok(g->x, g->ld_x) && ok(g->r, g->ld_r) && ok(g->i, g->ld_i);
     for (int k = 0; k < n; ++k) r = r && ok(more[k], lds[k]);
     return r;
 }
@@ -927,9 +1036,9 @@ int vimscan_gated_fwd(const vimscan_gated* g, int64_t seg_len, void* y, float* h
     const void* out[] = {y};
     const int64_t out_ld[] = {launch->d_inner};
     const bool f32 = launch->io_dtype == VIMSCAN_F32;
-    if (by_four(g, launch->d_inner, f32 ? 4 : 2, out, out_ld, 1)) {
-        if (f32) launch_fwd<float, 4>(a, p, s);
-        else launch_fwd<Bf16, 4>(a, p, s);
+    if (by_vec(g, launch->d_inner, f32 ? 4 : 2, out, out_ld, 1)) {
+        if (f32) launch_fwd<float, VEC>(a, p, s);
+        else launch_fwd<Bf16, VEC>(a, p, s);
     } else {
         if (f32) launch_fwd<float, 1>(a, p, s);
         else launch_fwd<Bf16, 1>(a, p, s);
@@ -966,9 +1075,9 @@ int vimscan_gated_bwd(const vimscan_gated* g, int64_t seg_len, const vimscan_gat
         const void* more[] = {grad->dy, grad->dx, grad->dr, grad->di};
         const int64_t lds[] = {grad->ld_dy, grad->ld_dx, grad->ld_dr, grad->ld_di};
         const bool f32 = launch->io_dtype == VIMSCAN_F32;
-        if (by_four(g, launch->d_inner, f32 ? 4 : 2, more, lds, 4)) {
-            if (f32) launch_bwd<float, 4>(a, p, s);
-            else launch_bwd<Bf16, 4>(a, p, s);
+        if (by_vec(g, launch->d_inner, f32 ? 4 : 2, more, lds, 4)) {
+            if (f32) launch_bwd<float, VEC>(a, p, s);
+            else launch_bwd<Bf16, VEC>(a, p, s);
         } else {
             if (f32) launch_bwd<float, 1>(a, p, s);
             else launch_bwd<Bf16, 1>(a, p, s);
