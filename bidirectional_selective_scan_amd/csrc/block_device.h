@@ -24,12 +24,14 @@ __device__ __forceinline__ float fast_rcp(float v) { return __builtin_amdgcn_rcp
 __device__ __forceinline__ float fast_sqrt(float v) { return __builtin_amdgcn_sqrtf(v); }
 __device__ __forceinline__ float fast_rsq(float v) { return __builtin_amdgcn_rsqf(v); }
 
-// bf16 from fp32, to nearest even (the hardware conversion).
+// bf16 from fp32, to nearest even (the hardware conversion, two at a time).
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
+using F32x2 = float __attribute__((ext_vector_type(2)));
+using Bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    return static_cast<uint32_t>(bf16_bits(lo)) | (static_cast<uint32_t>(bf16_bits(hi)) << 16);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((F32x2{lo, hi}), Bf16x2));
 }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

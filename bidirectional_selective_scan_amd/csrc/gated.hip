@@ -13,9 +13,9 @@
 // written once at any shape: one long sequence fills the chip as well as many short ones.
 //  * Layout: V consecutive channels per lane (8 or 16 bytes), 64 / V lanes over the channels (rows of
 //    128 or 256 bytes), the other lanes and waves over the positions.
-//  * A map whose positions contain a sequence start does not depend on the entering state: it is
-//    marked by A < 0 (a is never negative) and composed with selects, not with a factor 0, so that NaN
-//    or infinity in one sequence never reaches the next.
+//  * A map whose positions contain a sequence start does not depend on the entering state: A = 0, and
+//    maps are applied and composed with the multiplication that gives 0 for a factor 0 whatever the
+//    other one is, so that NaN or infinity in one sequence never reaches the next.
 //  * Between tiles: a tile publishes its map before it waits for anything, then composes the maps of
 //    the tiles before it in its group of kGatedGroup onto the state that the group before left, always
 //    in this order (the same bits on every run); a group's last tile publishes the state it leaves.
@@ -75,8 +75,8 @@ struct GatedArgs {
     float* dlam;
     float* dh0;
     // workspace
-    uint64_t* agg;           // [tile][width][2] maps handed over, width = 64 ncb
-    uint64_t* inc;           // [group][width][2] the state a group leaves
+    uint64_t* agg;           // [tile][2][width] maps handed over, width = 64 ncb
+    uint64_t* inc;           // [group][2][width] the state a group leaves
     float* part;             // [tile][width] partial sums of dlam
 };
 
@@ -124,50 +124,33 @@ __device__ __forceinline__ int seq_at_wave(const GatedArgs& a, int p, int lane) 
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// The sequences around a tile of positions p0 .. p1 - 1 (the same for every lane).
-struct TileSeqs {
-    int lo, hi;    // the sequences that hold the first and the last position
-    int start;     // first position of sequence lo
-    bool any;      // a sequence starts at p0, or ends inside the tile
-    __device__ __forceinline__ void init(const GatedArgs& a, int p0, int p1, int lane) {
-        lo = seq_at_wave(a, p0, lane);
-        start = bound_of(a, lo);
-        any = start == p0 || bound_of(a, lo + 1) <= p1;
-        hi = a.offsets && any ? seq_at_wave(a, p1 - 1, lane) : lo;
+// The sequence boundaries among a wave's P positions (P <= 64): every wave finds its own, one position a
+// lane, so that no barrier is needed.
+struct WaveSeqs {
+    uint64_t starts, ends;   // bit per position: the first, the last one of its sequence
+    // row: the wave's place in LDS for the caller's sequence of each position, written only where there is
+    // a boundary; lo: the sequence of the tile's first position. No bit is set past the stream's end; its
+    // last position counts as an end whatever the offsets hold: the stores behind it hang on that.
+    template <int P>
+    __device__ __forceinline__ void find(const GatedArgs& a, int pw, int lo, int lane, int* row) {
+        starts = ends = 0;
+        const int pe = min(pw + P, a.N);
+        if (pw >= a.N || (bound_of(a, lo) != pw && bound_of(a, lo + 1) > pe)) return;
+        const int hi = a.offsets ? seq_at_wave(a, pe - 1, lane) : 0;
+        const int p = pw + lane;
+        const bool in = p < pe;
+        const int q = in ? seq_at(a, p, lo, hi) : lo;
+        if (lane < P) row[lane] = static_cast<int>(seq_of(a, q));
+        starts = __ballot(in && bound_of(a, q) == p);
+        ends = __ballot(in && (bound_of(a, q + 1) == p + 1 || p + 1 == a.N));
+        asm volatile("" ::: "memory");  // the rows are read by this wave only, after they are written
+    }
+    // The bits of T positions from at on.
+    template <int T>
+    __device__ __forceinline__ static uint32_t bits(uint64_t m, int at) {
+        return static_cast<uint32_t>(m >> at) & static_cast<uint32_t>((uint64_t(1) << T) - 1);
     }
 };
-
-// The sequence boundaries among a thread's positions p .. p + T - 1 of the stream: bit k of starts
-// (ends) is set where position p + k is the first (last) of its sequence. No bit is set for a position
-// past the stream's end.
-struct Cuts {
-    uint32_t starts, ends;
-};
-template <int T>
-__device__ __forceinline__ Cuts cuts_of(const GatedArgs& a, int p, const TileSeqs& ts) {
-    uint64_t m = 0;  // bit k: p + k is a boundary, the stream's end included
-    const int n = min(T, a.N - p);
-    if (!ts.any || n <= 0) return {0, 0};
-    if (!a.offsets) {
-        const int rem = p - uniform_seq(a, p) * a.Lp;
-        for (int64_t o = rem ? a.Lp - rem : 0; o <= n; o += a.Lp) m |= uint64_t(1) << o;
-    } else {
-        int q = seq_at(a, p, ts.lo, ts.hi);
-        if (bound_of(a, q) == p) m = 1;
-        while (q < a.nseq) {
-            const int o = bound_of(a, q + 1) - p;
-            if (o > n || o <= 0) break;
-            m |= uint64_t(1) << o;
-            if (o == n) break;
-            const int next = seq_at(a, p + o, q + 1, ts.hi);
-            if (next <= q) break;
-            q = next;
-        }
-        if (p + n == a.N) m |= uint64_t(1) << n;
-    }
-    const uint64_t in = (uint64_t(1) << n) - 1;
-    return {static_cast<uint32_t>(m & in), static_cast<uint32_t>((m >> 1) & in)};
-}
 
 // -c softplus(lam) log2(e), so that a = 2^(k2 sigmoid(r)). softplus in log2 units is
 // max(w, 0) + log2(1 + p), w = lam log2(e), p = 2^-|w|; log2(1 + p) as log2(v) plus the first-order
@@ -186,7 +169,10 @@ __device__ __forceinline__ float one_minus_sq(float q, float a) {
     constexpr double z = -2.0 * 0.693147180559945309417;
     constexpr float c1 = float(z), c2 = float(-z * z / 2), c3 = float(z * z * z / 6), c4 = float(-z * z * z * z / 24),
                     c5 = float(z * z * z * z * z / 120), c6 = float(-z * z * z * z * z * z / 720);
-    float s = fmaf(q, c6, c5);
+    // (two literals do not fit one instruction: one coefficient is kept in a register)
+    float first = c5;
+    asm("" : "+v"(first));
+    float s = fmaf(q, c6, first);
     s = fmaf(q, s, c4);
     s = fmaf(q, s, c3);
     s = fmaf(q, s, c2);
@@ -283,16 +269,17 @@ __device__ __forceinline__ void st_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, u
     }
 }
 
-// The map h -> A h + H of some consecutive positions; A < 0: h -> H whatever h is.
+// The product in which a factor 0 gives 0 whatever the other one is.
+extern "C" __device__ float vimscan_mul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
+
+// The map h -> A h + H of some consecutive positions; A = 0 where a sequence starts among them.
 struct Map {
     float A, H;
-    __device__ __forceinline__ float operator()(float h) const { return A < 0.0f ? H : fmaf(A, h, H); }
+    __device__ __forceinline__ float operator()(float h) const { return vimscan_mul_legacy(A, h) + H; }
 };
 __device__ __forceinline__ Map identity() { return {1.0f, 0.0f}; }
 // f, then g.
-__device__ __forceinline__ Map then(const Map& f, const Map& g) {
-    return {g.A < 0.0f || f.A < 0.0f ? -1.0f : f.A * g.A, g(f.H)};
-}
+__device__ __forceinline__ Map then(const Map& f, const Map& g) { return {vimscan_mul_legacy(f.A, g.A), g(f.H)}; }
 __device__ __forceinline__ Map pick(bool c, const Map& f, const Map& g) { return {c ? f.A : g.A, c ? f.H : g.H}; }
 
 // Every lane's pair: the values of the even and the odd row of 16 lanes, or of the lower and the
@@ -353,23 +340,33 @@ struct ChainLds {
     float inc[kGatedBlock];        // the state that the group before left
 };
 
-// A value handed over: two 64-bit words, the value and the value xor the dispatch's tag, each stored and
+// A value handed over: two 64-bit words (second words apart, so that a wave's are contiguous), the value and the value xor the dispatch's tag, each stored and
 // loaded on its own (device-coherent, no order between them). A reader takes the value when the two
 // differ by exactly this dispatch's tag, so words of earlier dispatches, arbitrary bytes and half a
 // value never pass, the memory needs no clearing, and neither side waits for one access before the
 // next: a value costs its reader one trip to memory after it was stored.
-__device__ __forceinline__ void hand_over(uint64_t* w, uint64_t tag, float x, float y) {
+// w: the wave's first word (the same for all lanes).
+__device__ __forceinline__ void hand_over(uint64_t* w, int64_t second, int lane, uint64_t tag, float x, float y) {
     const uint64_t v = __float_as_uint(x) | (static_cast<uint64_t>(__float_as_uint(y)) << 32);
-    __hip_atomic_store(w, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(w + 1, v ^ tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(w + lane, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(w + second + lane, v ^ tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 struct Handed {
     uint64_t v, c;
-    __device__ __forceinline__ void load(const uint64_t* w) {
-        v = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        c = __hip_atomic_load(w + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __device__ __forceinline__ void load(const uint64_t* w, int64_t second, int lane) {
+        v = __hip_atomic_load(w + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        c = __hip_atomic_load(w + second + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __device__ __forceinline__ bool there(uint64_t tag) const { return (v ^ c) == tag; }
+    // Loads until every lane's value is there.
+    __device__ __forceinline__ void wait(const uint64_t* w, int64_t second, int lane, uint64_t tag) {
+        for (int it = 0; it < kSpinLimit; ++it) {
+            load(w, second, lane);
+            if (__all(there(tag))) return;
+            __builtin_amdgcn_s_sleep(1);
+        }
+        if (lane == 0) __hip_atomic_fetch_add(&g_wait_timeouts, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     __device__ __forceinline__ float x() const { return __uint_as_float(static_cast<uint32_t>(v)); }
     __device__ __forceinline__ float y() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 };
@@ -394,39 +391,35 @@ __device__ __forceinline__ void chain_gather(const GatedArgs& a, ChainLds& l, in
                                              int wave, int lane) {
     constexpr int kEach = kGatedGroup / 4;
     const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
-    const int ch = cb * kGatedBlock + lane;
+    const int64_t at = cb * kGatedBlock;
     if (wave == 3 && j + 1 < a.tiles) {
         const Map f = tile_map<kBack>(l, lane);
-        hand_over(a.agg + 2 * (j * width + ch), tag, f.A, f.H);
+        hand_over(a.agg + 2 * j * width + at, width, lane, tag, f.A, f.H);
     }
     const int group = j / kGatedGroup, g0 = group * kGatedGroup;
     const bool from_group = first < g0;
     const int lo = (from_group ? g0 : first) + wave * kEach;   // this wave's tiles: lo .. lo + n - 1
     const int n = min(j - lo, kEach);
     const bool inc = from_group && wave == 0;
-    Handed v[kEach], vi;
-    int todo = 0;  // bit k: tile lo + k is still awaited; bit kEach: the group's state
-    if (n > 0) todo = (1 << n) - 1;
-    if (inc) todo |= 1 << kEach;
-    for (int it = 0; todo && it < kSpinLimit; ++it) {
-        if (it > 0) __builtin_amdgcn_s_sleep(1);
-#pragma unroll
-        for (int k = 0; k < kEach; ++k)
-            if (todo >> k & 1) v[k].load(a.agg + 2 * ((lo + k) * width + ch));
-        if (todo >> kEach) vi.load(a.inc + 2 * ((group - 1) * width + ch));
-#pragma unroll
-        for (int k = 0; k < kEach; ++k)
-            if ((todo >> k & 1) && __all(v[k].there(tag))) todo &= ~(1 << k);
-        if ((todo >> kEach) && __all(vi.there(tag))) todo &= ~(1 << kEach);
-    }
-    if (todo && lane == 0)
-        __hip_atomic_fetch_add(&g_wait_timeouts, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    Handed v[kEach];
     Map f = identity();
+    // all loads first; then every value is waited for in turn
 #pragma unroll
     for (int k = 0; k < kEach; ++k)
-        if (k < n) f = then(f, Map{v[k].x(), v[k].y()});
+        if (k < n) v[k].load(a.agg + 2 * (lo + k) * width + at, width, lane);
+    if (wave == 0) {
+        Handed h;
+        h.v = 0;
+        if (inc) h.wait(a.inc + 2 * (group - 1) * width + at, width, lane, tag);
+        l.inc[lane] = h.x();
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        if (k < n) {
+            if (!__all(v[k].there(tag))) v[k].wait(a.agg + 2 * (lo + k) * width + at, width, lane, tag);
+            f = then(f, Map{v[k].x(), v[k].y()});
+        }
     l.part[wave][lane] = make_float2(f.A, f.H);
-    if (wave == 0) l.inc[lane] = inc ? vi.x() : 0.0f;
 }
 // What enters the tile in channel ch of the block (0 when nothing does).
 __device__ __forceinline__ float chain_carry(const ChainLds& l, int ch) {
@@ -442,7 +435,7 @@ __device__ __forceinline__ void chain_leave(const GatedArgs& a, const ChainLds& 
     if (wave != 0 || j + 1 >= a.tiles || j % kGatedGroup != kGatedGroup - 1) return;
     const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
     const float h = tile_map<kBack>(l, lane)(chain_carry(l, lane));
-    hand_over(a.inc + 2 * (j / kGatedGroup * width + cb * kGatedBlock + lane), tag, h, 0.0f);
+    hand_over(a.inc + 2 * (j / kGatedGroup) * width + cb * kGatedBlock, width, lane, tag, h, 0.0f);
 }
 
 // Sequences without tokens: what comes out is what went in (0 without it). Shared out over the tiles.
@@ -458,75 +451,56 @@ __device__ __forceinline__ void pass_empty(const GatedArgs& a, const float* in, 
     }
 }
 
-// v[k] of the thread's positions for a k that differs between lanes.
+// Pins values: they are computed before this point, not where they are used (which would keep what they
+// are computed from in registers).
 template <int T, int V>
-__device__ __forceinline__ void at_position(const float (&v)[T][V], int k, float (&o)[V]) {
+__device__ __forceinline__ void pin_all(float (&a)[T][V]) {
 #pragma unroll
-    for (int n = 0; n < T; ++n)
+    for (int k = 0; k < T; ++k)
 #pragma unroll
-        for (int c = 0; c < V; ++c) o[c] = n == 0 || n == k ? v[n][c] : o[c];
+        for (int v = 0; v < V; ++v) asm volatile("" : "+v"(a[k][v]));
 }
 
-// The caller's row of the sequence that holds position p, first of the thread's channels.
-__device__ __forceinline__ int64_t seq_row(const GatedArgs& a, int p, const TileSeqs& ts, int c0) {
-    return seq_of(a, seq_at(a, p, ts.lo, ts.hi)) * a.D + c0;
-}
-
-// A sequence that starts among the thread's positions brings its initial state in: added to that
-// position's input.
-template <int T, int V>
-__device__ __forceinline__ void add_h0(const GatedArgs& a, uint32_t starts, int pt, const TileSeqs& ts, int c0,
-                                       const float (&av)[T][V], float (&bv)[T][V]) {
-    if (!a.h0 || c0 >= a.D) return;
-    for (; starts; starts &= starts - 1) {
-        const int k = __builtin_ctz(starts);
-        const float* h0 = a.h0 + seq_row(a, pt + k, ts, c0);
-        float h[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = h0[v];
-#pragma unroll
-        for (int n = 0; n < T; ++n)
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (n == k) bv[n][v] = fmaf(av[n][v], h[v], bv[n][v]);
+// Makes the compiler take loaded values as new ones, so that what was computed from them before is not
+// kept in registers for a later use.
+template <int V>
+__device__ __forceinline__ void forget(Raw<Bf16, V>& r) {
+    if constexpr (V == 1) {
+        uint32_t w = r.w;
+        asm volatile("" : "+v"(w));
+        r.w = static_cast<uint16_t>(w);
+    } else if constexpr (V == 2) {
+        asm volatile("" : "+v"(r.w));
+    } else {
+        asm volatile("" : "+v"(r.w.x), "+v"(r.w.y));
     }
 }
+template <int V>
+__device__ __forceinline__ void forget(Raw<float, V>&) {}
 
-// The map of the thread's positions, from the first to the last. kCut: some lane of the wave has a
-// sequence start among them.
-template <bool kCut, int T, int V>
-__device__ __forceinline__ void thread_map(uint32_t starts, const float (&av)[T][V], const float (&bv)[T][V], Map (&f)[V]) {
+// The initial state of the sequence that starts at a position (row: the caller's sequence), for the
+// thread's channels from c0 on.
+template <int V>
+__device__ __forceinline__ void seq_value(const GatedArgs& a, const float* from, int row, int c0, float (&h)[V]) {
+    const float* p = from + static_cast<int64_t>(row) * a.D + c0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = {av[0][v], bv[0][v]};
-#pragma unroll
-    for (int k = 1; k < T; ++k) {
-        const bool start = kCut && (starts >> k & 1);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float h = fmaf(av[k][v], f[v].H, bv[k][v]);
-            f[v].H = start ? bv[k][v] : h;
-            f[v].A *= av[k][v];
-        }
-    }
-    if constexpr (kCut) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) f[v].A = starts ? -1.0f : f[v].A;
-    }
+    for (int v = 0; v < V; ++v) h[v] = from && c0 < a.D ? p[v] : 0.0f;
 }
 
 // Forward pass: a tile of kGatedFwdTile positions x 64 channels.
 template <typename IO, int V, bool kChain>
-__global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 ? 4 : 3) void k_gated_fwd(GatedArgs a) {
+__global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_fwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedFwdTile / TG;
     __shared__ ChainLds lds;
+    constexpr int P = T * 64 / CL;  // positions of a wave
+    __shared__ int rows[4][P];
     const int j = static_cast<int>(blockIdx.x) / a.ncb, cb = static_cast<int>(blockIdx.x) % a.ncb;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (a.N == 0) return pass_empty(a, a.h0, a.h_last, j, cb);
     const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
     const bool live = c0 < a.D;
-    const int p0 = j * kGatedFwdTile, pt = p0 + tg * T, p1 = min(p0 + kGatedFwdTile, a.N);
-    const bool full = p0 + kGatedFwdTile <= a.N;
+    const int p0 = j * kGatedFwdTile, pt = p0 + tg * T;
 
     float k2[V];
 #pragma unroll
@@ -537,20 +511,29 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 ? 4 : 3) void k_gated_
         r.init(a, a.r, a.ld_r, p0, tg, c0);
         i.init(a, a.i, a.ld_i, p0, tg, c0);
         x.init(a, a.x, a.ld_x, p0, tg, c0);
+        if (p0 + kGatedFwdTile <= a.N) {
 #pragma unroll
-        for (int k = 0; k < T; ++k) {
-            const bool in = full || pt + k < a.N;
-            rr[k] = ld_tile<IO, V>(r.rsrc, r.at(in), r.so + k * r.step);
-            ir[k] = ld_tile<IO, V>(i.rsrc, i.at(in), i.so + k * i.step);
-            xr[k] = ld_tile<IO, V>(x.rsrc, x.at(in), x.so + k * x.step);
+            for (int k = 0; k < T; ++k) {
+                rr[k] = ld_tile<IO, V>(r.rsrc, r.vo, r.so + k * r.step);
+                ir[k] = ld_tile<IO, V>(i.rsrc, i.vo, i.so + k * i.step);
+                xr[k] = ld_tile<IO, V>(x.rsrc, x.vo, x.so + k * x.step);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                rr[k] = ld_tile<IO, V>(r.rsrc, r.at(pt + k < a.N), r.so + k * r.step);
+                ir[k] = ld_tile<IO, V>(i.rsrc, i.at(pt + k < a.N), i.so + k * i.step);
+                xr[k] = ld_tile<IO, V>(x.rsrc, x.at(pt + k < a.N), x.so + k * x.step);
+            }
         }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) k2[v] = decay_rate(k2[v], a.c);
-    TileSeqs ts;
-    ts.init(a, p0, p1, lane);
-    const Cuts cut = cuts_of<T>(a, pt, ts);
-    const bool starts = __any(cut.starts != 0);
+    const int q0 = seq_at_wave(a, p0, lane), wt = lane / CL * T;  // wt: the thread's first position in its wave
+    WaveSeqs ws;
+    ws.find<P>(a, p0 + wave * P, q0, lane, rows[wave]);
+    const uint32_t starts = WaveSeqs::bits<T>(ws.starts, wt), ends = WaveSeqs::bits<T>(ws.ends, wt);
+    const bool cuts = (ws.starts | ws.ends) != 0;
 
     float av[T][V], bv[T][V];
     Map f[V], before[V];
@@ -562,23 +545,42 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 ? 4 : 3) void k_gated_
             gates(rr[k].get(v), ir[k].get(v), k2[v], &av[k][v], &mg);
             bv[k][v] = mg * xr[k].get(v);
         }
-    if (starts) {
-        add_h0(a, cut.starts, pt, ts, c0, av, bv);
-        thread_map<true>(cut.starts, av, bv, f);
+    pin_all(av);
+    pin_all(bv);
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        h[v] = 0.0f;
+        f[v].A = av[0][v];
+    }
+    if (!cuts) {
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = fmaf(av[k][v], h[v], bv[k][v]);
     } else {
-        thread_map<false>(0, av, bv, f);
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            if (starts >> k & 1) seq_value(a, a.h0, rows[wave][wt + k], c0, h);
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = fmaf(av[k][v], h[v], bv[k][v]);
+        }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int k = 1; k < T; ++k) f[v].A *= av[k][v];
+        f[v].H = h[v];
+        f[v].A = starts ? 0.0f : f[v].A;
         Map total;
         scan_rows<CL, false>(f[v], lane, &total, &before[v]);
         if (lane < CL) lds.wave[wave][lane * V + v] = make_float2(total.A, total.H);
     }
     __syncthreads();
-    float h[V];
     if constexpr (kChain) {
         const uint64_t tag = dispatch_tag();
-        const int first = ts.start >= p0 ? j : ts.start / kGatedFwdTile;
+        const int start = bound_of(a, q0);
+        const int first = start >= p0 ? j : start / kGatedFwdTile;
         chain_gather<false>(a, lds, j, cb, first, tag, wave, lane);
         __syncthreads();
         chain_leave<false>(a, lds, j, cb, tag, wave, lane);
@@ -600,31 +602,28 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 ? 4 : 3) void k_gated_
     }
     TileRows<IO, kGatedFwdTile, T> y;
     y.init(a, a.y, a.D, p0, tg, c0);
-    // from here bv is the state after each position
-    if (starts) {
+    if (!cuts) {
+        // (also a wave past the stream's end comes here, without a boundary: its stores are dropped)
 #pragma unroll
-        for (int k = 0; k < T; ++k)
+        for (int k = 0; k < T; ++k) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float n = fmaf(av[k][v], h[v], bv[k][v]);
-                bv[k][v] = h[v] = cut.starts >> k & 1 ? bv[k][v] : n;
-            }
+            for (int v = 0; v < V; ++v) h[v] = fmaf(av[k][v], h[v], bv[k][v]);
+            st_tile<IO, V>(y.rsrc, y.at(pt < a.N), y.so + k * y.step, h);
+        }
     } else {
 #pragma unroll
-        for (int k = 0; k < T; ++k)
+        for (int k = 0; k < T; ++k) {
+            if (starts >> k & 1) seq_value(a, a.h0, rows[wave][wt + k], c0, h);
 #pragma unroll
-            for (int v = 0; v < V; ++v) bv[k][v] = h[v] = fmaf(av[k][v], h[v], bv[k][v]);
-    }
+            for (int v = 0; v < V; ++v) h[v] = fmaf(av[k][v], h[v], bv[k][v]);
+            st_tile<IO, V>(y.rsrc, y.at(pt + k < a.N), y.so + k * y.step, h);
+            if (a.h_last && live && (ends >> k & 1)) {
+                float* dst = a.h_last + static_cast<int64_t>(rows[wave][wt + k]) * a.D + c0;
 #pragma unroll
-    for (int k = 0; k < T; ++k) st_tile<IO, V>(y.rsrc, y.at(full || pt + k < a.N), y.so + k * y.step, bv[k]);
-    if (a.h_last && live)
-        for (uint32_t m = cut.ends; m; m &= m - 1) {
-            const int k = __builtin_ctz(m);
-            float* dst = a.h_last + seq_row(a, pt + k, ts, c0);
-            at_position(bv, k, h);
-#pragma unroll
-            for (int v = 0; v < V; ++v) dst[v] = h[v];
+                for (int v = 0; v < V; ++v) dst[v] = h[v];
+            }
         }
+    }
     pass_empty(a, a.h0, a.h_last, j, cb);
 }
 
@@ -632,9 +631,11 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 ? 4 : 3) void k_gated_
 // last to the first. With e the gradient that comes in behind a position (dh_last behind a sequence's
 // last one), d = dy + e is the state's and a d goes on to the position before.
 template <typename IO, int V, bool kChain>
-__global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
+__global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_bwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedBwdTile / TG;
     __shared__ ChainLds lds;
+    constexpr int P = T * 64 / CL;  // positions of a wave
+    __shared__ int rows[4][P];
     __shared__ float2 fwd[4][kGatedBlock];
     __shared__ __align__(16) float park[2 * T][256 * V];
     const int j = static_cast<int>(blockIdx.x) / a.ncb, cb = static_cast<int>(blockIdx.x) % a.ncb;
@@ -644,8 +645,7 @@ __global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
     const int tile = a.tiles - 1 - j;
     const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
     const bool live = c0 < a.D;
-    const int p0 = tile * kGatedBwdTile, pt = p0 + tg * T, p1 = min(p0 + kGatedBwdTile, a.N);
-    const bool full = p0 + kGatedBwdTile <= a.N;
+    const int p0 = tile * kGatedBwdTile, pt = p0 + tg * T;
 
     float k2[V], h[V];
 #pragma unroll
@@ -660,25 +660,35 @@ __global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
         i.init(a, a.i, a.ld_i, p0, tg, c0);
         x.init(a, a.x, a.ld_x, p0, tg, c0);
         g.init(a, a.dy, a.ld_dy, p0, tg, c0);
+        if (p0 + kGatedBwdTile <= a.N) {
 #pragma unroll
-        for (int k = 0; k < T; ++k) {
-            const bool in = full || pt + k < a.N;
-            rr[k] = ld_tile<IO, V>(r.rsrc, r.at(in), r.so + k * r.step);
-            ir[k] = ld_tile<IO, V>(i.rsrc, i.at(in), i.so + k * i.step);
-            xr[k] = ld_tile<IO, V>(x.rsrc, x.at(in), x.so + k * x.step);
-            gr[k] = ld_tile<IO, V>(g.rsrc, g.at(in), g.so + k * g.step);
+            for (int k = 0; k < T; ++k) {
+                rr[k] = ld_tile<IO, V>(r.rsrc, r.vo, r.so + k * r.step);
+                ir[k] = ld_tile<IO, V>(i.rsrc, i.vo, i.so + k * i.step);
+                xr[k] = ld_tile<IO, V>(x.rsrc, x.vo, x.so + k * x.step);
+                gr[k] = ld_tile<IO, V>(g.rsrc, g.vo, g.so + k * g.step);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                rr[k] = ld_tile<IO, V>(r.rsrc, r.at(pt + k < a.N), r.so + k * r.step);
+                ir[k] = ld_tile<IO, V>(i.rsrc, i.at(pt + k < a.N), i.so + k * i.step);
+                xr[k] = ld_tile<IO, V>(x.rsrc, x.at(pt + k < a.N), x.so + k * x.step);
+                gr[k] = ld_tile<IO, V>(g.rsrc, g.at(pt + k < a.N), g.so + k * g.step);
+            }
         }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) k2[v] = decay_rate(k2[v], a.c);
-    TileSeqs ts;
-    ts.init(a, p0, p1, lane);
-    const Cuts cut = cuts_of<T>(a, pt, ts);
-    const bool starts = __any(cut.starts != 0), ends = __any(cut.ends != 0);
+    const int q0 = seq_at_wave(a, p0, lane), wt = lane / CL * T;  // wt: the thread's first position in its wave
+    WaveSeqs ws;
+    ws.find<P>(a, p0 + wave * P, q0, lane, rows[wave]);
+    const uint32_t starts = WaveSeqs::bits<T>(ws.starts, wt), ends = WaveSeqs::bits<T>(ws.ends, wt);
+    const bool cuts = (ws.starts | ws.ends) != 0;
 
-    // per position: a; m g (of dx); u a and g x a^2 u / m (of w); the state's input. 1 - sigmoid(r) and
-    // 1 - sigmoid(i), wanted at the end only, wait in LDS
-    float av[T][V], mg[T][V], ua[T][V], gm[T][V], bv[T][V];
+    // per position: a; m g (of dx and the state's input); u a and g x a^2 u / m (of w). 1 - sigmoid(r)
+    // and 1 - sigmoid(i), wanted at the end only, wait in LDS
+    float av[T][V], mg[T][V], ua[T][V], gm[T][V];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
         float ns[V], ng[V];
@@ -688,12 +698,10 @@ __global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
             const float gx = sigmoid2(ir[k].get(v), &ng[v]);
             const float at = fast_exp2(q), m2 = one_minus_sq(q, at), u = q * kLn2;
             const float im = m2 > 0.0f ? fast_rsq(m2) : 0.0f;  // 1 / m; where m is 0 its terms are taken as 0
-            const float b = m2 * im * gx;
             av[k][v] = at;
-            mg[k][v] = b;
+            mg[k][v] = m2 * im * gx;
             ua[k][v] = u * at;
             gm[k][v] = gx * xr[k].get(v) * (ua[k][v] * at) * im;
-            bv[k][v] = b * xr[k].get(v);
         }
         Raw<float, V> w;
         w.set(ns);
@@ -701,63 +709,56 @@ __global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
         w.set(ng);
         w.store(&park[2 * k + 1][tid * V]);
     }
+    pin_all(av);
+    pin_all(mg);
+    pin_all(ua);
+    pin_all(gm);
     Map f[V], e[V];
-    if (starts) {
-        // an initial state comes in through the input, and through gm into w (the walk below takes the
-        // state before such a position as 0)
-        if (a.h0 && live)
-            for (uint32_t m = cut.starts; m; m &= m - 1) {
-                const int k = __builtin_ctz(m);
-                const float* h0 = a.h0 + seq_row(a, pt + k, ts, c0);
-                float g[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) g[v] = h0[v];
+    for (int v = 0; v < V; ++v) f[v].H = e[v].H = 0.0f;
+    if (!cuts) {
 #pragma unroll
-                for (int n = 0; n < T; ++n)
+        for (int k = 0; k < T; ++k)
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (n == k) {
-                            bv[n][v] = fmaf(av[n][v], g[v], bv[n][v]);
-                            gm[n][v] = fmaf(-ua[n][v], g[v], gm[n][v]);
-                        }
-            }
-        thread_map<true>(cut.starts, av, bv, f);
+            for (int v = 0; v < V; ++v) f[v].H = fmaf(av[k][v], f[v].H, mg[k][v] * xr[k].get(v));
+#pragma unroll
+        for (int k = T - 1; k >= 0; --k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v].H = av[k][v] * (gr[k].get(v) + e[v].H);
     } else {
-        thread_map<false>(0, av, bv, f);
+        float g[V];
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            if (starts >> k & 1) {
+                seq_value(a, a.h0, rows[wave][wt + k], c0, g);
+#pragma unroll
+                for (int v = 0; v < V; ++v) f[v].H = g[v];
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v].H = fmaf(av[k][v], f[v].H, mg[k][v] * xr[k].get(v));
+        }
+#pragma unroll
+        for (int k = T - 1; k >= 0; --k) {
+            if (ends >> k & 1) {
+                seq_value(a, a.dh_last, rows[wave][wt + k], c0, g);
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v].H = g[v];
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v].H = av[k][v] * (gr[k].get(v) + e[v].H);
+        }
     }
-    // what is added to dy: the gradient of a sequence's last state at its last position
-    float gv[T][V];
 #pragma unroll
-    for (int k = 0; k < T; ++k)
+    for (int v = 0; v < V; ++v) {
+        f[v].A = av[0][v];
 #pragma unroll
-        for (int v = 0; v < V; ++v) gv[k][v] = gr[k].get(v);
-    if (ends && a.dh_last && live)
-        for (uint32_t m = cut.ends; m; m &= m - 1) {
-            const int k = __builtin_ctz(m);
-            const float* last = a.dh_last + seq_row(a, pt + k, ts, c0);
-            float g[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[v] = last[v];
-#pragma unroll
-            for (int n = 0; n < T; ++n)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (n == k) gv[n][v] += g[v];
-        }
-#pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = {av[T - 1][v], av[T - 1][v] * gv[T - 1][v]};
-#pragma unroll
-    for (int k = T - 2; k >= 0; --k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float in = ends && (cut.ends >> k & 1) ? 0.0f : e[v].H;
-            e[v].H = av[k][v] * (gv[k][v] + in);
-            e[v].A *= av[k][v];
-        }
+        for (int k = 1; k < T; ++k) f[v].A *= av[k][v];
+        e[v].A = ends ? 0.0f : f[v].A;
+        f[v].A = starts ? 0.0f : f[v].A;
+    }
     Map fb[V], eb[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        if (ends) e[v].A = cut.ends ? -1.0f : e[v].A;
         Map total;
         scan_rows<CL, false>(f[v], lane, &total, &fb[v]);
         if (lane < CL) fwd[wave][lane * V + v] = make_float2(total.A, total.H);
@@ -765,6 +766,13 @@ __global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
         if (lane < CL) lds.wave[wave][lane * V + v] = make_float2(total.A, total.H);
     }
     __syncthreads();
+    // widening again is cheaper than keeping the widened values
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        forget(xr[k]);
+        forget(gr[k]);
+    }
+    pin_all(mg);
     const uint64_t tag = kChain ? dispatch_tag() : 0;
     if constexpr (kChain) {
         // what comes in comes from the tiles up to the end of the sequence that goes on behind this one
@@ -782,14 +790,27 @@ __global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
         for (int w = 0; w < wave; ++w) h[v] = Map{fwd[w][cl * V + v].x, fwd[w][cl * V + v].y}(h[v]);
         h[v] = fb[v](h[v]);
     }
+    if (!cuts) {
 #pragma unroll
-    for (int k = 0; k < T; ++k)
+        for (int k = 0; k < T; ++k)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (starts) h[v] = cut.starts >> k & 1 ? 0.0f : h[v];
-            ua[k][v] = fmaf(ua[k][v], h[v], -gm[k][v]);
-            h[v] = fmaf(av[k][v], h[v], bv[k][v]);
+            for (int v = 0; v < V; ++v) {
+                ua[k][v] = fmaf(ua[k][v], h[v], -gm[k][v]);
+                h[v] = fmaf(av[k][v], h[v], mg[k][v] * xr[k].get(v));
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            if (starts >> k & 1) seq_value(a, a.h0, rows[wave][wt + k], c0, h);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                ua[k][v] = fmaf(ua[k][v], h[v], -gm[k][v]);
+                h[v] = fmaf(av[k][v], h[v], mg[k][v] * xr[k].get(v));
+            }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < T; ++k) forget(xr[k]);
     float d[V], sum[V];
     if constexpr (kChain) {
         __syncthreads();
@@ -810,41 +831,52 @@ __global__ __launch_bounds__(256, 3) void k_gated_bwd(GatedArgs a) {
     dx.init(a, a.dx, a.ld_dx, p0, tg, c0);
     dr.init(a, a.dr, a.ld_dr, p0, tg, c0);
     di.init(a, a.di, a.ld_di, p0, tg, c0);
-#pragma unroll
-    for (int k = T - 1; k >= 0; --k) {
+    // the gradient's walk through position k; in: the position is inside the stream
+    auto walk = [&](int k, bool in) {
         float ox[V], orr[V], oi[V];
-        const bool in = full || pt + k < a.N;
         Raw<float, V> ns, ng;
         ns.load(&park[2 * k][tid * V]);
         ng.load(&park[2 * k + 1][tid * V]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (ends) d[v] = cut.ends >> k & 1 ? 0.0f : d[v];
-            const float del = gv[k][v] + d[v];
+            const float del = gr[k].get(v) + d[v];
             const float w = del * ua[k][v];
             ox[v] = del * mg[k][v];
             oi[v] = ox[v] * xr[k].get(v) * ng.get(v);
             orr[v] = w * ns.get(v);
-            sum[v] += in ? w : 0.0f;
-            bv[k][v] = d[v] = av[k][v] * del;
+            sum[v] += w;
+            d[v] = av[k][v] * del;
         }
         st_tile<IO, V>(dx.rsrc, dx.at(in), dx.so + k * dx.step, ox);
         st_tile<IO, V>(dr.rsrc, dr.at(in), dr.so + k * dr.step, orr);
         st_tile<IO, V>(di.rsrc, di.at(in), di.so + k * di.step, oi);
-    }
-    if (starts && a.dh0 && live)
-        for (uint32_t m = cut.starts; m; m &= m - 1) {
-            const int k = __builtin_ctz(m);
-            float* dst = a.dh0 + seq_row(a, pt + k, ts, c0);
-            at_position(bv, k, d);
+    };
+    if (!cuts) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) dst[v] = d[v];
+        for (int k = T - 1; k >= 0; --k) walk(k, pt < a.N);
+    } else {
+#pragma unroll
+        for (int k = T - 1; k >= 0; --k) {
+            if (ends >> k & 1) {
+                // behind the stream's end nothing counts for dlam (it may be NaN that came in from a tile)
+                seq_value(a, a.dh_last, rows[wave][wt + k], c0, d);
+#pragma unroll
+                for (int v = 0; v < V; ++v) sum[v] = pt + k == a.N - 1 ? 0.0f : sum[v];
+            }
+            walk(k, pt + k < a.N);
+            if (a.dh0 && live && (starts >> k & 1)) {
+                float* dst = a.dh0 + static_cast<int64_t>(rows[wave][wt + k]) * a.D + c0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) dst[v] = d[v];
+            }
         }
+    }
     pass_empty(a, a.dh_last, a.dh0, j, cb);
     if (!a.dlam) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float p, q;
+        sum[v] = pt < a.N && live ? sum[v] : 0.0f;
         if constexpr (CL == 16) {
             swap16(sum[v], &p, &q);
             sum[v] = p + q;
