@@ -20,6 +20,7 @@ constexpr int64_t kNormMaxWidth = 32768;
 // tokens, each thread tile * kGatedBlock / 256 elements.
 constexpr int kGatedBlock = 64;
 constexpr int kGatedFwdTile = 128;
+constexpr int kGatedFwdTileSmall = 64;
 constexpr int kGatedBwdTile = 64;
 // Tiles per group of the hand-over: a tile folds the aggregates of the tiles before it in its group
 // onto the state that the group before left.

@@ -44,6 +44,7 @@ using vimscan_host::GatedPlan;
 using vimscan_host::kGatedBlock;
 using vimscan_host::kGatedBwdTile;
 using vimscan_host::kGatedFwdTile;
+using vimscan_host::kGatedFwdTileSmall;
 using vimscan_host::kGatedGroup;
 using vimscan_host::kGatedStride;
 
@@ -487,10 +488,10 @@ __device__ __forceinline__ void seq_value(const GatedArgs& a, const float* from,
     for (int v = 0; v < V; ++v) h[v] = from && c0 < a.D ? p[v] : 0.0f;
 }
 
-// Forward pass: a tile of kGatedFwdTile positions x 64 channels.
-template <typename IO, int V, bool kChain>
-__global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_fwd(GatedArgs a) {
-    constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedFwdTile / TG;
+// Forward pass: a tile of TILE positions x 64 channels.
+template <typename IO, int V, int TILE, bool kChain>
+__global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_fwd(GatedArgs a) {
+    constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = TILE / TG;
     __shared__ ChainLds lds;
     constexpr int P = T * 64 / CL;  // positions of a wave
     __shared__ int rows[4][P];
@@ -500,18 +501,18 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
     if (a.N == 0) return pass_empty(a, a.h0, a.h_last, j, cb);
     const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
     const bool live = c0 < a.D;
-    const int p0 = j * kGatedFwdTile, pt = p0 + tg * T;
+    const int p0 = j * TILE, pt = p0 + tg * T;
 
     float k2[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) k2[v] = a.lam[live ? c0 + v : 0];
     Raw<IO, V> xr[T], rr[T], ir[T];
     {
-        TileRows<IO, kGatedFwdTile, T> x, r, i;
+        TileRows<IO, TILE, T> x, r, i;
         r.init(a, a.r, a.ld_r, p0, tg, c0);
         i.init(a, a.i, a.ld_i, p0, tg, c0);
         x.init(a, a.x, a.ld_x, p0, tg, c0);
-        if (p0 + kGatedFwdTile <= a.N) {
+        if (p0 + TILE <= a.N) {
 #pragma unroll
             for (int k = 0; k < T; ++k) {
                 rr[k] = ld_tile<IO, V>(r.rsrc, r.vo, r.so + k * r.step);
@@ -580,7 +581,7 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
     if constexpr (kChain) {
         const uint64_t tag = dispatch_tag();
         const int start = bound_of(a, q0);
-        const int first = start >= p0 ? j : start / kGatedFwdTile;
+        const int first = start >= p0 ? j : start / TILE;
         chain_gather<false>(a, lds, j, cb, first, tag, wave, lane);
         __syncthreads();
         chain_leave<false>(a, lds, j, cb, tag, wave, lane);
@@ -600,7 +601,7 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
 #pragma unroll
         for (int v = 0; v < V; ++v) dst[v] = h[v];
     }
-    TileRows<IO, kGatedFwdTile, T> y;
+    TileRows<IO, TILE, T> y;
     y.init(a, a.y, a.D, p0, tg, c0);
     if (!cuts) {
         // (also a wave past the stream's end comes here, without a boundary: its stores are dropped)
@@ -919,19 +920,6 @@ __global__ __launch_bounds__(1024) void k_gated_dlam(GatedArgs a, int parts) {
     a.dlam[d] = sum * ratio;
 }
 
-template <typename IO>
-__device__ __forceinline__ float ld(const void* p, int64_t k) {
-    Raw<IO, 1> w;
-    w.load(static_cast<const IoElem<IO>*>(p) + k);
-    return w.get(0);
-}
-template <typename IO>
-__device__ __forceinline__ void st(void* p, int64_t k, float v) {
-    Raw<IO, 1> w;
-    w.set(&v);
-    w.store(static_cast<IoElem<IO>*>(p) + k);
-}
-
 struct StepArgs {
     const void* x;
     const void* r;
@@ -944,25 +932,41 @@ struct StepArgs {
     const int32_t* slots_in;
     const int32_t* slots_out;
     void* y;
-    int32_t D, ncb;
+    int32_t D, batch, per_row;
 };
 
-// One token: a wave per row and block of 64 channels.
-template <typename IO>
-__global__ __launch_bounds__(64) void k_gated_step(StepArgs a) {
-    const int64_t b = blockIdx.x / a.ncb;
-    const int d = static_cast<int>(blockIdx.x % a.ncb) * 64 + static_cast<int>(threadIdx.x);
-    if (d >= a.D) return;
-    const int64_t from = a.slots_in ? a.slots_in[b] : b;
+// One token: V channels a thread, a row of D takes per_row threads.
+template <typename IO, int V>
+__global__ __launch_bounds__(256) void k_gated_step(StepArgs a) {
+    const uint32_t t = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t b = t / static_cast<uint32_t>(a.per_row);
+    const int d = static_cast<int>(t - b * static_cast<uint32_t>(a.per_row)) * V;
+    if (b >= static_cast<uint32_t>(a.batch)) return;
+    using E = IoElem<IO>;
+    const int64_t from = a.slots_in ? a.slots_in[b] : static_cast<int64_t>(b);
     const int64_t to = a.slots_out ? a.slots_out[b] : from;
-    float h = 0.0f;
-    if (from >= 0 && from < a.nslots && to >= 0 && to < a.nslots) {
+    Raw<IO, V> x, r, i, y;
+    Raw<float, V> lam, s;
+    x.load(static_cast<const E*>(a.x) + b * a.ld_x + d);
+    r.load(static_cast<const E*>(a.r) + b * a.ld_r + d);
+    i.load(static_cast<const E*>(a.i) + b * a.ld_i + d);
+    lam.load(a.lam + d);
+    const bool in = from >= 0 && from < a.nslots && to >= 0 && to < a.nslots;
+    if (in) s.load(a.state + from * a.D + d);
+    else s.zero();
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
         float at, mg;
-        gates(ld<IO>(a.r, b * a.ld_r + d), ld<IO>(a.i, b * a.ld_i + d), decay_rate(a.lam[d], a.c), &at, &mg);
-        h = fmaf(at, a.state[from * a.D + d], mg * ld<IO>(a.x, b * a.ld_x + d));
-        a.state[to * a.D + d] = h;
+        gates(r.get(v), i.get(v), decay_rate(lam.get(v), a.c), &at, &mg);
+        h[v] = in ? fmaf(at, s.get(v), mg * x.get(v)) : 0.0f;
     }
-    st<IO>(a.y, b * a.D + d, h);
+    if (in) {
+        s.set(h);
+        s.store(a.state + to * a.D + d);
+    }
+    y.set(h);
+    y.store(static_cast<E*>(a.y) + static_cast<int64_t>(b) * a.D + d);
 }
 
 GatedArgs common_args(const vimscan_gated* g, const vimscan_launch* l, const GatedPlan& p) {
@@ -1007,24 +1011,30 @@ bool record(const vimscan_launch* l, int k) {
     return hipEventRecord(static_cast<hipEvent_t>(l->scan_events[k]), static_cast<hipStream_t>(l->stream)) == hipSuccess;
 }
 
-// VEC channels per lane where every row of every tensor is aligned to them.
-#ifndef VEC
-#define VEC 2
-#endif
+// kVec channels per lane where every row of every tensor is aligned to them: two are enough to read rows
+// of 128 or 256 bytes a half wave, and leave a thread more positions of fewer channels than four (the work
+// per thread and channel outside the element loops: maps, waits, carries); measured 40 us with either at
+// 128 x 197 x 768 bf16 forward, 89 us against 136 us backward.
+constexpr int kVec = 2;
 bool by_vec(const vimscan_gated* g, int64_t d, size_t e, const void* const* more, const int64_t* lds, int n) {
     auto ok = [&](const void* p, int64_t ld) {
-        return !p || (reinterpret_cast<uintptr_t>(p) % (VEC * e) == 0 && ld % VEC == 0);
+        return !p || (reinterpret_cast<uintptr_t>(p) % (kVec * e) == 0 && ld % kVec == 0);
     };
-    bool r = d % VEC == 0 && ok(g->x, g->ld_x) && ok(g->r, g->ld_r) && ok(g->i, g->ld_i);
+    bool r = d % kVec == 0 && ok(g->x, g->ld_x) && ok(g->r, g->ld_r) && ok(g->i, g->ld_i);
     for (int k = 0; k < n; ++k) r = r && ok(more[k], lds[k]);
     return r;
 }
 
+template <typename IO, int V, int TILE>
+void launch_fwd_tile(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.wgs));
+    if (p.chain) hipLaunchKernelGGL((k_gated_fwd<IO, V, TILE, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_gated_fwd<IO, V, TILE, false>), grid, dim3(256), 0, s, a);
+}
 template <typename IO, int V>
 void launch_fwd(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.wgs));
-    if (p.chain) hipLaunchKernelGGL((k_gated_fwd<IO, V, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_gated_fwd<IO, V, false>), grid, dim3(256), 0, s, a);
+    if (p.tile == kGatedFwdTile) launch_fwd_tile<IO, V, kGatedFwdTile>(a, p, s);
+    else launch_fwd_tile<IO, V, kGatedFwdTileSmall>(a, p, s);
 }
 
 template <typename IO, int V>
@@ -1069,8 +1079,8 @@ int vimscan_gated_fwd(const vimscan_gated* g, int64_t seg_len, void* y, float* h
     const int64_t out_ld[] = {launch->d_inner};
     const bool f32 = launch->io_dtype == VIMSCAN_F32;
     if (by_vec(g, launch->d_inner, f32 ? 4 : 2, out, out_ld, 1)) {
-        if (f32) launch_fwd<float, VEC>(a, p, s);
-        else launch_fwd<Bf16, VEC>(a, p, s);
+        if (f32) launch_fwd<float, kVec>(a, p, s);
+        else launch_fwd<Bf16, kVec>(a, p, s);
     } else {
         if (f32) launch_fwd<float, 1>(a, p, s);
         else launch_fwd<Bf16, 1>(a, p, s);
@@ -1108,8 +1118,8 @@ int vimscan_gated_bwd(const vimscan_gated* g, int64_t seg_len, const vimscan_gat
         const int64_t lds[] = {grad->ld_dy, grad->ld_dx, grad->ld_dr, grad->ld_di};
         const bool f32 = launch->io_dtype == VIMSCAN_F32;
         if (by_vec(g, launch->d_inner, f32 ? 4 : 2, more, lds, 4)) {
-            if (f32) launch_bwd<float, VEC>(a, p, s);
-            else launch_bwd<Bf16, VEC>(a, p, s);
+            if (f32) launch_bwd<float, kVec>(a, p, s);
+            else launch_bwd<Bf16, kVec>(a, p, s);
         } else {
             if (f32) launch_bwd<float, 1>(a, p, s);
             else launch_bwd<Bf16, 1>(a, p, s);
@@ -1145,12 +1155,24 @@ int vimscan_gated_step(const vimscan_gated* g, float* state, int64_t nslots, con
     a.slots_out = slots_out;
     a.y = y;
     a.D = static_cast<int32_t>(launch->d_inner);
-    a.ncb = static_cast<int32_t>((launch->d_inner + 63) / 64);
+    a.batch = static_cast<int32_t>(launch->batch);
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
+    const bool f32 = launch->io_dtype == VIMSCAN_F32;
+    const void* out[] = {y};
+    const int64_t out_ld[] = {launch->d_inner};
+    const bool vec = by_vec(g, launch->d_inner, f32 ? 4 : 2, out, out_ld, 1) &&
+                     reinterpret_cast<uintptr_t>(g->lam) % (4 * kVec) == 0 &&
+                     reinterpret_cast<uintptr_t>(state) % (4 * kVec) == 0;
+    a.per_row = static_cast<int32_t>(vec ? launch->d_inner / kVec : launch->d_inner);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
-    const dim3 grid(static_cast<unsigned>(launch->batch * a.ncb));
-    if (launch->io_dtype == VIMSCAN_F32) hipLaunchKernelGGL(k_gated_step<float>, grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL(k_gated_step<Bf16>, grid, dim3(64), 0, s, a);
+    const dim3 grid(static_cast<unsigned>((launch->batch * a.per_row + 255) / 256));
+    if (vec) {
+        if (f32) hipLaunchKernelGGL((k_gated_step<float, kVec>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_gated_step<Bf16, kVec>), grid, dim3(256), 0, s, a);
+    } else {
+        if (f32) hipLaunchKernelGGL((k_gated_step<float, 1>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_gated_step<Bf16, 1>), grid, dim3(256), 0, s, a);
+    }
     if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
     return VIMSCAN_OK;
 }
