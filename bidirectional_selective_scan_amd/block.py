@@ -108,6 +108,8 @@ class _Call:
     """A prepared ctypes call: the buffers it keeps alive, its launch description, its stream."""
 
     def _prepare(self, dev, stream, launch, fn, args, own, keep):
+        # arguments as ctypes objects once, so that a call converts nothing
+        args = tuple(t(a) if isinstance(a, int) else a for a, t in zip(args, fn.argtypes))
         self._launch, self._fn, self._args, self._keep = launch, fn, args, keep
         # with several GPUs the call must be made with the tensors' device current
         self._dev = dev if torch.cuda.device_count() > 1 else None

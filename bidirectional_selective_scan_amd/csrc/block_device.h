@@ -123,6 +123,43 @@ template <> struct Raw<float, 8> {
     }
 };
 
+// Every lane's pair: the values of the even and the odd row of 16 lanes, or of the lower and the
+// upper 32 lanes.
+__device__ __forceinline__ void swap16(float v, float* even, float* odd) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    *even = __uint_as_float(r[0]);
+    *odd = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap32(float v, float* lo, float* hi) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    *lo = __uint_as_float(r[0]);
+    *hi = __uint_as_float(r[1]);
+}
+
+// Sum of column c0 + (lane of 16) over the rows of part, width elements apart, by a workgroup of 1024: each
+// thread takes every 64th row of its column, then its wave's four row groups and the 16 waves are added, in a
+// fixed order. The result is in threads 0..15 (0 in a column past cols). 16 columns to a workgroup: a few
+// hundred rows of some hundred columns spread over dozens of workgroups, a few loads per thread.
+constexpr int kColumns = 16;
+__device__ __forceinline__ float column_sum(const float* part, int64_t rows, int64_t width, int c0, int cols) {
+    __shared__ float lds[16][kColumns];
+    const int tid = static_cast<int>(threadIdx.x), c = c0 + (tid & 15);
+    float s = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int64_t k = tid >> 4; k < rows; k += 64) s += part[k * width + c];
+    }
+    float p, q;
+    swap16(s, &p, &q);
+    swap32(p + q, &p, &q);
+    if ((tid & 63) < 16) lds[tid >> 6][tid & 15] = p + q;
+    __syncthreads();
+    s = 0.0f;
+    if (tid < 16)
+        for (int k = 0; k < 16; ++k) s += lds[k][tid];
+    return s;
+}
+
 }  // namespace vimscan_dev
 
 #endif  // VIMSCAN_BLOCK_DEVICE_H

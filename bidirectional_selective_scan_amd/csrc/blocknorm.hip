@@ -50,10 +50,10 @@ __device__ __forceinline__ float wave_sum(float v) {
     v = add_dpp<0x4E>(v);   // lane ^ 2
     v = add_dpp<0x141>(v);  // half row mirrored
     v = add_dpp<0x140>(v);  // row mirrored
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+    float p, q;
+    swap16(v, &p, &q);
+    swap32(p + q, &p, &q);
+    return p + q;
 }
 
 // Sums of two values over the W waves of a row, in the waves' order. Calls alternate between two slots:
@@ -327,25 +327,13 @@ __global__ __launch_bounds__((Spread<V, NV, W>::kThreads)) void k_norm_bwd(NormA
     }
 }
 
-// The weight gradients: the workgroups' partial sums, 16 waves taking every 16th each, then the waves in
-// their order.
+// The weight gradients: the workgroups' partial sums.
 __global__ __launch_bounds__(1024) void k_norm_cols(NormArgs a, int parts) {
-    __shared__ float lds[16][64];
-    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
-    const int c = static_cast<int>(blockIdx.x) * 64 + lane;
     float* dst = a.dw[blockIdx.y];
     if (!dst) return;
-    float s = 0.0f;
-    if (c < a.D) {
-#pragma unroll 8
-        for (int k = wave; k < parts; k += 16) s += a.part[(static_cast<int64_t>(k) * 3 + blockIdx.y) * a.D + c];
-    }
-    lds[wave][lane] = s;
-    __syncthreads();
-    if (wave != 0 || c >= a.D) return;
-    s = 0.0f;
-    for (int k = 0; k < 16; ++k) s += lds[k][lane];
-    dst[c] = s;
+    const int c0 = static_cast<int>(blockIdx.x) * kColumns, c = c0 + static_cast<int>(threadIdx.x);
+    const float s = column_sum(a.part + static_cast<int64_t>(blockIdx.y) * a.D, parts, 3 * static_cast<int64_t>(a.D), c0, a.D);
+    if (threadIdx.x < kColumns && c < a.D) dst[c] = s;
 }
 
 // Wide loads where every row of every tensor, and every weight, is aligned to them.
@@ -371,7 +359,7 @@ void launch(const NormArgs& a, const NormPlan& p, bool back, hipStream_t s) {
     if (back) hipLaunchKernelGGL((k_norm_bwd<IO, RES, V, NV, W>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_norm_fwd<IO, RES, V, NV, W>), grid, block, 0, s, a);
     if (back && a.part)
-        hipLaunchKernelGGL(k_norm_cols, dim3(static_cast<unsigned>((a.D + 63) / 64), 3), dim3(1024), 0, s, a,
+        hipLaunchKernelGGL(k_norm_cols, dim3(static_cast<unsigned>((a.D + kColumns - 1) / kColumns), 3), dim3(1024), 0, s, a,
                            static_cast<int>(grid.x));
 }
 

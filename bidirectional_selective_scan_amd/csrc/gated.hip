@@ -283,19 +283,6 @@ __device__ __forceinline__ Map identity() { return {1.0f, 0.0f}; }
 __device__ __forceinline__ Map then(const Map& f, const Map& g) { return {vimscan_mul_legacy(f.A, g.A), g(f.H)}; }
 __device__ __forceinline__ Map pick(bool c, const Map& f, const Map& g) { return {c ? f.A : g.A, c ? f.H : g.H}; }
 
-// Every lane's pair: the values of the even and the odd row of 16 lanes, or of the lower and the
-// upper 32 lanes.
-__device__ __forceinline__ void swap16(float v, float* even, float* odd) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    *even = __uint_as_float(r[0]);
-    *odd = __uint_as_float(r[1]);
-}
-__device__ __forceinline__ void swap32(float v, float* lo, float* hi) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    *lo = __uint_as_float(r[0]);
-    *hi = __uint_as_float(r[1]);
-}
-
 // Composes the maps of a wave's position groups (64 / CL of them, CL lanes each): total of the wave,
 // and before: the map of the groups before this lane's in walking order, or after it with kBack.
 template <int CL, bool kBack>
@@ -898,21 +885,11 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
             (fwd[0][lane].x + fwd[1][lane].x) + (fwd[2][lane].x + fwd[3][lane].x);
 }
 
-// dlam = sigmoid(lam) / softplus(lam) * the sum of the tiles' partial sums, in a fixed order: 16 waves
-// take every 16th tile each.
+// dlam = sigmoid(lam) / softplus(lam) * the sum of the tiles' partial sums.
 __global__ __launch_bounds__(1024) void k_gated_dlam(GatedArgs a, int parts) {
-    __shared__ float lds[16][64];
-    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
-    const int d = static_cast<int>(blockIdx.x) * 64 + lane;
-    const int64_t width = static_cast<int64_t>(a.ncb) * kGatedBlock;
-    float sum = 0.0f;
-#pragma unroll 8
-    for (int k = wave; k < parts; k += 16) sum += a.part[k * width + d];
-    lds[wave][lane] = sum;
-    __syncthreads();
-    if (wave != 0 || d >= a.D) return;
-    sum = 0.0f;
-    for (int k = 0; k < 16; ++k) sum += lds[k][lane];
+    const int c0 = static_cast<int>(blockIdx.x) * kColumns, d = c0 + static_cast<int>(threadIdx.x);
+    const float sum = column_sum(a.part, parts, static_cast<int64_t>(a.ncb) * kGatedBlock, c0, a.D);
+    if (threadIdx.x >= kColumns || d >= a.D) return;
     const float lam = a.lam[d];
     const float sp = decay_rate(lam, -kLn2);  // softplus(lam)
     // both tend to e^lam as lam goes to -infinity, where the ratio goes to 1
@@ -1126,9 +1103,8 @@ int vimscan_gated_bwd(const vimscan_gated* g, int64_t seg_len, const vimscan_gat
         }
     }
     if (a.dlam) {
-        const unsigned blocks = static_cast<unsigned>((launch->d_inner + 63) / 64);
+        const unsigned blocks = static_cast<unsigned>((launch->d_inner + kColumns - 1) / kColumns);
         const int parts = p.tokens > 0 && p.wgs > 0 ? static_cast<int>(p.tiles) : 0;
-        a.ncb = static_cast<int32_t>(blocks);
         hipLaunchKernelGGL(k_gated_dlam, dim3(blocks), dim3(1024), 0, s, a, parts);
     }
     if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
