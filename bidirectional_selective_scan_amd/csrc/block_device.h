@@ -123,6 +123,43 @@ template <> struct Raw<float, 8> {
     }
 };
 
+// The same from and to any element address: the hardware takes a wide access at any alignment (the
+// unaligned access mode of the HSA target), which memcpy tells the compiler.
+template <typename IO, int V>
+__device__ __forceinline__ void load_any(Raw<IO, V>& r, const IoElem<IO>* p) { __builtin_memcpy(&r, p, sizeof(r)); }
+template <typename IO, int V>
+__device__ __forceinline__ void store_any(const Raw<IO, V>& r, IoElem<IO>* p) { __builtin_memcpy(p, &r, sizeof(r)); }
+// The first n < V elements.
+template <typename IO, int V>
+__device__ __forceinline__ void load_some(Raw<IO, V>& r, const IoElem<IO>* p, int n) {
+    IoElem<IO> e[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) e[k] = k < n ? p[k] : IoElem<IO>(0);
+    __builtin_memcpy(&r, e, sizeof(r));
+}
+// Elements n.. move to 0.., zeros behind them.
+__device__ __forceinline__ void shift_down(Raw<Bf16, 4>& r, int n) {
+    uint64_t w;
+    __builtin_memcpy(&w, &r, 8);
+    w >>= 16 * n;
+    __builtin_memcpy(&r, &w, 8);
+}
+__device__ __forceinline__ void shift_down(Raw<float, 4>& r, int n) {
+    const float4 w = r.w;
+    r.w.x = n == 0 ? w.x : n == 1 ? w.y : n == 2 ? w.z : w.w;
+    r.w.y = n == 0 ? w.y : n == 1 ? w.z : n == 2 ? w.w : 0.0f;
+    r.w.z = n == 0 ? w.z : n == 1 ? w.w : 0.0f;
+    r.w.w = n == 0 ? w.w : 0.0f;
+}
+template <typename IO, int V>
+__device__ __forceinline__ void store_some(const Raw<IO, V>& r, IoElem<IO>* p, int n) {
+    IoElem<IO> e[V];
+    __builtin_memcpy(e, &r, sizeof(r));
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        if (k < n) p[k] = e[k];
+}
+
 // Every lane's pair: the values of the even and the odd row of 16 lanes, or of the lower and the
 // upper 32 lanes.
 __device__ __forceinline__ void swap16(float v, float* even, float* odd) {

@@ -201,7 +201,10 @@ int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p) {
     p->rows = l->batch * l->seqlen;
     p->D = l->d_inner;
     if (p->rows == 0 || p->D == 0) return VIMSCAN_OK;
-    p->wgs = p->rows < 512 ? p->rows : 512;
+    // enough workgroups for every CU's waves; fewer, each with more rows, where every one leaves three rows
+    // of partial weight gradients
+    const int64_t most = p->D <= 256 ? 2048 : 512;
+    p->wgs = p->rows < most ? p->rows : most;
     p->rows_per_wg = (p->rows + p->wgs - 1) / p->wgs;
     if (backward) p->ws = up256(static_cast<size_t>(p->wgs) * 3 * p->D * sizeof(float));
     return VIMSCAN_OK;
