@@ -241,10 +241,14 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
     constexpr int NV = S::NV, L = S::L, W = S::W, V = S::V;
     __shared__ float2 lds[2][W];
     const int wave = S::wave();
+    // (a workgroup of 1024 threads has 128 registers a thread: there the weights are read again per row)
+    constexpr bool kKeep = W < 16;
     float wp[NV][V], ga[NV][V], wn[NV][V];
-    ld_weight<S>(a.w_post, a.D, wp);
-    ld_weight<S>(a.gamma, a.D, ga);
-    ld_weight<S>(a.w_pre, a.D, wn);
+    if constexpr (kKeep) {
+        ld_weight<S>(a.w_post, a.D, wp);
+        ld_weight<S>(a.gamma, a.D, ga);
+        ld_weight<S>(a.w_pre, a.D, wn);
+    }
     float dwp[NV][V], dga[NV][V], dwn[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -265,6 +269,11 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
         settle<RES, S>(a.D, r);
         settle<IO, S>(a.D, dn);
         settle<RES, S>(a.D, ds);
+        if constexpr (!kKeep) {
+            ld_weight<S>(a.w_post, a.D, wp);
+            ld_weight<S>(a.gamma, a.D, ga);
+            ld_weight<S>(a.w_pre, a.D, wn);
+        }
         // val: the post-norm's input; s: the sum
         float val[NV][V], s[NV][V];
         float u = 0.0f, t = 0.0f;
@@ -357,40 +366,41 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
         st_row<float, S>(part, a.D, a.D, dga);
         st_row<float, S>(part, 2 * a.D, a.D, dwn);
     } else {
-        // the rows of a wave, then the workgroup's waves in their order, one weight at a time
-        constexpr int kTurns = S::kThreads / 64;
+        // the rows of a wave, then the workgroup's four waves in their order
+        constexpr int kWaves = S::kThreads / 64;
         const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-        const bool first = (threadIdx.x & 63) < L;
-        __shared__ float col[NV * V][L];
-        auto add_up = [&](float (&g)[NV][V], int which) {
-            for (int turn = 0; turn < kTurns; ++turn) {
-                if (w == turn) {
+        __shared__ float col[3][kWaves][NV * V][L];
+        auto leave = [&](float (&g)[NV][V], int which) {
 #pragma unroll
-                    for (int k = 0; k < NV; ++k)
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            float p, q;
-                            if constexpr (L < 32) {
-                                swap16(g[k][v], &p, &q);
-                                g[k][v] = p + q;
-                            }
-                            if constexpr (L < 64) {
-                                swap32(g[k][v], &p, &q);
-                                g[k][v] = p + q;
-                            }
-                            if (first) {
-                                if (turn > 0) g[k][v] += col[k * V + v][S::place()];
-                                col[k * V + v][S::place()] = g[k][v];
-                            }
-                        }
-                    if (turn == kTurns - 1 && first) st_row<float, S>(part, which * a.D, a.D, g);
+                for (int v = 0; v < V; ++v) {
+                    float p, q;
+                    if constexpr (L < 32) {
+                        swap16(g[k][v], &p, &q);
+                        g[k][v] = p + q;
+                    }
+                    if constexpr (L < 64) {
+                        swap32(g[k][v], &p, &q);
+                        g[k][v] = p + q;
+                    }
+                    if ((threadIdx.x & 63) < L) col[which][w][k * V + v][S::place()] = g[k][v];
                 }
-                __syncthreads();
-            }
         };
-        add_up(dwp, 0);
-        add_up(dga, 1);
-        add_up(dwn, 2);
+        leave(dwp, 0);
+        leave(dga, 1);
+        leave(dwn, 2);
+        __syncthreads();
+        // one channel of one weight per thread and turn
+        for (int n = static_cast<int>(threadIdx.x); n < 3 * S::kWidth; n += S::kThreads) {
+            const int which = n / S::kWidth, c = n % S::kWidth;
+            if (c >= a.D) continue;
+            const int v = c % V, at = c / V % L, k = c / V / L;
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < kWaves; ++t) sum += col[which][t][k * V + v][at];
+            part[which * static_cast<int64_t>(a.D) + c] = sum;
+        }
     }
 }
 
