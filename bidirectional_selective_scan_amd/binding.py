@@ -372,7 +372,14 @@ def ncssd_fwd(x, B, C, m, seg_len: int = 0, out=None, chunk_len: int = 0, worksp
     return PreparedNcssd(x, B, C, m, seg_len, out, chunk_len, workspace)()
 
 
-# The recurrent block's operators are part of this interface (block.py uses the helpers above).
-from .block import (GATED_STRIDE, GatedInputs, PreparedBlockNorm, PreparedBlockNormGrad,  # noqa: E402,F401
-                    PreparedGated, PreparedGatedGrad, PreparedGatedStep, block_norm, gated_fwd, gated_info, gated_step,
-                    norm_info)
+# The recurrent block's operators (block.py, which uses the helpers above) are part of this interface.
+_BLOCK_NAMES = ("GATED_STRIDE", "GatedInputs", "PreparedBlockNorm", "PreparedBlockNormGrad", "PreparedGated",
+                "PreparedGatedGrad", "PreparedGatedStep", "block_norm", "gated_fwd", "gated_info", "gated_step",
+                "norm_info")
+
+
+def __getattr__(name):
+    if name in _BLOCK_NAMES:
+        from . import block
+        return getattr(block, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
