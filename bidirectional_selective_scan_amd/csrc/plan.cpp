@@ -397,7 +397,7 @@ const char* vimscan_status_string(int status) {
     return kStatusText[i];
 }
 
-const char* vimscan_version(void) { return "vimscan 0.3.0 gfx950"; }
+const char* vimscan_version(void) { return "vimscan 0.4.0 gfx950"; }
 
 int vimscan_ncssd_plan(const vimscan_launch* launch, int64_t seg_len, vimscan_plan* plan) {
     if (!plan) return VIMSCAN_ERR_NULL;

@@ -341,7 +341,9 @@ typedef struct vimscan_gated {
  * needs: row k receives the state entering the k-th group of VIMSCAN_GATED_STRIDE tokens in walking
  * order (unspecified where a sequence starts there). y, h_last and states must not overlap an input,
  * each other or the workspace (of strided rows the whole extent counts). Pointers are aligned to
- * their element size. An empty call (no tokens) only writes h_last.
+ * their element size. An empty call (no tokens) only writes h_last. Where sequences go on from one
+ * workgroup's tokens to the next one's, the states are handed over through the workspace
+ * (vimscan_gated_plan; its contents on entry do not matter).
  */
 int vimscan_gated_fwd(const vimscan_gated* g, int64_t seg_len, void* y, float* h_last, float* states,
                       const vimscan_launch* launch);
@@ -463,7 +465,7 @@ int vimscan_workspace_bytes(const vimscan_launch* launch, int64_t seg_len, size_
 /* Static text for a status code; never NULL. */
 const char* vimscan_status_string(int status);
 
-/* Library version string, e.g. "vimscan 0.3.0 gfx950". */
+/* Library version string, e.g. "vimscan 0.4.0 gfx950". */
 const char* vimscan_version(void);
 
 /*

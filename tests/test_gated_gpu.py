@@ -430,3 +430,52 @@ def test_nothing_is_written_past_the_last_sequence(seqlen, seg, d):
     ref.check(h, want["h_last"])
     assert bool((hbuf[:4] == 7).all()) and bool((hbuf[4 + nseq:] == 7).all())
     assert bool((ybuf[:100] == 7).all()) and bool((ybuf[100 + 3 * seqlen:] == 7).all())
+
+
+def test_graph_replays_see_new_inputs():
+    """A captured forward and backward pass over a sequence of many workgroups, replayed on inputs that
+    change between the replays: the states handed over are this replay's, not the last one's."""
+    p = Problem(1, 20000, 64, "f32", seed=31)
+    p.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s = torch.cuda.current_stream().cuda_stream
+        f = PreparedGated(p.inputs(), None, None, None, save_states=True, stream=s)
+        f()
+        b = PreparedGatedGrad(f, p.dy, p.dh_last, stream=s)
+        b()
+    for k in range(4):
+        for t in (p.x, p.r, p.i, p.dy, p.h0):
+            t.copy_(torch.randn_like(t))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        f1, b1 = p.run()
+        for a, c in zip((f.y, f.h_last, b.dx, b.dr, b.di, b.dlam, b.dh0),
+                        (f1.y, f1.h_last, b1.dx, b1.dr, b1.di, b1.dlam, b1.dh0)):
+            assert torch.equal(a, c), k
+    assert binding.wait_timeouts() == 0
+
+
+def test_a_workspace_of_arbitrary_contents():
+    """The hand-over needs no cleared workspace: zeros, ones, equal words and another call's leftovers."""
+    p = Problem(1, 3000, 66, "f32", seed=32)
+    f0, b0 = p.run()
+    need = max(f0.plan["workspace_bytes"], b0.plan["workspace_bytes"])
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    other = Problem(1, 3000, 66, "f32", seed=33)
+    for fill in (0, 255, 63, "other"):
+        if fill == "other":
+            PreparedGated(other.inputs(), None, None, None, workspace=ws)()
+        else:
+            ws.fill_(fill)
+        f = PreparedGated(p.inputs(), None, None, None, save_states=True, workspace=ws)
+        f()
+        assert torch.equal(f.y, f0.y) and torch.equal(f.h_last, f0.h_last)
+        if fill != "other":
+            ws.fill_(fill)
+        b = PreparedGatedGrad(f, p.dy, p.dh_last, workspace=ws)
+        b()
+        for a, c in ((b.dx, b0.dx), (b.dr, b0.dr), (b.di, b0.di), (b.dlam, b0.dlam), (b.dh0, b0.dh0)):
+            assert torch.equal(a, c)
