@@ -227,46 +227,51 @@ struct TileRows {
     __device__ __forceinline__ uint32_t at(bool in) const { return in ? vo : kOutside; }
 };
 
-template <typename IO, int V>
+// Cache policy of the rows' accesses. kOnce: the lines are not wanted again and are evicted first. Taken
+// where every row starts on a line, so that no two workgroups share one: 65537 x 1536 bf16 forward 188 us
+// instead of 203, 128 x 197 x 768 backward 67 instead of 72; where workgroups do share lines it makes them be
+// fetched twice (32 x 1024 x 770: 81 us instead of 65).
+constexpr int kPlain = 0, kOnce = 2;
+template <typename IO, int V, int kPolicy>
 __device__ __forceinline__ Raw<IO, V> ld_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so) {
     Raw<IO, V> o;
     if constexpr (sizeof(o) == 2) {
-        const uint16_t w = __builtin_amdgcn_raw_buffer_load_b16(r, vo, so, 0);
+        const uint16_t w = __builtin_amdgcn_raw_buffer_load_b16(r, vo, so, kPolicy);
         __builtin_memcpy(&o, &w, 2);
     } else if constexpr (sizeof(o) == 4) {
-        const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
+        const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, kPolicy);
         __builtin_memcpy(&o, &w, 4);
     } else if constexpr (sizeof(o) == 8) {
-        const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, vo, so, 0);
+        const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, vo, so, kPolicy);
         __builtin_memcpy(&o, &w, 8);
     } else {
-        const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, vo, so, 0);
+        const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, vo, so, kPolicy);
         __builtin_memcpy(&o, &w, 16);
     }
     return o;
 }
 using U2 = uint32_t __attribute__((vector_size(8)));
 using U4 = uint32_t __attribute__((vector_size(16)));
-template <typename IO, int V>
+template <typename IO, int V, int kPolicy>
 __device__ __forceinline__ void st_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so, const float* v) {
     Raw<IO, V> o;
     o.set(v);
     if constexpr (sizeof(o) == 2) {
         uint16_t w;
         __builtin_memcpy(&w, &o, 2);
-        __builtin_amdgcn_raw_buffer_store_b16(w, r, vo, so, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(w, r, vo, so, kPolicy);
     } else if constexpr (sizeof(o) == 4) {
         uint32_t w;
         __builtin_memcpy(&w, &o, 4);
-        __builtin_amdgcn_raw_buffer_store_b32(w, r, vo, so, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(w, r, vo, so, kPolicy);
     } else if constexpr (sizeof(o) == 8) {
         U2 w;
         __builtin_memcpy(&w, &o, 8);
-        __builtin_amdgcn_raw_buffer_store_b64(w, r, vo, so, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(w, r, vo, so, kPolicy);
     } else {
         U4 w;
         __builtin_memcpy(&w, &o, 16);
-        __builtin_amdgcn_raw_buffer_store_b128(w, r, vo, so, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, vo, so, kPolicy);
     }
 }
 
@@ -476,7 +481,7 @@ __device__ __forceinline__ void seq_value(const GatedArgs& a, const float* from,
 }
 
 // Forward pass: a tile of TILE positions x 64 channels.
-template <typename IO, int V, int TILE, bool kChain>
+template <typename IO, int V, int TILE, bool kChain, int kPolicy>
 __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_fwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = TILE / TG;
     __shared__ ChainLds lds;
@@ -502,16 +507,16 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
         if (p0 + TILE <= a.N) {
 #pragma unroll
             for (int k = 0; k < T; ++k) {
-                rr[k] = ld_tile<IO, V>(r.rsrc, r.vo, r.so + k * r.step);
-                ir[k] = ld_tile<IO, V>(i.rsrc, i.vo, i.so + k * i.step);
-                xr[k] = ld_tile<IO, V>(x.rsrc, x.vo, x.so + k * x.step);
+                rr[k] = ld_tile<IO, V, kPolicy>(r.rsrc, r.vo, r.so + k * r.step);
+                ir[k] = ld_tile<IO, V, kPolicy>(i.rsrc, i.vo, i.so + k * i.step);
+                xr[k] = ld_tile<IO, V, kPolicy>(x.rsrc, x.vo, x.so + k * x.step);
             }
         } else {
 #pragma unroll
             for (int k = 0; k < T; ++k) {
-                rr[k] = ld_tile<IO, V>(r.rsrc, r.at(pt + k < a.N), r.so + k * r.step);
-                ir[k] = ld_tile<IO, V>(i.rsrc, i.at(pt + k < a.N), i.so + k * i.step);
-                xr[k] = ld_tile<IO, V>(x.rsrc, x.at(pt + k < a.N), x.so + k * x.step);
+                rr[k] = ld_tile<IO, V, kPolicy>(r.rsrc, r.at(pt + k < a.N), r.so + k * r.step);
+                ir[k] = ld_tile<IO, V, kPolicy>(i.rsrc, i.at(pt + k < a.N), i.so + k * i.step);
+                xr[k] = ld_tile<IO, V, kPolicy>(x.rsrc, x.at(pt + k < a.N), x.so + k * x.step);
             }
         }
     }
@@ -596,7 +601,7 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
         for (int k = 0; k < T; ++k) {
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = fmaf(av[k][v], h[v], bv[k][v]);
-            st_tile<IO, V>(y.rsrc, y.at(pt < a.N), y.so + k * y.step, h);
+            st_tile<IO, V, kPolicy>(y.rsrc, y.at(pt < a.N), y.so + k * y.step, h);
         }
     } else {
 #pragma unroll
@@ -604,7 +609,7 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
             if (starts >> k & 1) seq_value(a, a.h0, rows[wave][wt + k], c0, h);
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = fmaf(av[k][v], h[v], bv[k][v]);
-            st_tile<IO, V>(y.rsrc, y.at(pt + k < a.N), y.so + k * y.step, h);
+            st_tile<IO, V, kPolicy>(y.rsrc, y.at(pt + k < a.N), y.so + k * y.step, h);
             if (a.h_last && live && (ends >> k & 1)) {
                 float* dst = a.h_last + static_cast<int64_t>(rows[wave][wt + k]) * a.D + c0;
 #pragma unroll
@@ -618,7 +623,7 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
 // Backward pass: a tile of kGatedBwdTile positions x 64 channels; workgroups take the tiles from the
 // last to the first. With e the gradient that comes in behind a position (dh_last behind a sequence's
 // last one), d = dy + e is the state's and a d goes on to the position before.
-template <typename IO, int V, bool kChain>
+template <typename IO, int V, bool kChain, int kPolicy>
 __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_bwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedBwdTile / TG;
     __shared__ ChainLds lds;
@@ -651,18 +656,18 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
         if (p0 + kGatedBwdTile <= a.N) {
 #pragma unroll
             for (int k = 0; k < T; ++k) {
-                rr[k] = ld_tile<IO, V>(r.rsrc, r.vo, r.so + k * r.step);
-                ir[k] = ld_tile<IO, V>(i.rsrc, i.vo, i.so + k * i.step);
-                xr[k] = ld_tile<IO, V>(x.rsrc, x.vo, x.so + k * x.step);
-                gr[k] = ld_tile<IO, V>(g.rsrc, g.vo, g.so + k * g.step);
+                rr[k] = ld_tile<IO, V, kPolicy>(r.rsrc, r.vo, r.so + k * r.step);
+                ir[k] = ld_tile<IO, V, kPolicy>(i.rsrc, i.vo, i.so + k * i.step);
+                xr[k] = ld_tile<IO, V, kPolicy>(x.rsrc, x.vo, x.so + k * x.step);
+                gr[k] = ld_tile<IO, V, kPolicy>(g.rsrc, g.vo, g.so + k * g.step);
             }
         } else {
 #pragma unroll
             for (int k = 0; k < T; ++k) {
-                rr[k] = ld_tile<IO, V>(r.rsrc, r.at(pt + k < a.N), r.so + k * r.step);
-                ir[k] = ld_tile<IO, V>(i.rsrc, i.at(pt + k < a.N), i.so + k * i.step);
-                xr[k] = ld_tile<IO, V>(x.rsrc, x.at(pt + k < a.N), x.so + k * x.step);
-                gr[k] = ld_tile<IO, V>(g.rsrc, g.at(pt + k < a.N), g.so + k * g.step);
+                rr[k] = ld_tile<IO, V, kPolicy>(r.rsrc, r.at(pt + k < a.N), r.so + k * r.step);
+                ir[k] = ld_tile<IO, V, kPolicy>(i.rsrc, i.at(pt + k < a.N), i.so + k * i.step);
+                xr[k] = ld_tile<IO, V, kPolicy>(x.rsrc, x.at(pt + k < a.N), x.so + k * x.step);
+                gr[k] = ld_tile<IO, V, kPolicy>(g.rsrc, g.at(pt + k < a.N), g.so + k * g.step);
             }
         }
     }
@@ -835,9 +840,9 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
             sum[v] += w;
             d[v] = av[k][v] * del;
         }
-        st_tile<IO, V>(dx.rsrc, dx.at(in), dx.so + k * dx.step, ox);
-        st_tile<IO, V>(dr.rsrc, dr.at(in), dr.so + k * dr.step, orr);
-        st_tile<IO, V>(di.rsrc, di.at(in), di.so + k * di.step, oi);
+        st_tile<IO, V, kPolicy>(dx.rsrc, dx.at(in), dx.so + k * dx.step, ox);
+        st_tile<IO, V, kPolicy>(dr.rsrc, dr.at(in), dr.so + k * dr.step, orr);
+        st_tile<IO, V, kPolicy>(di.rsrc, di.at(in), di.so + k * di.step, oi);
     };
     if (!cuts) {
 #pragma unroll
@@ -993,32 +998,56 @@ bool record(const vimscan_launch* l, int k) {
 // per thread and channel outside the element loops: maps, waits, carries); measured 40 us with either at
 // 128 x 197 x 768 bf16 forward, 89 us against 136 us backward.
 constexpr int kVec = 2;
-bool by_vec(const vimscan_gated* g, int64_t d, size_t e, const void* const* more, const int64_t* lds, int n) {
-    auto ok = [&](const void* p, int64_t ld) {
-        return !p || (reinterpret_cast<uintptr_t>(p) % (kVec * e) == 0 && ld % kVec == 0);
-    };
-    bool r = d % kVec == 0 && ok(g->x, g->ld_x) && ok(g->r, g->ld_r) && ok(g->i, g->ld_i);
-    for (int k = 0; k < n; ++k) r = r && ok(more[k], lds[k]);
-    return r;
+
+// Rows of one tensor, as far as the choice of a kernel goes.
+struct RowsOf {
+    const void* p;
+    int64_t ld;
+};
+// Every tensor's rows start at multiples of bytes.
+template <size_t N>
+bool rows_at(const RowsOf (&rows)[N], size_t e, size_t bytes) {
+    for (const RowsOf& r : rows)
+        if (r.p && (reinterpret_cast<uintptr_t>(r.p) % bytes != 0 || static_cast<size_t>(r.ld) * e % bytes != 0)) return false;
+    return true;
 }
 
-template <typename IO, int V, int TILE>
-void launch_fwd_tile(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.wgs));
-    if (p.chain) hipLaunchKernelGGL((k_gated_fwd<IO, V, TILE, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_gated_fwd<IO, V, TILE, false>), grid, dim3(256), 0, s, a);
-}
-template <typename IO, int V>
+template <typename IO, int V, int TILE, int kPolicy>
 void launch_fwd(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
-    if (p.tile == kGatedFwdTile) launch_fwd_tile<IO, V, kGatedFwdTile>(a, p, s);
-    else launch_fwd_tile<IO, V, kGatedFwdTileSmall>(a, p, s);
+    const dim3 grid(static_cast<unsigned>(p.wgs));
+    if (p.chain) hipLaunchKernelGGL((k_gated_fwd<IO, V, TILE, true, kPolicy>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_gated_fwd<IO, V, TILE, false, kPolicy>), grid, dim3(256), 0, s, a);
+}
+template <typename IO>
+void launch_fwd_any(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
+    constexpr size_t e = sizeof(IoElem<IO>);
+    const RowsOf rows[] = {{a.x, a.ld_x}, {a.r, a.ld_r}, {a.i, a.ld_i}, {a.y, a.D}};
+    const bool vec = a.D % kVec == 0 && rows_at(rows, e, kVec * e), big = p.tile == kGatedFwdTile;
+    // small calls do not gain from kOnce: their inputs are often in the caches still (8 x 1025 x 768 bf16 15.7
+    // us, with it 16.7; 256 x 51 x 1536, 7,000 workgroups, 46.4 and 41.6)
+    const bool once = rows_at(rows, e, 128) && (big || p.wgs >= 2048);
+    if (vec && big && once) launch_fwd<IO, kVec, kGatedFwdTile, kOnce>(a, p, s);
+    else if (vec && once) launch_fwd<IO, kVec, kGatedFwdTileSmall, kOnce>(a, p, s);
+    else if (vec && big) launch_fwd<IO, kVec, kGatedFwdTile, kPlain>(a, p, s);
+    else if (vec) launch_fwd<IO, kVec, kGatedFwdTileSmall, kPlain>(a, p, s);
+    else if (big) launch_fwd<IO, 1, kGatedFwdTile, kPlain>(a, p, s);
+    else launch_fwd<IO, 1, kGatedFwdTileSmall, kPlain>(a, p, s);
 }
 
-template <typename IO, int V>
+template <typename IO, int V, int kPolicy>
 void launch_bwd(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(p.wgs));
-    if (p.chain) hipLaunchKernelGGL((k_gated_bwd<IO, V, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_gated_bwd<IO, V, false>), grid, dim3(256), 0, s, a);
+    if (p.chain) hipLaunchKernelGGL((k_gated_bwd<IO, V, true, kPolicy>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_gated_bwd<IO, V, false, kPolicy>), grid, dim3(256), 0, s, a);
+}
+template <typename IO>
+void launch_bwd_any(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
+    constexpr size_t e = sizeof(IoElem<IO>);
+    const RowsOf rows[] = {{a.x, a.ld_x},   {a.r, a.ld_r},   {a.i, a.ld_i},  {a.dy, a.ld_dy},
+                           {a.dx, a.ld_dx}, {a.dr, a.ld_dr}, {a.di, a.ld_di}};
+    if (a.D % kVec != 0 || !rows_at(rows, e, kVec * e)) launch_bwd<IO, 1, kPlain>(a, p, s);
+    else if (rows_at(rows, e, 128)) launch_bwd<IO, kVec, kOnce>(a, p, s);
+    else launch_bwd<IO, kVec, kPlain>(a, p, s);
 }
 
 }  // namespace
@@ -1052,16 +1081,8 @@ int vimscan_gated_fwd(const vimscan_gated* g, int64_t seg_len, void* y, float* h
     a.states = states;
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
-    const void* out[] = {y};
-    const int64_t out_ld[] = {launch->d_inner};
-    const bool f32 = launch->io_dtype == VIMSCAN_F32;
-    if (by_vec(g, launch->d_inner, f32 ? 4 : 2, out, out_ld, 1)) {
-        if (f32) launch_fwd<float, kVec>(a, p, s);
-        else launch_fwd<Bf16, kVec>(a, p, s);
-    } else {
-        if (f32) launch_fwd<float, 1>(a, p, s);
-        else launch_fwd<Bf16, 1>(a, p, s);
-    }
+    if (launch->io_dtype == VIMSCAN_F32) launch_fwd_any<float>(a, p, s);
+    else launch_fwd_any<Bf16>(a, p, s);
     if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
     return VIMSCAN_OK;
 }
@@ -1091,16 +1112,8 @@ int vimscan_gated_bwd(const vimscan_gated* g, int64_t seg_len, const vimscan_gat
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
     if (p.wgs > 0) {
-        const void* more[] = {grad->dy, grad->dx, grad->dr, grad->di};
-        const int64_t lds[] = {grad->ld_dy, grad->ld_dx, grad->ld_dr, grad->ld_di};
-        const bool f32 = launch->io_dtype == VIMSCAN_F32;
-        if (by_vec(g, launch->d_inner, f32 ? 4 : 2, more, lds, 4)) {
-            if (f32) launch_bwd<float, kVec>(a, p, s);
-            else launch_bwd<Bf16, kVec>(a, p, s);
-        } else {
-            if (f32) launch_bwd<float, 1>(a, p, s);
-            else launch_bwd<Bf16, 1>(a, p, s);
-        }
+        if (launch->io_dtype == VIMSCAN_F32) launch_bwd_any<float>(a, p, s);
+        else launch_bwd_any<Bf16>(a, p, s);
     }
     if (a.dlam) {
         const unsigned blocks = static_cast<unsigned>((launch->d_inner + kColumns - 1) / kColumns);
@@ -1134,9 +1147,9 @@ int vimscan_gated_step(const vimscan_gated* g, float* state, int64_t nslots, con
     a.batch = static_cast<int32_t>(launch->batch);
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     const bool f32 = launch->io_dtype == VIMSCAN_F32;
-    const void* out[] = {y};
-    const int64_t out_ld[] = {launch->d_inner};
-    const bool vec = by_vec(g, launch->d_inner, f32 ? 4 : 2, out, out_ld, 1) &&
+    const size_t e = f32 ? 4 : 2;
+    const RowsOf rows[] = {{a.x, a.ld_x}, {a.r, a.ld_r}, {a.i, a.ld_i}, {y, launch->d_inner}};
+    const bool vec = launch->d_inner % kVec == 0 && rows_at(rows, e, kVec * e) &&
                      reinterpret_cast<uintptr_t>(g->lam) % (4 * kVec) == 0 &&
                      reinterpret_cast<uintptr_t>(state) % (4 * kVec) == 0;
     a.per_row = static_cast<int32_t>(vec ? launch->d_inner / kVec : launch->d_inner);
