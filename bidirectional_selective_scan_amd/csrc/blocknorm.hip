@@ -86,6 +86,7 @@ __device__ __forceinline__ void row_sum(float* u, float* v, float2 (*lds)[W], in
 }
 
 __device__ __forceinline__ float sigmoid(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 
 // How a row is spread: over L lanes of a wave (W = 1) or W whole waves (L = 64), each lane NV vectors of V
 // channels. A workgroup of 256 threads works on several rows at once where they are narrow; wide rows
@@ -169,7 +170,11 @@ __device__ __forceinline__ void ld_weight(const float* w, int D, float (&o)[S::N
         for (int v = 0; v < V; ++v) o[k][v] = w ? r[k].get(v) : 1.0f;
 }
 
-// Forward: a row stays in registers from its one read to its one write.
+// Forward: v = x (silu(z)), q = v rsq(mean v^2 + eps) w_post, s = residual + gamma q, n = s rsq(mean s^2 +
+// eps) w_pre. Memory bounds it: a row stays in registers from its one read to its one write, and the
+// workgroups walk the rows so that the weights are read once per workgroup and not per row. Measured: 25216
+// x 768 bf16 with fp32 residuals 50 us (271 MB, 5.4 TB/s), 4099 x 8192 all bf16 49 us (269 MB, 5.5 TB/s),
+// 13056 x 1531 fp32 48 us with a gate and no pre-norm (5.0 TB/s); a copy of 256 MiB reaches 5.4 TB/s.
 template <typename IO, typename RES, typename S>
 __global__ __launch_bounds__(S::kThreads) void k_norm_fwd(NormArgs a) {
     constexpr int NV = S::NV, L = S::L, W = S::W, V = S::V;
@@ -192,68 +197,73 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_fwd(NormArgs a) {
         settle<RES, S>(a.D, r);
         float s[NV][V];
         float ss = 0.0f, none = 0.0f;
+        // (the stages that are there or not are chosen outside the element loops: one branch a row)
+        auto all = [](auto&& f) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[k][v] = x[k].get(v);
-                if (a.z && !a.after) {
-                    const float zv = z[k].get(v);
-                    s[k][v] *= zv * sigmoid(zv);
-                }
-                ss = fmaf(s[k][v], s[k][v], ss);
-            }
+                for (int v = 0; v < V; ++v) f(k, v);
+        };
+        all([&](int k, int v) { s[k][v] = x[k].get(v); });
+        if (a.z && !a.after) all([&](int k, int v) { s[k][v] *= silu(z[k].get(v)); });
+        all([&](int k, int v) { ss = fmaf(s[k][v], s[k][v], ss); });
         float rho = 1.0f;
         if (a.w_post) {
             row_sum<L, W>(&ss, &none, lds, slot, wave);
             rho = fast_rsq(fmaf(ss, a.inv_d, a.eps));
         }
         ss = none = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[k][v] *= rho * wp[k][v];
-                if (a.after) {
-                    const float zv = z[k].get(v);
-                    s[k][v] *= zv * sigmoid(zv);
-                }
-                s[k][v] = fmaf(s[k][v], ga[k][v], r[k].get(v));
-                ss = fmaf(s[k][v], s[k][v], ss);
-            }
+        all([&](int k, int v) { s[k][v] *= rho * wp[k][v]; });
+        if (a.after) all([&](int k, int v) { s[k][v] *= silu(z[k].get(v)); });
+        all([&](int k, int v) {
+            s[k][v] = fmaf(s[k][v], ga[k][v], r[k].get(v));
+            ss = fmaf(s[k][v], s[k][v], ss);
+        });
         if (a.sum) st_row<RES, S>(a.sum, row * a.D, a.D, s);
         if (!a.w_pre) continue;
         row_sum<L, W>(&ss, &none, lds, slot, wave);
         rho = fast_rsq(fmaf(ss, a.inv_d, a.eps));
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[k][v] *= rho * wn[k][v];
+        all([&](int k, int v) { s[k][v] *= rho * wn[k][v]; });
         st_row<IO, S>(a.n, row * a.D, a.D, s);
     }
 }
 
-// Backward: the row's stages again from its inputs, then the gradients against them; the weights'
-// gradients of a wave's rows stay in registers, are added up over the workgroup's waves at the end and
-// left for k_norm_cols.
+// Backward: the row's stages again from its inputs (reading them costs less than saved statistics and
+// intermediates would), then the gradients against them. With g = dn w_pre: ds' = dsum + rho2 g - s rho2^3
+// mean(g s); the post-norm's likewise; the gate's through silu' = sg (1 + z (1 - sg)). Memory bounds it: 25216
+// x 768 bf16 82 us (426 MB, 5.2 TB/s), 13056 x 1531 fp32 83 us (400 MB, 4.8 TB/s). The weights' gradients
+// of a thread's channels stay with the thread over all its rows, are added up over the workgroup's rows at
+// the end and left for k_norm_cols: no atomics, the same bits every time. Past 4096 channels a thread's registers
+// are short (128 with 16 waves); LDS holds the weights' gradients up to 8192 channels: 4099 x 8192 bf16 173
+// us against 289 with spilled registers. Wider rows spill (1000 x 16384 bf16: 410 us).
 template <typename IO, typename RES, typename S>
 __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
     constexpr int NV = S::NV, L = S::L, W = S::W, V = S::V;
     __shared__ float2 lds[2][W];
     const int wave = S::wave();
-    // (a workgroup of 1024 threads has 128 registers a thread: there the weights are read again per row)
-    constexpr bool kKeep = W < 16;
+    // (a workgroup of 1024 threads has 128 registers a thread: there the weights are read again per stage)
+    constexpr bool kKeep = W < 16 || NV * V < 8;
     float wp[NV][V], ga[NV][V], wn[NV][V];
     if constexpr (kKeep) {
         ld_weight<S>(a.w_post, a.D, wp);
         ld_weight<S>(a.gamma, a.D, ga);
         ld_weight<S>(a.w_pre, a.D, wn);
     }
+    // the weights' gradients: in registers, or each thread's in LDS where those are short and LDS holds them
+    constexpr bool kInLds = !kKeep && S::kWidth <= 8192;
     float dwp[NV][V], dga[NV][V], dwn[NV][V];
+    __shared__ __align__(16) float sums[kInLds ? 3 : 1][kInLds ? NV : 1][kInLds ? S::kThreads : 1][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int v = 0; v < V; ++v) dwp[k][v] = dga[k][v] = dwn[k][v] = 0.0f;
+        for (int v = 0; v < V; ++v) {
+            dwp[k][v] = dga[k][v] = dwn[k][v] = 0.0f;
+            if constexpr (kInLds) sums[0][k][threadIdx.x][v] = sums[1][k][threadIdx.x][v] = sums[2][k][threadIdx.x][v] = 0.0f;
+        }
+    auto add = [&](int which, float (&g)[NV][V], int k, int v, float a, float b) {
+        if constexpr (kInLds) sums[which][k][threadIdx.x][v] = fmaf(a, b, sums[which][k][threadIdx.x][v]);
+        else g[k][v] = fmaf(a, b, g[k][v]);
+    };
     int slot = 0;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * S::kRows + S::row(); row < a.rows;
          row += static_cast<int64_t>(gridDim.x) * S::kRows) {
@@ -269,98 +279,115 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
         settle<RES, S>(a.D, r);
         settle<IO, S>(a.D, dn);
         settle<RES, S>(a.D, ds);
-        if constexpr (!kKeep) {
-            ld_weight<S>(a.w_post, a.D, wp);
-            ld_weight<S>(a.gamma, a.D, ga);
-            ld_weight<S>(a.w_pre, a.D, wn);
-        }
+        auto read_first = [&] {   // the weights of the stages up to the sum
+            if constexpr (!kKeep) {
+                ld_weight<S>(a.w_post, a.D, wp);
+                ld_weight<S>(a.gamma, a.D, ga);
+            }
+        };
+        auto read_last = [&] {    // that of the pre-norm
+            if constexpr (!kKeep) ld_weight<S>(a.w_pre, a.D, wn);
+        };
         // val: the post-norm's input; s: the sum
         float val[NV][V], s[NV][V];
         float u = 0.0f, t = 0.0f;
+        auto all = [](auto&& f) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                val[k][v] = x[k].get(v);
-                if (a.z && !a.after) {
-                    const float zv = z[k].get(v);
-                    val[k][v] *= zv * sigmoid(zv);
-                }
-                u = fmaf(val[k][v], val[k][v], u);
-            }
+                for (int v = 0; v < V; ++v) f(k, v);
+        };
+        all([&](int k, int v) { val[k][v] = x[k].get(v); });
+        if (a.z && !a.after) all([&](int k, int v) { val[k][v] *= silu(z[k].get(v)); });
+        all([&](int k, int v) { u = fmaf(val[k][v], val[k][v], u); });
         float rho1 = 1.0f, rho2 = 0.0f, k2 = 0.0f;
         if (a.w_post) {
             row_sum<L, W>(&u, &t, lds, slot, wave);
             rho1 = fast_rsq(fmaf(u, a.inv_d, a.eps));
         }
         u = t = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float p = val[k][v] * rho1 * wp[k][v];
-                if (a.after) {
-                    const float zv = z[k].get(v);
-                    p *= zv * sigmoid(zv);
-                }
-                s[k][v] = fmaf(p, ga[k][v], r[k].get(v));
+        read_first();
+        all([&](int k, int v) { s[k][v] = val[k][v] * rho1 * wp[k][v]; });
+        if (a.after) all([&](int k, int v) { s[k][v] *= silu(z[k].get(v)); });
+        all([&](int k, int v) { s[k][v] = fmaf(s[k][v], ga[k][v], r[k].get(v)); });
+        if (a.dn) {
+            read_last();
+            all([&](int k, int v) {
                 u = fmaf(s[k][v], s[k][v], u);
                 t = fmaf(dn[k].get(v) * wn[k][v], s[k][v], t);
-            }
-        if (a.dn) {
+            });
             row_sum<L, W>(&u, &t, lds, slot, wave);
             rho2 = fast_rsq(fmaf(u, a.inv_d, a.eps));
             k2 = t * a.inv_d * rho2 * rho2 * rho2;
+            read_last();
+            // from here s is the gradient of the sum
+            all([&](int k, int v) {
+                const float g = dn[k].get(v) * rho2;
+                add(2, dwn, k, v, g, s[k][v]);
+                s[k][v] = ds[k].get(v) + fmaf(g, wn[k][v], -s[k][v] * k2);
+            });
+        } else {
+            all([&](int k, int v) { s[k][v] = ds[k].get(v); });
         }
-        // from here s is the gradient of the sum
         u = t = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float g = dn[k].get(v);
-                dwn[k][v] = fmaf(g, s[k][v] * rho2, dwn[k][v]);
-                s[k][v] = ds[k].get(v) + fmaf(rho2 * g, wn[k][v], -s[k][v] * k2);
-                const float q = val[k][v] * rho1 * wp[k][v], dp = s[k][v] * ga[k][v];
-                float p = q, dq = dp;
-                if (a.after) {
-                    const float zv = z[k].get(v), gate = zv * sigmoid(zv);
-                    p *= gate;
-                    dq *= gate;
-                }
-                dga[k][v] = fmaf(p, s[k][v], dga[k][v]);
-                dwp[k][v] = fmaf(dq, val[k][v] * rho1, dwp[k][v]);
+        read_first();
+        // gradients of gamma and w_post; dq: of the post-norm's output
+        if (a.after) {
+            all([&](int k, int v) {
+                const float gs = silu(z[k].get(v)) * s[k][v], vr = val[k][v] * rho1;
+                const float dq = gs * ga[k][v];
+                add(1, dga, k, v, vr * wp[k][v], gs);
+                add(0, dwp, k, v, dq, vr);
                 u = fmaf(dq * wp[k][v], val[k][v], u);
-            }
+            });
+        } else {
+            all([&](int k, int v) {
+                const float vr = val[k][v] * rho1, dq = s[k][v] * ga[k][v];
+                add(1, dga, k, v, vr * wp[k][v], s[k][v]);
+                add(0, dwp, k, v, dq, vr);
+                u = fmaf(dq * wp[k][v], val[k][v], u);
+            });
+        }
         if (a.dres) st_row<RES, S>(a.dres, row * a.D, a.D, s);
         float k1 = 0.0f;
         if (a.w_post) {
             row_sum<L, W>(&u, &t, lds, slot, wave);
             k1 = u * a.inv_d * rho1 * rho1 * rho1;
         }
+        read_first();
+        // gradient of the post-norm's input: rho1 dq w_post - val k1 (dq itself without w_post)
         float dz[NV][V];
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float dp = s[k][v] * ga[k][v];
-                float gate = 1.0f, slope = 0.0f;
-                if (a.z) {
-                    const float zv = z[k].get(v), sg = sigmoid(zv);
-                    gate = zv * sg;
-                    slope = sg * fmaf(zv, 1.0f - sg, 1.0f);
-                }
-                const float dq = a.after ? dp * gate : dp;
-                const float dv = fmaf(rho1 * dq, wp[k][v], -val[k][v] * k1);
-                const float q = val[k][v] * rho1 * wp[k][v];
-                dz[k][v] = (a.after ? dp * q : dv * x[k].get(v)) * slope;
-                s[k][v] = a.after ? dv : dv * gate;
-            }
+        if (!a.z) {
+            all([&](int k, int v) { s[k][v] = fmaf(rho1 * s[k][v] * ga[k][v], wp[k][v], -val[k][v] * k1); });
+        } else if (a.after) {
+            all([&](int k, int v) {
+                const float zv = z[k].get(v), sg = sigmoid(zv), dp = s[k][v] * ga[k][v], rw = rho1 * wp[k][v];
+                dz[k][v] = dp * (val[k][v] * rw) * (sg * fmaf(zv, 1.0f - sg, 1.0f));
+                s[k][v] = fmaf(dp * (zv * sg), rw, -val[k][v] * k1);
+            });
+        } else {
+            all([&](int k, int v) {
+                const float zv = z[k].get(v), sg = sigmoid(zv);
+                const float dv = fmaf(rho1 * s[k][v] * ga[k][v], wp[k][v], -val[k][v] * k1);
+                dz[k][v] = dv * x[k].get(v) * (sg * fmaf(zv, 1.0f - sg, 1.0f));
+                s[k][v] = dv * (zv * sg);
+            });
+        }
         if (a.dx) st_row<IO, S>(a.dx, row * a.ld_dx, a.D, s);
         if (a.dz) st_row<IO, S>(a.dz, row * a.ld_dz, a.D, dz);
     }
     if (!a.part) return;
     float* part = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.D;
+    if constexpr (kInLds) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                dwp[k][v] = sums[0][k][threadIdx.x][v];
+                dga[k][v] = sums[1][k][threadIdx.x][v];
+                dwn[k][v] = sums[2][k][threadIdx.x][v];
+            }
+    }
     if constexpr (S::kRows == 1) {
         st_row<float, S>(part, 0, a.D, dwp);
         st_row<float, S>(part, a.D, a.D, dga);
@@ -404,7 +431,8 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
     }
 }
 
-// The weight gradients: the workgroups' partial sums.
+// The weight gradients: the workgroups' partial sums, in a fixed order. Latency bounds it: 4.7 us for 512
+// partials of 3 x 768.
 __global__ __launch_bounds__(1024) void k_norm_cols(NormArgs a, int parts) {
     float* dst = a.dw[blockIdx.y];
     if (!dst) return;
@@ -445,27 +473,27 @@ void launch_vectors(const NormArgs& a, const NormPlan& p, bool back, hipStream_t
     using C4 = Spread<4, 64, 1, 4, kWhole>;
     using D2 = Spread<2, 64, 4, 4, kWhole>;
     using D4 = Spread<4, 64, 4, 4, kWhole>;
-    using E2 = Spread<2, 64, 8, 4, kWhole>;
     using E4 = Spread<4, 64, 8, 4, kWhole>;
     using F2 = Spread<2, 64, 16, 4, kWhole>;
     using F4 = Spread<4, 64, 16, 4, kWhole>;
     using F8 = Spread<8, 64, 16, 4, kWhole>;
     // forward fewer waves with more of a row each; backward, where a channel takes three times the
-    // registers, more waves from 2048 channels on (4099 x 8192 bf16: 342 us with 16 waves, 577 with 8)
+    // registers, more waves from 1024 channels on (13056 x 1536 bf16: 86 us with 8 waves, 93 with 4; 4099 x
+    // 8192: 342 us with 16 waves, 577 with 8, and 173 with the weights' gradients in LDS)
     if (!back) launch_first<IO, RES, false, A, B, C, C2, C3, C4, D2, D4, E4, F4, F8>(a, p, s);
-    else launch_first<IO, RES, true, A, B, C, C2, C3, C4, D2, E2, F2, F4, F8>(a, p, s);
+    else launch_first<IO, RES, true, A, B, C, C2, C3, C4, Spread<1, 64, 8, 4, kWhole>, Spread<1, 64, 16, 4, kWhole>, F2, F4, F8>(a, p, s);
 }
 template <bool kBack>
 void launch_singles(const NormArgs& a, const NormPlan& p, hipStream_t s) {
     launch_first<float, float, kBack, Spread<4, 16, 1, 1, true>, Spread<4, 32, 1, 1, true>, Spread<4, 64, 1, 1, true>,
-                 Spread<8, 64, 1, 1, true>, Spread<4, 64, 4, 1, true>, Spread<8, 64, 4, 1, true>,
+                 Spread<8, 64, 1, 1, true>, Spread<4, 64, 4, 1, true>, Spread<4, 64, 8, 1, true>,
                  Spread<8, 64, 8, 1, true>, Spread<8, 64, 16, 1, true>, Spread<16, 64, 16, 1, true>,
                  Spread<32, 64, 16, 1, true>>(a, p, s);
 }
 
 // Widths that are no multiple of four: in bf16 vectors at any alignment are still twice as fast as single
-// channels (13056 x 1531: 80 us against 180 forward, 130 against 253 backward), in fp32, where a single
-// channel is a full access, they are slower (108 against 77 us, 163 against 123).
+// channels (13056 x 1531: 76 us against 180 forward, 116 against 253 backward), in fp32, where a single
+// channel is a full access, they are slower (108 against 74 us, 163 against 110).
 void launch_typed(const NormArgs& a, const NormPlan& p, int io, bool back, hipStream_t s) {
     const bool whole = a.D % 4 == 0;
     if (io == VIMSCAN_F32) {

@@ -258,8 +258,8 @@ def test_workspace_of_the_hand_over(shape, backward):
 
 SPREADS_VECTOR_FWD = [(1, 16, 1), (1, 32, 1), (1, 64, 1), (2, 64, 1), (3, 64, 1), (4, 64, 1), (2, 64, 4), (4, 64, 4), (4, 64, 8),
                       (4, 64, 16), (8, 64, 16)]
-SPREADS_VECTOR_BWD = SPREADS_VECTOR_FWD[:7] + [(2, 64, 8), (2, 64, 16), (4, 64, 16), (8, 64, 16)]
-SPREADS_SINGLE = [(4, 16, 1), (4, 32, 1), (4, 64, 1), (8, 64, 1), (4, 64, 4), (8, 64, 4), (8, 64, 8), (8, 64, 16), (16, 64, 16),
+SPREADS_VECTOR_BWD = SPREADS_VECTOR_FWD[:6] + [(1, 64, 8), (1, 64, 16), (2, 64, 16), (4, 64, 16), (8, 64, 16)]
+SPREADS_SINGLE = [(4, 16, 1), (4, 32, 1), (4, 64, 1), (8, 64, 1), (4, 64, 4), (4, 64, 8), (8, 64, 8), (8, 64, 16), (16, 64, 16),
                   (32, 64, 16)]
 
 
@@ -289,6 +289,7 @@ def test_every_width_is_covered_once(spreads, v):
         assert rows >= 1
         # LDS of the partial gradients (several rows) and of the sums
         assert rows == 1 or 3 * 4 * nv * v * lanes * 4 <= 64 * 1024
+        assert waves < 16 or nv * v < 8 or nv * lanes * waves * v > 8192 or 3 * nv * 64 * waves * v * 4 <= 128 * 1024
 
 
 @pytest.mark.parametrize("rows,d", [(1, 1), (3, 768), (25216, 768), (4099, 8192), (30000, 32), (5, 32768)])
