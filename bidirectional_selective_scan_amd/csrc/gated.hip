@@ -278,14 +278,19 @@ __device__ __forceinline__ void st_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, u
 // The product in which a factor 0 gives 0 whatever the other one is.
 extern "C" __device__ float vimscan_mul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
 
-// The map h -> A h + H of some consecutive positions; A = 0 where a sequence starts among them.
+// The map h -> A h + H of some consecutive positions; A = 0 where a sequence starts among them, and only
+// there: a product of transitions that underflows is held at the least number above 0, so that NaN and
+// infinity stay in the rest of their sequence (a finite state gets at most 5e-7 from it).
+constexpr float kLeast = 0x1p-149f;
 struct Map {
     float A, H;
     __device__ __forceinline__ float operator()(float h) const { return vimscan_mul_legacy(A, h) + H; }
 };
 __device__ __forceinline__ Map identity() { return {1.0f, 0.0f}; }
 // f, then g.
-__device__ __forceinline__ Map then(const Map& f, const Map& g) { return {vimscan_mul_legacy(f.A, g.A), g(f.H)}; }
+__device__ __forceinline__ Map then(const Map& f, const Map& g) {
+    return {fmaxf(vimscan_mul_legacy(f.A, g.A), fminf(fminf(f.A, g.A), kLeast)), g(f.H)};
+}
 __device__ __forceinline__ Map pick(bool c, const Map& f, const Map& g) { return {c ? f.A : g.A, c ? f.H : g.H}; }
 
 // Composes the maps of a wave's position groups (64 / CL of them, CL lanes each): total of the wave,
@@ -569,7 +574,7 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
 #pragma unroll
         for (int k = 1; k < T; ++k) f[v].A *= av[k][v];
         f[v].H = h[v];
-        f[v].A = starts ? 0.0f : f[v].A;
+        f[v].A = starts ? 0.0f : fmaxf(f[v].A, kLeast);
         Map total;
         scan_rows<CL, false>(f[v], lane, &total, &before[v]);
         if (lane < CL) lds.wave[wave][lane * V + v] = make_float2(total.A, total.H);
@@ -755,8 +760,8 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
         f[v].A = av[0][v];
 #pragma unroll
         for (int k = 1; k < T; ++k) f[v].A *= av[k][v];
-        e[v].A = ends ? 0.0f : f[v].A;
-        f[v].A = starts ? 0.0f : f[v].A;
+        e[v].A = ends ? 0.0f : fmaxf(f[v].A, kLeast);
+        f[v].A = starts ? 0.0f : fmaxf(f[v].A, kLeast);
     }
     Map fb[V], eb[V];
 #pragma unroll

@@ -172,6 +172,34 @@ def test_nothing_crosses_a_sequence_boundary(reverse):
     assert bool(fwd1.y[0, offsets[2] - 1 if not reverse else offsets[1]].isnan().all())
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [33, 64])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_non_finite_values_stay_in_their_sequence(io, d, reverse):
+    """A NaN input makes every later output NaN, a NaN gradient every earlier one, an infinite initial state every
+    output: also where the product of the decays between them is far below the smallest number."""
+    offsets = [0, 50, 50 + 3000, 50 + 3000 + 70]
+    p = Problem(1, offsets[-1], d, io, offsets=offsets, reverse=reverse, seed=21)
+    p.lam[:] = 1.0   # decays of about e^-5 a token
+    order = range(offsets[2] - 1, offsets[1] - 1, -1) if reverse else range(offsets[1], offsets[2])
+    tokens = torch.tensor(list(order), device=DEV)
+    p.x[0, tokens[700], 3] = float("nan")
+    p.dy[0, tokens[2200], 5] = float("nan")
+    p.h0[1, 7] = float("inf")
+    fwd, bwd = p.run()
+    y, dx = fwd.y[0], bwd.dx[0]
+    lost = torch.zeros_like(y, dtype=torch.bool)
+    lost[tokens[700:], 3] = True
+    lost[tokens, 7] = True
+    assert torch.equal(~y.isfinite(), lost)
+    assert torch.equal(~fwd.h_last.isfinite().cpu(), torch.tensor([[q == 1 and c in (3, 7) for c in range(d)] for q in range(3)]))
+    lost[:] = False
+    lost[tokens[:2201], 5] = True
+    lost[tokens[700], 3] = False   # dx does not depend on x
+    assert torch.equal(dx.isnan(), lost)
+    assert bool(bwd.dh0[1, 5].isnan()) and bool(bwd.dh0[[0, 2]].isfinite().all())
+
+
 def test_extreme_gates_and_rates():
     """Gates at both ends, infinite among them, and decay rates from 0 (lam -> -inf) to very fast."""
     p = Problem(2, 90, 24, "f32", seed=13)
