@@ -21,7 +21,9 @@
 //    in this order (the same bits on every run); a group's last tile publishes the state it leaves.
 //    Tiles wait only for tiles of lower workgroup ids, and the hardware starts the workgroups of each
 //    XCD in increasing id order: the lowest unfinished id has nothing unfinished to wait for and
-//    nothing of a higher id in its way, so every wait ends. Waits are bounded all the same
+//    nothing of a higher id in its way, so every wait ends. Where several such calls overlap on
+//    different streams this needs one thing more, that no XCD is filled by one of them alone for as
+//    long as the other one waits for a workgroup there. Waits are bounded all the same
 //    (kSpinLimit) and counted (vimscan_wait_timeouts).
 //  * Backward: the same with the positions' gradients walked the other way; the state before every
 //    position is walked again from the states that the forward pass saved at every tile's first

@@ -475,7 +475,8 @@ const char* vimscan_version(void);
  * aggregates of the earlier chunks of their sequence gave up after its bound (about a second);
  * their calls' outputs are unspecified. The hardware starts the workgroups of every XCD in
  * increasing id order, which makes every such wait end (the kernel's own comment gives the
- * argument), so the count stays 0; it exists so that a failure of that premise is visible.
+ * argument; calls of this kind that overlap on several streams also rely on every XCD being
+ * shared between them), so the count stays 0; it exists so that a failure of that premise is visible.
  * Synchronous (a device-to-host copy after the device's queued work). Returns VIMSCAN_OK,
  * VIMSCAN_ERR_NULL or VIMSCAN_ERR_HIP.
  */
