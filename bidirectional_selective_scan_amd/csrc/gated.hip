@@ -340,8 +340,8 @@ struct ChainLds {
     float inc[kGatedBlock];        // the state that the group before left
 };
 
-// A value handed over: two 64-bit words (second words apart, so that a wave's are contiguous), the value and the value xor the dispatch's tag, each stored and
-// loaded on its own (device-coherent, no order between them). A reader takes the value when the two
+// A value handed over: two 64-bit words (second words apart, so that a wave's are contiguous), the value and
+// the value xor the dispatch's tag, each stored and loaded on its own (device-coherent, no order between them). A reader takes the value when the two
 // differ by exactly this dispatch's tag, so words of earlier dispatches, arbitrary bytes and half a
 // value never pass, the memory needs no clearing, and neither side waits for one access before the
 // next: a value costs its reader one trip to memory after it was stored.
