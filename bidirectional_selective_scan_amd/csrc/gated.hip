@@ -706,7 +706,9 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
             const float q = k2[v] * sigmoid2(rr[k].get(v), &ns[v]);
             const float gx = sigmoid2(ir[k].get(v), &ng[v]);
             const float at = fast_exp2(q), m2 = one_minus_sq(q, at), u = q * kLn2;
-            const float im = m2 > 0.0f ? fast_rsq(m2) : 0.0f;  // 1 / m; where m is 0 its terms are taken as 0
+            // 1 / m; where m^2 is below the normal numbers the hardware's rsq takes it for 0 and gives infinity:
+            // m, below 1.1e-19 there, and its terms are taken as 0
+            const float im = m2 >= 0x1p-126f ? fast_rsq(m2) : 0.0f;
             av[k][v] = at;
             mg[k][v] = m2 * im * gx;
             ua[k][v] = u * at;
