@@ -186,9 +186,10 @@ __device__ __forceinline__ float one_minus_sq(float q, float a) {
 // sigmoid(v) = 1 / (1 + e^-v)
 __device__ __forceinline__ float sigmoid(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
 
-// The same and 1 - sigmoid(v) = e / (1 + e), e = e^-v held below 2^126.
+// The same and 1 - sigmoid(v) = e / (1 + e), e = e^-v held below 2^126 (by the minimum that keeps a NaN: both
+// are NaN then).
 __device__ __forceinline__ float sigmoid2(float v, float* ns) {
-    const float e = fast_exp2(fminf(-v * kLog2e, 126.0f));
+    const float e = fast_exp2(__builtin_elementwise_minimum(-v * kLog2e, 126.0f));
     const float s = fast_rcp(1.0f + e);
     *ns = e * s;
     return s;

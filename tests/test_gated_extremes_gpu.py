@@ -1,11 +1,11 @@
-"""The gated recurrence's gradients where a gate is all but closed or closed: every pair of gate and decay
-rate, both io types, one and two channels a lane, against the 64-bit form (block_reference)."""
+"""The gated recurrence's gradients where a gate is all but closed, closed or NaN: every pair of gate and
+decay rate, both io types, one and two channels a lane, against the 64-bit form (block_reference)."""
 import numpy as np
 import pytest
 import torch
 
 import block_reference as ref
-from test_gated_gpu import DEV, Problem, rates
+from test_gated_gpu import DEV, Problem, f64, rates
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,24 @@ def test_every_gate_with_every_rate(io, extra, which):
     for name, t in outputs(fwd, bwd).items():
         assert bool(t.isfinite().all()), name
         ref.check(t, (want[name][0], want[name][1] + slack), io == "bf16" and name in ("y", "dx", "dr", "di"), name)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [33, 64])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("gate", ["r", "i"])
+def test_a_nan_gate_reaches_what_depends_on_it(io, d, reverse, gate):
+    """A NaN in r or i, in a sequence inside one tile and in one of many tiles: exactly the outputs that depend on
+    it by the definition are NaN, at the token, before it, behind it, in dh0 and in dlam."""
+    lens = [20, 0, 700, 33, 5]
+    offsets = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    p = Problem(1, offsets[-1], d, io, offsets=offsets, reverse=reverse, seed=42)
+    for token, channel in ((11, 3), (offsets[2] + 350, 5), (offsets[3] + 32, 7), (offsets[4], 9), (offsets[4] - 33, 9)):
+        getattr(p, gate)[0, token, channel] = float("nan")
+    with np.errstate(all="ignore"):
+        want = p.reference()
+    fwd, bwd = p.run()
+    for name, t in outputs(fwd, bwd).items():
+        got, lost = np.isnan(f64(t)).reshape(want[name][0].shape), np.isnan(want[name][0])
+        assert lost.any() or (gate == "i" and name == "dh0"), name
+        assert (got == lost).all(), (name, np.argwhere(got != lost)[:5])
