@@ -49,11 +49,14 @@ def declare(lib):
     lib.vimscan_gated_bwd.argtypes = [ctypes.POINTER(_Gated), _i64, ctypes.POINTER(_GatedGrad), launch]
     lib.vimscan_gated_step.argtypes = [ctypes.POINTER(_Gated), _vp, _i64, _vp, _vp, _vp, launch]
     lib.vimscan_gated_plan.argtypes = [launch, _i64, ctypes.c_int, _i64, ctypes.c_int, plan]
+    lib.vimscan_gated_wait_reads.argtypes = [ctypes.c_int32]
+    lib.vimscan_gated_alone.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
     lib.vimscan_norm_fwd.argtypes = [ctypes.POINTER(_Norm), _vp, _vp, launch]
     lib.vimscan_norm_bwd.argtypes = [ctypes.POINTER(_Norm), ctypes.POINTER(_NormGrad), launch]
     lib.vimscan_norm_plan.argtypes = [launch, ctypes.c_int, plan]
     for f in (lib.vimscan_gated_fwd, lib.vimscan_gated_bwd, lib.vimscan_gated_step, lib.vimscan_gated_plan,
-              lib.vimscan_norm_fwd, lib.vimscan_norm_bwd, lib.vimscan_norm_plan):
+              lib.vimscan_gated_wait_reads, lib.vimscan_gated_alone, lib.vimscan_norm_fwd, lib.vimscan_norm_bwd,
+              lib.vimscan_norm_plan):
         f.restype = ctypes.c_int
 
 
@@ -346,6 +349,21 @@ def gated_info(batch, seqlen, d_inner, seg_len=0, io_dtype="bf16", nseq=None, ba
     _b._check(_b.load_library().vimscan_gated_plan(ctypes.byref(launch), int(seg_len), int(nseq is not None),
                                                    int(nseq or 0), int(backward), ctypes.byref(plan)))
     return _plan_dict(plan)
+
+
+def gated_wait_reads(reads: int = 4096):
+    """How often a workgroup of a gated recurrence reads a state that is not handed over yet before it goes on
+    alone, from the inputs (vimscan_gated_wait_reads): for the calls queued from now on. The results do not
+    depend on it."""
+    _b._check(_b.load_library().vimscan_gated_wait_reads(int(reads)))
+
+
+def gated_alone() -> int:
+    """Workgroups of gated recurrences on the current device that went on alone since the library was loaded
+    (vimscan_gated_alone). Synchronous."""
+    n = ctypes.c_uint64(0)
+    _b._check(_b.load_library().vimscan_gated_alone(ctypes.byref(n)))
+    return int(n.value)
 
 
 # ------------------------------------------------------------------------------------------

@@ -46,9 +46,6 @@ int check_gated_call(const vimscan_gated* g, const void* y, const float* h_last,
 int check_gated_step(const vimscan_gated* g, const float* state, int64_t nslots, const int32_t* slots_in,
                      const int32_t* slots_out, const void* y, const vimscan_launch* l);
 
-// Waits of the gated recurrence's hand-over that gave up (gated.hip).
-int gated_wait_timeouts(uint64_t* count);
-
 // Plan of a block norm: how a row is spread over lanes.
 struct NormPlan {
     int64_t rows, D;

@@ -19,18 +19,19 @@
 //  * Between tiles: a tile publishes its map before it waits for anything, then composes the maps of
 //    the tiles before it in its group of kGatedGroup onto the state that the group before left, always
 //    in this order (the same bits on every run); a group's last tile publishes the state it leaves.
-//    Tiles wait only for tiles of lower workgroup ids, and the hardware starts the workgroups of each
-//    XCD in increasing id order: the lowest unfinished id has nothing unfinished to wait for and
-//    nothing of a higher id in its way, so every wait ends. Where several such calls overlap on
-//    different streams this needs one thing more, that no XCD is filled by one of them alone for as
-//    long as the other one waits for a workgroup there. Waits are bounded all the same
-//    (kSpinLimit) and counted (vimscan_wait_timeouts).
+//    Tiles wait only for tiles of lower workgroup ids, which the hardware starts first on each XCD, so
+//    that waits are short. None depends on it: a workgroup that has waited for long (kWaitReads; other
+//    work may hold the places that earlier tiles need, another such call on another stream among it)
+//    walks the tiles before it itself, from the inputs, and then its own (fwd_alone, bwd_alone). So a
+//    workgroup that has started ends by itself, whatever else runs, and as the walk takes the same
+//    operations in the same order, the results are the same bits either way.
 //  * Backward: the same with the positions' gradients walked the other way; the state before every
 //    position is walked again from the states that the forward pass saved at every tile's first
 //    position.
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -81,6 +82,7 @@ struct GatedArgs {
     uint64_t* agg;           // [tile][2][width] maps handed over, width = 64 ncb
     uint64_t* inc;           // [group][2][width] the state a group leaves
     float* part;             // [tile][width] partial sums of dlam
+    int32_t reads;           // reads of a value handed over before a workgroup goes on without it
 };
 
 // Walking positions: position p of the call is token p, or N - 1 - p walked from the end; sequence
@@ -201,6 +203,23 @@ __device__ __forceinline__ void gates(float r, float i, float k2, float* a, floa
     *a = fast_exp2(q);
     *mg = fast_sqrt(one_minus_sq(q, *a)) * sigmoid(i);
 }
+
+// What the backward pass takes of a position: a; m g; u a; g x a^2 u / m; 1 - sigmoid(r); 1 - sigmoid(i).
+struct BackGates {
+    float a, mg, ua, gm, ns, ng;
+    __device__ __forceinline__ BackGates(float r, float i, float x, float k2) {
+        const float q = k2 * sigmoid2(r, &ns);
+        const float gx = sigmoid2(i, &ng);
+        a = fast_exp2(q);
+        const float m2 = one_minus_sq(q, a), u = q * kLn2;
+        // 1 / m; where m^2 is below the normal numbers the hardware's rsq takes it for 0 and gives infinity:
+        // m, below 1.1e-19 there, and its terms are taken as 0
+        const float im = m2 >= 0x1p-126f ? fast_rsq(m2) : 0.0f;
+        mg = m2 * im * gx;
+        ua = u * a;
+        gm = gx * x * (ua * a) * im;
+    }
+};
 
 // The rows of a tile of one tensor as a buffer resource, rows in walking order. A position past the
 // end of the stream, or a channel past the row's, takes an offset outside the resource: the hardware
@@ -331,11 +350,16 @@ __device__ __forceinline__ void scan_rows(const Map& f, int lane, Map* total, Ma
     }
 }
 
-// Waits of this file's hand-over on this GPU that gave up after kSpinLimit reads.
-__device__ unsigned long long g_wait_timeouts;
+// Reads of a value handed over (about a microsecond each) before a workgroup goes on without it: some
+// milliseconds, many times what a tile takes.
+constexpr int kWaitReads = 1 << 12;
+std::atomic<int> g_wait_reads{kWaitReads};
+// Workgroups on this GPU that did.
+__device__ unsigned long long g_alone;
 
 // LDS of the hand-over.
 struct ChainLds {
+    int missing;                   // a wave went on without a value
     float2 wave[4][kGatedBlock];   // the maps of the waves
     float2 part[4][kGatedBlock];   // the maps of the tiles before this one, a quarter each
     float inc[kGatedBlock];        // the state that the group before left
@@ -359,14 +383,14 @@ struct Handed {
         c = __hip_atomic_load(w + second + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __device__ __forceinline__ bool there(uint64_t tag) const { return (v ^ c) == tag; }
-    // Loads until every lane's value is there.
-    __device__ __forceinline__ void wait(const uint64_t* w, int64_t second, int lane, uint64_t tag) {
-        for (int it = 0; it < kSpinLimit; ++it) {
+    // Loads until every lane's value is there; false when it was not in that many reads.
+    __device__ __forceinline__ bool wait(const uint64_t* w, int64_t second, int lane, uint64_t tag, int reads) {
+        for (int it = 0; it < reads; ++it) {
             load(w, second, lane);
-            if (__all(there(tag))) return;
+            if (__all(there(tag))) return true;
             __builtin_amdgcn_s_sleep(1);
         }
-        if (lane == 0) __hip_atomic_fetch_add(&g_wait_timeouts, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return false;
     }
     __device__ __forceinline__ float x() const { return __uint_as_float(static_cast<uint32_t>(v)); }
     __device__ __forceinline__ float y() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
@@ -374,8 +398,8 @@ struct Handed {
 
 // Hand-over along the chain: workgroup j of channel block cb publishes its tile's map (every one but
 // the last, whatever the sequences: no wait depends on what the offsets hold) and gathers what comes
-// in from tile first on (first == j: nothing comes in). Called by all threads between the barrier that
-// completes l.wave and one that completes l.part and l.inc. kBack: the waves' maps compose from the
+// in from tile first on (first == j: nothing comes in), or sets l.missing. Called by all threads between the
+// barrier that completes l.wave and one that completes l.part and l.inc. kBack: the waves' maps compose from the
 // last wave to the first.
 template <bool kBack>
 __device__ __forceinline__ Map tile_map(const ChainLds& l, int lane) {
@@ -404,6 +428,7 @@ __device__ __forceinline__ void chain_gather(const GatedArgs& a, ChainLds& l, in
     const bool inc = from_group && wave == 0;
     Handed v[kEach];
     Map f = identity();
+    bool all = true;
     // all loads first; then every value is waited for in turn
 #pragma unroll
     for (int k = 0; k < kEach; ++k)
@@ -411,16 +436,27 @@ __device__ __forceinline__ void chain_gather(const GatedArgs& a, ChainLds& l, in
     if (wave == 0) {
         Handed h;
         h.v = 0;
-        if (inc) h.wait(a.inc + 2 * (group - 1) * width + at, width, lane, tag);
+        if (inc) all = h.wait(a.inc + 2 * (group - 1) * width + at, width, lane, tag, a.reads);
         l.inc[lane] = h.x();
     }
 #pragma unroll
     for (int k = 0; k < kEach; ++k)
         if (k < n) {
-            if (!__all(v[k].there(tag))) v[k].wait(a.agg + 2 * (lo + k) * width + at, width, lane, tag);
+            if (!__all(v[k].there(tag)))
+                all = all && v[k].wait(a.agg + 2 * (lo + k) * width + at, width, lane, tag, a.reads);
             f = then(f, Map{v[k].x(), v[k].y()});
         }
     l.part[wave][lane] = make_float2(f.A, f.H);
+    if (!all) l.missing = 1;
+}
+// The first tile of the backward pass that something comes in from to tile j, whose positions begin at p0: the
+// one with the end of the sequence that goes on behind this one (j: none does).
+__device__ __forceinline__ int first_back(const GatedArgs& a, int j, int p0, int lane) {
+    const int next = p0 + kGatedBwdTile;
+    if (next >= a.N) return j;
+    const int q = seq_at_wave(a, next, lane);
+    if (bound_of(a, q) == next) return j;
+    return min(max(a.tiles - 1 - (bound_of(a, q + 1) - 1) / kGatedBwdTile, 0), j);
 }
 // What enters the tile in channel ch of the block (0 when nothing does).
 __device__ __forceinline__ float chain_carry(const ChainLds& l, int ch) {
@@ -452,6 +488,11 @@ __device__ __forceinline__ void pass_empty(const GatedArgs& a, const float* in, 
     }
 }
 
+// A value that the compiler fuses into no other operation.
+__device__ __forceinline__ float rounded(float v) {
+    asm("" : "+v"(v));
+    return v;
+}
 // Pins values: they are computed before this point, not where they are used (which would keep what they
 // are computed from in registers).
 template <int T, int V>
@@ -488,6 +529,322 @@ __device__ __forceinline__ void seq_value(const GatedArgs& a, const float* from,
     for (int v = 0; v < V; ++v) h[v] = from && c0 < a.D ? p[v] : 0.0f;
 }
 
+// The kernel's arguments, read again where the hardware points at them: the slow path below reads each where it
+// wants it, so that no register of the kernel is held for it (nor are indices: afresh makes one a new value to
+// the compiler).
+using ArgsAt = decltype(__builtin_amdgcn_kernarg_segment_ptr());
+__device__ __forceinline__ const GatedArgs& args_again(ArgsAt at) {
+    asm volatile("" : "+s"(at));
+    return *(const GatedArgs*)at;
+}
+__device__ __forceinline__ int afresh_s(int v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+__device__ __forceinline__ int afresh_v(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// The slow path of a workgroup whose wait took too long: each wave walks 64 channels, one a lane, element by
+// element from the inputs, about a microsecond a position. A tile of TILE positions is 4 G runs of T, in the order
+// of its threads. Measured, with every wait given up at once: 8 x 1025 x 768 bf16 1.3 ms forward, 2.0 backward; one
+// sequence of 16384 x 768 22 and 41 ms. Its being there costs the calls that do not take it nothing that
+// repeated timing shows above 1.5%.
+template <typename IO, int V, int TILE>
+struct Alone {
+    static constexpr int CL = kGatedBlock / V, T = TILE * CL / 256, G = 64 / CL, kEach = kGatedGroup / 4;
+    ArgsAt at;
+    int c, lane;             // the lane's channel
+    bool live;
+    float k2;
+
+    __device__ __forceinline__ Alone(ArgsAt args, int cb, int ln) : at(args), c(cb * kGatedBlock + ln), lane(ln) {
+        const GatedArgs& a = args_again(at);
+        live = c < a.D;
+        k2 = decay_rate(a.lam[live ? c : 0], a.c);
+    }
+
+    __device__ __forceinline__ const GatedArgs& args() const { return args_again(at); }
+    __device__ __forceinline__ int64_t row(const GatedArgs& a, int p) const { return a.rev ? a.N - 1 - p : p; }
+    // An element of position p; 0 past the stream's end, in a channel past the row's and of an absent tensor.
+    __device__ __forceinline__ float get(const void* base, int64_t ld, int p) const {
+        const GatedArgs& a = args();
+        Raw<IO, 1> v;
+        v.zero();
+        if (base && live && p < a.N) v.load(static_cast<const IoElem<IO>*>(base) + row(a, p) * ld + c);
+        return v.get(0);
+    }
+    __device__ __forceinline__ void put(void* base, int64_t ld, int p, float x) const {
+        const GatedArgs& a = args();
+        Raw<IO, 1> v;
+        v.set(&x);
+        if (base && live && p < a.N) v.store(static_cast<IoElem<IO>*>(base) + row(a, p) * ld + c);
+    }
+    __device__ __forceinline__ float state(const float* from, int q) const {
+        const GatedArgs& a = args();
+        return from && live ? from[seq_of(a, q) * a.D + c] : 0.0f;
+    }
+    __device__ __forceinline__ bool starts(int p, int q) const {
+        const GatedArgs& a = args();
+        return p < a.N && bound_of(a, q) == p;
+    }
+    __device__ __forceinline__ bool ends(int p, int q) const {
+        const GatedArgs& a = args();
+        return p < a.N && (bound_of(a, q + 1) == p + 1 || p + 1 == a.N);
+    }
+    __device__ __forceinline__ int seq(int p) const {
+        const GatedArgs& a = args();
+        return seq_at_wave(a, min(p, a.N - 1), lane);
+    }
+
+    // The map of a run of T positions from pt on.
+    __device__ __forceinline__ Map run_fwd(int pt) const {
+        Map f = identity();
+        bool cut = false;
+#pragma unroll 1
+        for (int p = pt; p < pt + T; ++p) {
+            const GatedArgs& a = args();
+            const int q = seq(p);
+            if (starts(p, q)) {
+                f.H = state(a.h0, q);
+                cut = true;
+            }
+            float at, mg;
+            gates(get(a.r, a.ld_r, p), get(a.i, a.ld_i, p), k2, &at, &mg);
+            f.A *= at;
+            f.H = fmaf(at, f.H, mg * get(a.x, a.ld_x, p));
+        }
+        f.A = cut ? 0.0f : fmaxf(f.A, kLeast);
+        return f;
+    }
+    // The same as the backward kernel forms it (its gates keep the complements).
+    __device__ __forceinline__ Map run_states(int pt) const {
+        Map f = identity();
+        bool cut = false;
+#pragma unroll 1
+        for (int p = pt; p < pt + T; ++p) {
+            const GatedArgs& a = args();
+            const int q = seq(p);
+            if (starts(p, q)) {
+                f.H = state(a.h0, q);
+                cut = true;
+            }
+            const float x = get(a.x, a.ld_x, p);
+            const BackGates g(get(a.r, a.ld_r, p), get(a.i, a.ld_i, p), x, k2);
+            f.A *= g.a;
+            f.H = fmaf(g.a, f.H, g.mg * x);
+        }
+        f.A = cut ? 0.0f : fmaxf(f.A, kLeast);
+        return f;
+    }
+    // Whether a sequence starts or ends among a wave's positions from p on: the backward kernel's walks round a
+    // product there that they fuse into the next sum elsewhere.
+    __device__ __forceinline__ bool has_cuts(int p) const {
+        bool any = false;
+#pragma unroll 1
+        for (int k = 0; k < T * G; ++k) {
+            const int q = seq(p + k);
+            any = any || starts(p + k, q) || ends(p + k, q);
+        }
+        return any;
+    }
+    // That of the gradient, walked from the run's end.
+    __device__ __forceinline__ Map run_back(int pt, bool cuts) const {
+        Map e = identity();
+        float after = 1.0f;   // what e.H is still to be multiplied with: the decay of the position behind
+        bool cut = false;
+#pragma unroll 1
+        for (int p = pt; p < pt + T; ++p) e.A *= decay(p);
+#pragma unroll 1
+        for (int p = pt + T - 1; p >= pt; --p) {
+            const GatedArgs& a = args();
+            const int q = seq(p);
+            if (ends(p, q)) {
+                e.H = state(a.dh_last, q);
+                cut = true;
+            }
+            e.H = fmaf(after, e.H, get(a.dy, a.ld_dy, p));
+            after = decay(p);
+            if (cuts) {
+                e.H = rounded(after * e.H);
+                after = 1.0f;
+            }
+        }
+        e.H = rounded(after * e.H);
+        e.A = cut ? 0.0f : fmaxf(e.A, kLeast);
+        return e;
+    }
+    __device__ __forceinline__ float decay(int p) const {
+        const GatedArgs& a = args();
+        float ns;
+        return fast_exp2(k2 * sigmoid2(get(a.r, a.ld_r, p), &ns));
+    }
+
+    // What tile j (in walking order) hands over.
+    template <bool kBack>
+    __device__ __forceinline__ Map tile(int j) const {
+        const int p0 = (kBack ? args().tiles - 1 - j : j) * TILE;
+        Map all = identity();
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+            Map part = identity();
+            const bool cuts = kBack && has_cuts(p0 + (3 - w) * G * T);
+#pragma unroll 1
+            for (int g = 0; g < G; ++g) {
+                const int run = w * G + g;
+                const Map f = kBack ? run_back(p0 + (4 * G - 1 - run) * T, cuts) : run_fwd(p0 + run * T);
+                part = g == 0 ? f : then(part, f);
+            }
+            all = then(all, part);
+        }
+        return all;
+    }
+
+    // Fills l.part and l.inc for tile j as chain_gather does: wave 0 walks the groups before tile j's, from tile
+    // first on, and then every wave its quarter of the group.
+    template <bool kBack>
+    __device__ __forceinline__ void gather(ChainLds& l, int j, int first, int wave) const {
+        const int g0 = j / kGatedGroup * kGatedGroup;
+        const int lo = (first < g0 ? g0 : first) + wave * kEach, end = min(j, lo + kEach);
+        float h = 0.0f;
+        Map f = identity();
+        int quarters = 0;
+#pragma unroll 1
+        for (int t = wave == 0 && first < g0 ? first : lo; t < end; ++t) {
+            const Map m = tile<kBack>(t);
+            const bool last = t < lo && t % kGatedGroup == kGatedGroup - 1;
+            if (!last) f = then(f, m);
+            if (t >= lo) continue;
+            // a quarter of a group before this one ends here, or the group does (empty quarters count too)
+            if (!last && (t - max(first, t / kGatedGroup * kGatedGroup)) % kEach != kEach - 1) continue;
+            do {
+                h = f(h);
+                f = identity();
+            } while (++quarters < 4 && last);
+            if (last) {
+                h = m(h);
+                quarters = 0;
+            }
+        }
+        l.part[wave][lane] = make_float2(f.A, f.H);
+        if (wave == 0) l.inc[lane] = h;
+        if (wave == 0 && lane == 0) __hip_atomic_fetch_add(&g_alone, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+};
+
+// The rest of k_gated_fwd behind the hand-over, without it. Called by all threads.
+template <typename IO, int V, int TILE>
+__device__ __forceinline__ void fwd_alone(ChainLds& l, int j, int cb, uint64_t tag) {
+    using W = Alone<IO, V, TILE>;
+    const int tid = afresh_v(static_cast<int>(threadIdx.x));
+    const ArgsAt args = __builtin_amdgcn_kernarg_segment_ptr();
+    const GatedArgs& a = args_again(args);
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    j = afresh_s(j);
+    cb = afresh_s(cb);
+    const W s(args, cb, lane);
+    const int p0 = j * TILE, start = bound_of(a, s.seq(p0));
+    s.template gather<false>(l, j, start >= p0 ? j : start / TILE, wave);
+    __syncthreads();
+    chain_leave<false>(a, l, j, cb, tag, wave, lane);
+    float enter = chain_carry(l, lane);
+#pragma unroll 1
+    for (int w = 0; w < wave; ++w) enter = Map{l.wave[w][lane].x, l.wave[w][lane].y}(enter);
+    Map before = identity();
+#pragma unroll 1
+    for (int g = 0; g < W::G; ++g) {
+        const int pt = p0 + (wave * W::G + g) * W::T;
+        float h = before(enter);
+        if (a.states && s.live && pt < a.N && pt % kGatedStride == 0)
+            a.states[static_cast<int64_t>(pt / kGatedStride) * a.D + s.c] = h;
+        before = s.run_fwd(pt);
+#pragma unroll 1
+        for (int p = pt; p < min(pt + W::T, a.N); ++p) {
+            const GatedArgs& a = s.args();
+            const int q = s.seq(p);
+            if (s.starts(p, q)) h = s.state(a.h0, q);
+            float at, mg;
+            gates(s.get(a.r, a.ld_r, p), s.get(a.i, a.ld_i, p), s.k2, &at, &mg);
+            h = fmaf(at, h, mg * s.get(a.x, a.ld_x, p));
+            s.put(a.y, a.D, p, h);
+            if (a.h_last && s.live && s.ends(p, q)) a.h_last[seq_of(a, q) * a.D + s.c] = h;
+        }
+    }
+    pass_empty(a, a.h0, a.h_last, j, cb);
+}
+
+// The rest of k_gated_bwd, likewise. fwd: the waves' maps of the states; park: T x 256 values.
+template <typename IO, int V>
+__device__ __forceinline__ void bwd_alone(ChainLds& l, int j, int cb, uint64_t tag, float2 (*fwd)[kGatedBlock], float* park) {
+    using W = Alone<IO, V, kGatedBwdTile>;
+    const int tid = afresh_v(static_cast<int>(threadIdx.x));
+    const ArgsAt args = __builtin_amdgcn_kernarg_segment_ptr();
+    const GatedArgs& a = args_again(args);
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    j = afresh_s(j);
+    cb = afresh_s(cb);
+    const W s(args, cb, lane);
+    const int at = a.tiles - 1 - j, p0 = at * kGatedBwdTile;
+    s.template gather<true>(l, j, first_back(a, j, p0, lane), wave);
+    __syncthreads();
+    chain_leave<true>(a, l, j, cb, tag, wave, lane);
+    float h = a.states_in[static_cast<int64_t>(at) * a.D + (s.live ? s.c : 0)], d = chain_carry(l, lane), total = 0.0f;
+#pragma unroll 1
+    for (int w = 0; w < wave; ++w) h = Map{fwd[w][lane].x, fwd[w][lane].y}(h);
+#pragma unroll 1
+    for (int w = 3; w > wave; --w) d = Map{l.wave[w][lane].x, l.wave[w][lane].y}(d);
+    float* mine = park + wave * W::T * 64 + lane;   // of position k: w / d
+    const int from = p0 + wave * W::G * W::T;
+    const bool cuts = s.has_cuts(from);
+#pragma unroll 1
+    for (int g = 0; g < W::G; ++g) {
+        const int pt = from + g * W::T;
+        float hk = (g == 0 ? identity() : s.run_states(from))(h);
+        float da = 1.0f, dk = (g == W::G - 1 ? identity() : s.run_back(from + W::T, cuts))(d);
+#pragma unroll 1
+        for (int p = pt; p < pt + W::T; ++p) {
+            const GatedArgs& a = s.args();
+            const int q = s.seq(p);
+            if (s.starts(p, q)) hk = s.state(a.h0, q);
+            const float x = s.get(a.x, a.ld_x, p);
+            const BackGates b(s.get(a.r, a.ld_r, p), s.get(a.i, a.ld_i, p), x, s.k2);
+            mine[(p - pt) * 64] = fmaf(b.ua, hk, -b.gm);
+            hk = fmaf(b.a, hk, b.mg * x);
+        }
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int p = pt + W::T - 1; p >= pt; --p) {
+            const GatedArgs& a = s.args();
+            const int q = s.seq(p);
+            if (s.ends(p, q)) {
+                dk = s.state(a.dh_last, q);
+                if (p == a.N - 1) sum = 0.0f;
+            }
+            const float x = s.get(a.x, a.ld_x, p);
+            const BackGates b(s.get(a.r, a.ld_r, p), s.get(a.i, a.ld_i, p), x, s.k2);
+            const float del = fmaf(da, dk, s.get(a.dy, a.ld_dy, p)), ua = mine[(p - pt) * 64], ox = del * b.mg;
+            s.put(a.dx, a.ld_dx, p, ox);
+            s.put(a.dr, a.ld_dr, p, del * ua * b.ns);
+            s.put(a.di, a.ld_di, p, ox * x * b.ng);
+            sum = fmaf(del, ua, sum);
+            da = cuts ? 1.0f : b.a;
+            dk = cuts ? rounded(b.a * del) : del;
+            if (a.dh0 && s.live && s.starts(p, q)) a.dh0[seq_of(a, q) * a.D + s.c] = dk;
+        }
+        if (pt >= a.N || !s.live) sum = 0.0f;
+        total = g == 0 ? sum : total + sum;
+    }
+    pass_empty(a, a.dh_last, a.dh0, j, cb);
+    if (!a.dlam) return;
+    __syncthreads();
+    fwd[wave][lane].x = total;
+    __syncthreads();
+    if (wave == 0)
+        a.part[static_cast<int64_t>(at) * a.ncb * kGatedBlock + cb * kGatedBlock + lane] =
+            (fwd[0][lane].x + fwd[1][lane].x) + (fwd[2][lane].x + fwd[3][lane].x);
+}
+
 // Forward pass: a tile of TILE positions x 64 channels. The maps compose as (A2, H2)(A1, H1) = (A2 A1, A2 H1 +
 // H2), so a tile needs only the state that enters it and no element is read twice. Measured: 1 x 65537 x
 // 1536 bf16 188 us (805 MB, 4.3 TB/s), 8 x 1025 x 768 bf16 16.5 us, 128 x 197 x 768 bf16 with saved states 39
@@ -507,6 +864,7 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
     const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
     const bool live = c0 < a.D;
     const int p0 = j * TILE, pt = p0 + tg * T;
+    if (kChain && tid == 0) lds.missing = 0;
 
     float k2[V];
 #pragma unroll
@@ -589,6 +947,7 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
         const int first = start >= p0 ? j : start / TILE;
         chain_gather<false>(a, lds, j, cb, first, tag, wave, lane);
         __syncthreads();
+        if (__builtin_expect(lds.missing, 0)) return fwd_alone<IO, V, TILE>(lds, j, cb, tag);
         chain_leave<false>(a, lds, j, cb, tag, wave, lane);
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = chain_carry(lds, cl * V + v);
@@ -656,6 +1015,7 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
     const int cl = tid % CL, tg = tid / CL, c0 = cb * kGatedBlock + cl * V;
     const bool live = c0 < a.D;
     const int p0 = tile * kGatedBwdTile, pt = p0 + tg * T;
+    if (kChain && tid == 0) lds.missing = 0;
 
     float k2[V], h[V];
 #pragma unroll
@@ -704,16 +1064,13 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
         float ns[V], ng[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float q = k2[v] * sigmoid2(rr[k].get(v), &ns[v]);
-            const float gx = sigmoid2(ir[k].get(v), &ng[v]);
-            const float at = fast_exp2(q), m2 = one_minus_sq(q, at), u = q * kLn2;
-            // 1 / m; where m^2 is below the normal numbers the hardware's rsq takes it for 0 and gives infinity:
-            // m, below 1.1e-19 there, and its terms are taken as 0
-            const float im = m2 >= 0x1p-126f ? fast_rsq(m2) : 0.0f;
-            av[k][v] = at;
-            mg[k][v] = m2 * im * gx;
-            ua[k][v] = u * at;
-            gm[k][v] = gx * xr[k].get(v) * (ua[k][v] * at) * im;
+            const BackGates g(rr[k].get(v), ir[k].get(v), xr[k].get(v), k2[v]);
+            av[k][v] = g.a;
+            mg[k][v] = g.mg;
+            ua[k][v] = g.ua;
+            gm[k][v] = g.gm;
+            ns[v] = g.ns;
+            ng[v] = g.ng;
         }
         Raw<float, V> w;
         w.set(ns);
@@ -736,7 +1093,9 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
 #pragma unroll
         for (int k = T - 1; k >= 0; --k)
 #pragma unroll
-            for (int v = 0; v < V; ++v) e[v].H = av[k][v] * (gr[k].get(v) + e[v].H);
+            for (int v = 0; v < V; ++v) e[v].H = k == T - 1 ? gr[k].get(v) : fmaf(av[k == T - 1 ? k : k + 1][v], e[v].H, gr[k].get(v));
+#pragma unroll
+        for (int v = 0; v < V; ++v) e[v].H *= av[0][v];
     } else {
         float g[V];
 #pragma unroll
@@ -757,7 +1116,7 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
                 for (int v = 0; v < V; ++v) e[v].H = g[v];
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v) e[v].H = av[k][v] * (gr[k].get(v) + e[v].H);
+            for (int v = 0; v < V; ++v) e[v].H = rounded(av[k][v] * (gr[k].get(v) + e[v].H));
         }
     }
 #pragma unroll
@@ -786,16 +1145,7 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
     }
     pin_all(mg);
     const uint64_t tag = kChain ? dispatch_tag() : 0;
-    if constexpr (kChain) {
-        // what comes in comes from the tiles up to the end of the sequence that goes on behind this one
-        const int next = p0 + kGatedBwdTile;
-        int first = j;
-        if (next < a.N) {
-            const int q = seq_at_wave(a, next, lane);
-            if (bound_of(a, q) != next) first = a.tiles - 1 - (bound_of(a, q + 1) - 1) / kGatedBwdTile;
-        }
-        chain_gather<true>(a, lds, j, cb, min(max(first, 0), j), tag, wave, lane);
-    }
+    if constexpr (kChain) chain_gather<true>(a, lds, j, cb, first_back(a, j, p0, lane), tag, wave, lane);
     // the state before every position, meanwhile: ua becomes w / d
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -826,6 +1176,7 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
     float d[V], sum[V];
     if constexpr (kChain) {
         __syncthreads();
+        if (__builtin_expect(lds.missing, 0)) return bwd_alone<IO, V>(lds, j, cb, tag, fwd, &park[0][0]);
         chain_leave<true>(a, lds, j, cb, tag, wave, lane);
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = chain_carry(lds, cl * V + v);
@@ -843,29 +1194,34 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
     dx.init(a, a.dx, a.ld_dx, p0, tg, c0);
     dr.init(a, a.dr, a.ld_dr, p0, tg, c0);
     di.init(a, a.di, a.ld_di, p0, tg, c0);
-    // the gradient's walk through position k; in: the position is inside the stream
-    auto walk = [&](int k, bool in) {
+    // the gradient's walk through position k, where what goes on to it is carry d; in: it is inside the stream
+    auto walk = [&](int k, const float (&carry)[V], bool in) {
         float ox[V], orr[V], oi[V];
         Raw<float, V> ns, ng;
         ns.load(&park[2 * k][tid * V]);
         ng.load(&park[2 * k + 1][tid * V]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float del = gr[k].get(v) + d[v];
-            const float w = del * ua[k][v];
+            const float del = fmaf(carry[v], d[v], gr[k].get(v));
             ox[v] = del * mg[k][v];
             oi[v] = ox[v] * xr[k].get(v) * ng.get(v);
-            orr[v] = w * ns.get(v);
-            sum[v] += w;
-            d[v] = av[k][v] * del;
+            orr[v] = del * ua[k][v] * ns.get(v);
+            sum[v] = fmaf(del, ua[k][v], sum[v]);
+            d[v] = del;
         }
         st_tile<IO, V, kPolicy>(dx.rsrc, dx.at(in), dx.so + k * dx.step, ox);
         st_tile<IO, V, kPolicy>(dr.rsrc, dr.at(in), dr.so + k * dr.step, orr);
         st_tile<IO, V, kPolicy>(di.rsrc, di.at(in), di.so + k * di.step, oi);
     };
+    float one[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) one[v] = 1.0f;
     if (!cuts) {
 #pragma unroll
-        for (int k = T - 1; k >= 0; --k) walk(k, pt < a.N);
+        for (int k = T - 1; k >= 0; --k) {
+            if (k == T - 1) walk(k, one, pt < a.N);
+            else walk(k, av[k + 1], pt < a.N);
+        }
     } else {
 #pragma unroll
         for (int k = T - 1; k >= 0; --k) {
@@ -875,7 +1231,9 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
 #pragma unroll
                 for (int v = 0; v < V; ++v) sum[v] = pt + k == a.N - 1 ? 0.0f : sum[v];
             }
-            walk(k, pt + k < a.N);
+            walk(k, one, pt + k < a.N);
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] = rounded(av[k][v] * d[v]);
             if (a.dh0 && live && (starts >> k & 1)) {
                 float* dst = a.dh0 + static_cast<int64_t>(rows[wave][wt + k]) * a.D + c0;
 #pragma unroll
@@ -1005,6 +1363,7 @@ GatedArgs common_args(const vimscan_gated* g, const vimscan_launch* l, const Gat
     }
     a.part = p.ws > p.off_part ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
     a.rev = (l->flags & VIMSCAN_FLAG_REVERSE) ? 1 : 0;
+    a.reads = g_wait_reads.load(std::memory_order_relaxed);
     return a;
 }
 
@@ -1073,19 +1432,22 @@ void launch_bwd_any(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
 
 }  // namespace
 
-namespace vimscan_host {
+extern "C" {
 
-int gated_wait_timeouts(uint64_t* count) {
+int vimscan_gated_alone(uint64_t* count) {
+    if (!count) return VIMSCAN_ERR_NULL;
     unsigned long long v = 0;
-    if (hipMemcpyFromSymbol(&v, HIP_SYMBOL(g_wait_timeouts), sizeof(v), 0, hipMemcpyDeviceToHost) != hipSuccess)
+    if (hipMemcpyFromSymbol(&v, HIP_SYMBOL(g_alone), sizeof(v), 0, hipMemcpyDeviceToHost) != hipSuccess)
         return VIMSCAN_ERR_HIP;
     *count = static_cast<uint64_t>(v);
     return VIMSCAN_OK;
 }
 
-}  // namespace vimscan_host
-
-extern "C" {
+int vimscan_gated_wait_reads(int32_t reads) {
+    if (reads < 0) return VIMSCAN_ERR_PARAM;
+    g_wait_reads.store(reads, std::memory_order_relaxed);
+    return VIMSCAN_OK;
+}
 
 int vimscan_gated_fwd(const vimscan_gated* g, int64_t seg_len, void* y, float* h_last, float* states,
                       const vimscan_launch* launch) {

@@ -61,7 +61,6 @@
 #include <cstring>
 #include <mutex>
 
-#include "block_plan.h"
 #include "handover.h"
 #include "plan.h"
 #include "vimscan.h"
@@ -1476,9 +1475,7 @@ int vimscan_wait_timeouts(uint64_t* count) {
     unsigned long long v = 0;
     if (hipMemcpyFromSymbol(&v, HIP_SYMBOL(g_wait_timeouts), sizeof(v), 0, hipMemcpyDeviceToHost) != hipSuccess)
         return VIMSCAN_ERR_HIP;
-    uint64_t gated = 0;
-    if (vimscan_host::gated_wait_timeouts(&gated) != VIMSCAN_OK) return VIMSCAN_ERR_HIP;
-    *count = static_cast<uint64_t>(v) + gated;
+    *count = static_cast<uint64_t>(v);
     return VIMSCAN_OK;
 }
 

@@ -469,18 +469,29 @@ const char* vimscan_status_string(int status);
 const char* vimscan_version(void);
 
 /*
- * Diagnostics of the one-kernel chunked scans (plans of 2..16 chunks) and of the gated
- * recurrence (whose workgroups hand their states on in the same way): *count = the number of
+ * Diagnostics of the one-kernel chunked scans (plans of 2..16 chunks): *count = the number of
  * waves on the current HIP device, since the library was loaded, whose wait for the chunk
  * aggregates of the earlier chunks of their sequence gave up after its bound (about a second);
  * their calls' outputs are unspecified. The hardware starts the workgroups of every XCD in
  * increasing id order, which makes every such wait end (the kernel's own comment gives the
- * argument; calls of this kind that overlap on several streams also rely on every XCD being
- * shared between them), so the count stays 0; it exists so that a failure of that premise is visible.
+ * argument), so the count stays 0; it exists so that a failure of that premise is visible.
  * Synchronous (a device-to-host copy after the device's queued work). Returns VIMSCAN_OK,
  * VIMSCAN_ERR_NULL or VIMSCAN_ERR_HIP.
  */
 int vimscan_wait_timeouts(uint64_t* count);
+
+/*
+ * The gated recurrence's workgroups hand states on to each other. One that has read a value
+ * that is not there for a number of times (4096, some milliseconds: other work, another such call on
+ * another stream among it, may hold up the workgroups before it) goes on alone, from the inputs:
+ * slower, the same bits. vimscan_gated_wait_reads sets that number for the calls queued from now on
+ * (a captured graph keeps the one it was captured with); 0 makes every workgroup whose value is not
+ * there at once go on alone. reads < 0 is VIMSCAN_ERR_PARAM. Host only; one number for the process.
+ * vimscan_gated_alone: *count = the workgroups on the current HIP device that went on alone since the
+ * library was loaded. Synchronous, as vimscan_wait_timeouts.
+ */
+int vimscan_gated_wait_reads(int32_t reads);
+int vimscan_gated_alone(uint64_t* count);
 
 #ifdef __cplusplus
 }
