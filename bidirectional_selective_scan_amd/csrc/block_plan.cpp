@@ -177,7 +177,7 @@ int check_gated_step(const vimscan_gated* g, const float* state, int64_t nslots,
     if (!positive(g->c)) return VIMSCAN_ERR_PARAM;
     if (!good_stride(g->ld_x, d) || !good_stride(g->ld_r, d) || !good_stride(g->ld_i, d)) return VIMSCAN_ERR_PARAM;
     if (n == 0 || d == 0) return VIMSCAN_OK;
-    if (n > kMaxGatedWgs / ((d + 63) / 64)) return VIMSCAN_ERR_SHAPE;
+    if (n > kMaxStepParts / ((d + 63) / 64)) return VIMSCAN_ERR_SHAPE;
     if (!g->x || !g->r || !g->i || !g->lam || !y || (nslots > 0 && !state)) return VIMSCAN_ERR_NULL;
     const size_t e = io_bytes(l);
     const void* io[] = {g->x, g->r, g->i, y};

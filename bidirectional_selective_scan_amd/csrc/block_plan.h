@@ -13,7 +13,11 @@ namespace vimscan_host {
 constexpr int kGatedStride = VIMSCAN_GATED_STRIDE;
 // Rows of a tile (128 at most) lie within the 2^31 bytes that one buffer resource's offsets span.
 constexpr int64_t kMaxRowStride = int64_t(1) << 22;
-constexpr int64_t kMaxGatedWgs = int64_t(1) << 24;  // x 256 threads: a grid's limit of 2^32 threads
+// Workgroups of 256 threads: a grid holds fewer than 2^32 threads. (So few tiles also keep every position of
+// the last tile below 2^31.)
+constexpr int64_t kMaxGatedWgs = (int64_t(1) << 24) - 1;
+// Single tokens: rows x parts of 64 channels.
+constexpr int64_t kMaxStepParts = int64_t(1) << 24;
 constexpr int64_t kNormMaxWidth = 32768;
 
 // Tiling of the gated recurrence: a workgroup of 256 threads takes kGatedBlock channels of a tile of

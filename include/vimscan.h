@@ -317,7 +317,7 @@ int vimscan_bidir_fwd_noalloc(const void* x, const void* dt, const void* z, cons
  * Rows of x, r and i are ld_* elements apart (>= d_inner, < 2^22), so they may be slices of one
  * projection's output; a row's channels are contiguous. h0, h_last and lam are dense fp32.
  * launch->d_state must be 1 and chunk_len 0 (VIMSCAN_ERR_CHUNK); flags: VIMSCAN_FLAG_REVERSE only.
- * tokens = batch * seqlen < 2^31; there is no limit on tokens * d_inner short of 2^24 workgroups
+ * tokens = batch * seqlen < 2^31; there is no limit on tokens * d_inner but that of 2^24 - 1 workgroups
  * (vimscan_gated_plan: VIMSCAN_ERR_SHAPE past it).
  */
 typedef struct vimscan_gated {
