@@ -81,6 +81,14 @@ int64_t fwd_tile(int64_t tokens, int64_t length, int64_t ncb) {
     return length <= kGatedFwdTileSmall || (length <= 2048 && wgs < 2048) ? kGatedFwdTileSmall : kGatedFwdTile;
 }
 
+// Rows of D channels that a workgroup of a block norm works on at once.
+template <size_t N>
+int64_t rows_at_once(const NormSpread (&spreads)[N], int64_t D) {
+    for (const NormSpread& s : spreads)
+        if (D <= s.width()) return s.rows();
+    return 1;
+}
+
 }  // namespace
 
 int make_gated_plan(const vimscan_launch* l, int64_t seg_len, bool packed, int64_t nseq, bool backward, GatedPlan* p) {
@@ -204,8 +212,12 @@ int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p) {
     // enough workgroups for every CU's waves; fewer, each with more rows, where every one leaves three rows
     // of partial weight gradients
     const int64_t most = p->D <= 256 ? 2048 : 512;
-    p->wgs = p->rows < most ? p->rows : most;
-    p->rows_per_wg = (p->rows + p->wgs - 1) / p->wgs;
+    const int64_t at_once = l->io_dtype == VIMSCAN_F32 && p->D % 4 != 0 ? rows_at_once(kNormSingles, p->D)
+                            : backward                                  ? rows_at_once(kNormBackward, p->D)
+                                                                        : rows_at_once(kNormForward, p->D);
+    const int64_t turns = (p->rows + at_once - 1) / at_once;
+    p->wgs = turns < most ? turns : most;
+    p->rows_per_wg = (turns + p->wgs - 1) / p->wgs * at_once;
     if (backward) p->ws = up256(static_cast<size_t>(p->wgs) * 3 * p->D * sizeof(float));
     return VIMSCAN_OK;
 }

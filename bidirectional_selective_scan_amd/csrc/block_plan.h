@@ -50,11 +50,31 @@ int check_gated_call(const vimscan_gated* g, const void* y, const float* h_last,
 int check_gated_step(const vimscan_gated* g, const float* state, int64_t nslots, const int32_t* slots_in,
                      const int32_t* slots_out, const void* y, const vimscan_launch* l);
 
-// Plan of a block norm: how a row is spread over lanes.
+// How a block norm's row is spread: over lanes of one wave (waves = 1) or over waves of 64, each lane nv vectors of
+// vec channels. A workgroup of 256 threads works on several narrow rows at once; wide rows take one of up to 1024.
+struct NormSpread {
+    int nv, lanes, waves, vec;
+    constexpr int64_t width() const { return int64_t(nv) * lanes * waves * vec; }   // channels at most
+    constexpr int threads() const { return waves > 4 ? 64 * waves : 256; }
+    constexpr int rows() const { return threads() / (lanes * waves); }
+};
+// The spreads from narrow to wide; a row takes the first that holds it. Forward fewer waves with more of a row
+// each; backward, where a channel takes three times the registers, more waves from 1024 channels on (13056 x 1536
+// bf16: 86 us with 8 waves, 93 with 4; 4099 x 8192: 342 us with 16 waves, 577 with 8, and 173 with the weights'
+// gradients in LDS).
+constexpr NormSpread kNormForward[] = {{1, 16, 1, 4}, {1, 32, 1, 4}, {1, 64, 1, 4}, {2, 64, 1, 4}, {3, 64, 1, 4}, {4, 64, 1, 4},
+                                       {2, 64, 4, 4}, {4, 64, 4, 4}, {4, 64, 8, 4}, {4, 64, 16, 4}, {8, 64, 16, 4}};
+constexpr NormSpread kNormBackward[] = {{1, 16, 1, 4}, {1, 32, 1, 4}, {1, 64, 1, 4}, {2, 64, 1, 4}, {3, 64, 1, 4}, {4, 64, 1, 4},
+                                        {1, 64, 8, 4}, {1, 64, 16, 4}, {2, 64, 16, 4}, {4, 64, 16, 4}, {8, 64, 16, 4}};
+// fp32 rows whose width is no multiple of 4: single channels, either direction.
+constexpr NormSpread kNormSingles[] = {{4, 16, 1, 1}, {4, 32, 1, 1}, {4, 64, 1, 1}, {8, 64, 1, 1}, {4, 64, 4, 1}, {4, 64, 8, 1},
+                                       {8, 64, 8, 1}, {8, 64, 16, 1}, {16, 64, 16, 1}, {32, 64, 16, 1}};
+
+// Plan of a block norm. A workgroup takes spread.rows() rows at a time.
 struct NormPlan {
     int64_t rows, D;
-    int64_t wgs, rows_per_wg;
-    size_t ws;
+    int64_t wgs, rows_per_wg;      // workgroups launched, and the rows that the first of them takes
+    size_t ws;                     // three rows of partial weight gradients for each
 };
 
 int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p);

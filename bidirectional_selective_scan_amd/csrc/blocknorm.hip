@@ -5,6 +5,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <iterator>
 
 #include "block_device.h"
 #include "block_plan.h"
@@ -13,7 +14,11 @@
 namespace {
 
 using namespace vimscan_dev;
+using vimscan_host::kNormBackward;
+using vimscan_host::kNormForward;
+using vimscan_host::kNormSingles;
 using vimscan_host::NormPlan;
+using vimscan_host::NormSpread;
 
 struct NormArgs {
     const void* x;
@@ -88,17 +93,16 @@ __device__ __forceinline__ void row_sum(float* u, float* v, float2 (*lds)[W], in
 __device__ __forceinline__ float sigmoid(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 
-// How a row is spread: over L lanes of a wave (W = 1) or W whole waves (L = 64), each lane NV vectors of V
-// channels. A workgroup of 256 threads works on several rows at once where they are narrow; wide rows
-// take one of up to 1024 threads. kWhole: the width is a multiple of V; otherwise a row's last vector is
+// A row spread over L lanes of a wave (W = 1) or W whole waves (L = 64), each lane NV vectors of V channels
+// (NormSpread, whose tables say which widths take which). kWhole: the width is a multiple of V; otherwise a row's last vector is
 // read as the row's last V elements and shifted into place once every load of the row has been issued
 // (settle), and written by elements.
 template <int NV_, int L_, int W_, int V_, bool kWhole_> struct Spread {
     static constexpr int NV = NV_, L = L_, W = W_, V = V_;
     static constexpr bool kWhole = kWhole_;
-    static constexpr int kThreads = W > 4 ? 64 * W : 256;
-    static constexpr int kRows = kThreads / (L * W);
-    static constexpr int kWidth = NV * L * W * V;   // channels at most
+    static constexpr NormSpread kSpread{NV, L, W, V};
+    static constexpr int kThreads = kSpread.threads(), kRows = kSpread.rows();
+    static constexpr int kWidth = static_cast<int>(kSpread.width());
     static_assert(W == 1 || L == 64, "part of a wave, or whole waves");
     static_assert(V == 4 || kWhole, "single channels are always whole");
     // the thread's place in its row, and its row among the workgroup's
@@ -443,8 +447,7 @@ __global__ __launch_bounds__(1024) void k_norm_cols(NormArgs a, int parts) {
 
 template <typename IO, typename RES, bool kBack, typename S>
 void launch(const NormArgs& a, const NormPlan& p, hipStream_t s) {
-    const int64_t full = (a.rows + S::kRows - 1) / S::kRows;
-    const dim3 grid(static_cast<unsigned>(full < p.wgs ? full : p.wgs)), block(S::kThreads);
+    const dim3 grid(static_cast<unsigned>(p.wgs)), block(S::kThreads);
     if constexpr (kBack) {
         hipLaunchKernelGGL((k_norm_bwd<IO, RES, S>), grid, block, 0, s, a);
         if (a.part)
@@ -455,40 +458,23 @@ void launch(const NormArgs& a, const NormPlan& p, hipStream_t s) {
     }
 }
 
-// The first of the spreads that holds the row, from narrow to wide.
-template <typename IO, typename RES, bool kBack, typename S, typename... More>
+// The first of N spreads that holds the row.
+template <typename IO, typename RES, bool kBack, bool kWhole, const NormSpread* kSpreads, size_t N, size_t I = 0>
 void launch_first(const NormArgs& a, const NormPlan& p, hipStream_t s) {
-    if constexpr (sizeof...(More) > 0) {
-        if (a.D > S::kWidth) return launch_first<IO, RES, kBack, More...>(a, p, s);
+    constexpr NormSpread f = kSpreads[I];
+    if constexpr (I + 1 < N) {
+        if (a.D > f.width()) return launch_first<IO, RES, kBack, kWhole, kSpreads, N, I + 1>(a, p, s);
     }
-    launch<IO, RES, kBack, S>(a, p, s);
+    launch<IO, RES, kBack, Spread<f.nv, f.lanes, f.waves, f.vec, kWhole>>(a, p, s);
 }
 template <typename IO, typename RES, bool kWhole>
 void launch_vectors(const NormArgs& a, const NormPlan& p, bool back, hipStream_t s) {
-    using A = Spread<1, 16, 1, 4, kWhole>;
-    using B = Spread<1, 32, 1, 4, kWhole>;
-    using C = Spread<1, 64, 1, 4, kWhole>;
-    using C2 = Spread<2, 64, 1, 4, kWhole>;
-    using C3 = Spread<3, 64, 1, 4, kWhole>;
-    using C4 = Spread<4, 64, 1, 4, kWhole>;
-    using D2 = Spread<2, 64, 4, 4, kWhole>;
-    using D4 = Spread<4, 64, 4, 4, kWhole>;
-    using E4 = Spread<4, 64, 8, 4, kWhole>;
-    using F2 = Spread<2, 64, 16, 4, kWhole>;
-    using F4 = Spread<4, 64, 16, 4, kWhole>;
-    using F8 = Spread<8, 64, 16, 4, kWhole>;
-    // forward fewer waves with more of a row each; backward, where a channel takes three times the
-    // registers, more waves from 1024 channels on (13056 x 1536 bf16: 86 us with 8 waves, 93 with 4; 4099 x
-    // 8192: 342 us with 16 waves, 577 with 8, and 173 with the weights' gradients in LDS)
-    if (!back) launch_first<IO, RES, false, A, B, C, C2, C3, C4, D2, D4, E4, F4, F8>(a, p, s);
-    else launch_first<IO, RES, true, A, B, C, C2, C3, C4, Spread<1, 64, 8, 4, kWhole>, Spread<1, 64, 16, 4, kWhole>, F2, F4, F8>(a, p, s);
+    if (back) launch_first<IO, RES, true, kWhole, kNormBackward, std::size(kNormBackward)>(a, p, s);
+    else launch_first<IO, RES, false, kWhole, kNormForward, std::size(kNormForward)>(a, p, s);
 }
 template <bool kBack>
 void launch_singles(const NormArgs& a, const NormPlan& p, hipStream_t s) {
-    launch_first<float, float, kBack, Spread<4, 16, 1, 1, true>, Spread<4, 32, 1, 1, true>, Spread<4, 64, 1, 1, true>,
-                 Spread<8, 64, 1, 1, true>, Spread<4, 64, 4, 1, true>, Spread<4, 64, 8, 1, true>,
-                 Spread<8, 64, 8, 1, true>, Spread<8, 64, 16, 1, true>, Spread<16, 64, 16, 1, true>,
-                 Spread<32, 64, 16, 1, true>>(a, p, s);
+    launch_first<float, float, kBack, true, kNormSingles, std::size(kNormSingles)>(a, p, s);
 }
 
 // Widths that are no multiple of four: in bf16 vectors at any alignment are still twice as fast as single
