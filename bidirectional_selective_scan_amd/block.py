@@ -144,6 +144,8 @@ def _stream_of(dev, stream):
 
 def _workspace(workspace, need, dev, launch):
     """A workspace of the plan's size (the caller's when it is large enough)."""
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous on {dev}")
     if need == 0:
         return None
     if workspace is None or workspace.numel() * workspace.element_size() < need:
