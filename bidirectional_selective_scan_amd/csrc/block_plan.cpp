@@ -36,6 +36,17 @@ bool meet(const Span& a, const Span& b) {
     return x < y + b.n && y < x + a.n;
 }
 
+// Whether two arrays of equally many rows of d elements of e bytes, ld_* elements apart, share an element. Slices of
+// one array may be interleaved: their rows have the same distance and lie beside each other. (Of rows at different
+// distances only the first ones are compared.)
+bool rows_meet(const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t rows, int64_t d, size_t e) {
+    if (!meet(rows_span(a, rows, ld_a, d, e), rows_span(b, rows, ld_b, d, e))) return false;
+    if (ld_a != ld_b) return meet(dense_span(a, 1, d, e), dense_span(b, 1, d, e));
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const size_t beside = (x > y ? x - y : y - x) % (static_cast<size_t>(ld_a) * e), row = static_cast<size_t>(d) * e;
+    return beside < row || static_cast<size_t>(ld_a) * e - beside < row;
+}
+
 template <size_t N, size_t M>
 bool any_meet(const Span (&a)[N], const Span (&b)[M]) {
     for (const Span& x : a)
@@ -167,9 +178,10 @@ int check_gated_call(const vimscan_gated* g, const void* y, const float* h_last,
                          rows_span(grad->di, n, grad->ld_di, d, e), dense_span(grad->dlam, 1, d, 4),
                          dense_span(grad->dh0, p.nseq, d, 4)};
     if (any_meet(outs, ins) || meet(outs[3], outs[4])) return VIMSCAN_ERR_ALIAS;
-    for (int k = 0; k < 3; ++k)  // dx, dr, di may be interleaved slices, but not the same rows
-        for (int j = 0; j < k; ++j)
-            if (outs[k].p && outs[k].p == outs[j].p) return VIMSCAN_ERR_ALIAS;
+    if (rows_meet(grad->dx, grad->ld_dx, grad->dr, grad->ld_dr, n, d, e) ||
+        rows_meet(grad->dx, grad->ld_dx, grad->di, grad->ld_di, n, d, e) ||
+        rows_meet(grad->dr, grad->ld_dr, grad->di, grad->ld_di, n, d, e))
+        return VIMSCAN_ERR_ALIAS;
     for (int k = 0; k < 3; ++k)
         if (meet(outs[k], outs[3]) || meet(outs[k], outs[4])) return VIMSCAN_ERR_ALIAS;
     return check_workspace(l, p.ws, ins, outs);
@@ -274,7 +286,7 @@ int check_norm_call(const vimscan_norm* n, const void* sum, const void* out, con
     if (any_meet(outs, ins) || any_meet(outs, rin) || any_meet(outs, rout) || any_meet(rout, ins) || meet(dres, res))
         return VIMSCAN_ERR_ALIAS;
     if (g->dresidual != g->dsum && meet(dres, dsum)) return VIMSCAN_ERR_ALIAS;
-    if (outs[0].p && outs[0].p == outs[1].p) return VIMSCAN_ERR_ALIAS;
+    if (rows_meet(g->dx, g->ld_dx, g->dz, g->ld_dz, rows, d, e)) return VIMSCAN_ERR_ALIAS;
     for (int k = 2; k < 5; ++k)
         for (int j = 0; j < k; ++j)
             if (meet(outs[k], outs[j])) return VIMSCAN_ERR_ALIAS;

@@ -368,8 +368,8 @@ typedef struct vimscan_gated_grad {
  *   dx = d m g,  di = d m x g (1 - g),  dh0 = e at the first token,
  *   w = d (u a h_{t-1} - g x a^2 u / m),  dr = w (1 - s),  dlam = sum w * sigmoid(lam) / softplus(lam)
  * (w is u dL/du, which stays finite as u goes to 0; u / m is taken as 0 there). Arguments as the
- * forward pass; the outputs must not overlap an input or the workspace, but dx, dr and di may be
- * slices of one array. Needs a workspace (vimscan_gated_plan).
+ * forward pass; the outputs must not overlap an input, each other or the workspace, but dx, dr and
+ * di may be slices of one array, their rows side by side. Needs a workspace (vimscan_gated_plan).
  */
 int vimscan_gated_bwd(const vimscan_gated* g, int64_t seg_len, const vimscan_gated_grad* grad,
                       const vimscan_launch* launch);

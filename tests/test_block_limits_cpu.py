@@ -54,3 +54,35 @@ def test_a_norm_plan_is_what_is_launched(io, backward):
             assert info["chunk_len"] == -(-turns // wgs) * at_once
             need = wgs * 3 * d * 4 if backward else 0
             assert need <= info["workspace_bytes"] < need + 256
+
+
+def test_gradient_rows_that_share_elements_are_refused(lib):  # noqa: F811
+    """dx, dr and di (dx and dz) as slices of one array: side by side they are taken (the call then stops at its
+    missing workspace), shifted into each other they are refused."""
+    from bidirectional_selective_scan_amd import block
+    from test_block_abi_cpu import bwd, grad, norm
+    big = addr(11)
+
+    def gated_status(*offsets, ld=(200, 200, 200), io=1):
+        e = 2 if io else 4
+        at = [None if o is None else big + o * e for o in offsets]
+        return bwd(lib, gated(), grad(dx=at[0], dr=at[1], di=at[2], ld_dx=ld[0], ld_dr=ld[1], ld_di=ld[2]), launch(io=io))
+
+    def norm_status(x, z, ld=100):
+        g = block._NormGrad(dsum=addr(8), dn=addr(9), dx=big + 2 * x, dz=big + 2 * z, ld_dx=ld, ld_dz=ld, dresidual=addr(12),
+                            dw_post=addr(13), dgamma=addr(14), dw_pre=addr(15))
+        return lib.vimscan_norm_bwd(ctypes.byref(norm()), ctypes.byref(g), ctypes.byref(launch(d_state=0)))
+
+    for io in (0, 1):
+        assert gated_status(0, 48, 96, io=io) == -7 and gated_status(152, 0, 104, io=io) == -7
+        assert gated_status(0, 48 + 200 * 7, 96, io=io) == -7                     # other rows of the array
+        assert gated_status(0, 200 * 200, 2 * 200 * 200, io=io) == -7             # arrays behind each other
+        assert gated_status(0, None, None, io=io) == -7
+        for shift in (1, 47, 153, 199, 200, 201, 200 * 199 + 47):
+            assert gated_status(0, shift, None, io=io) == -6 and gated_status(shift, 0, None, io=io) == -6
+            assert gated_status(0, None, shift, io=io) == -6
+            assert gated_status(3 * 10 ** 6, 0, shift, io=io) == -6
+    assert gated_status(0, 48, 96, ld=(96, 192, 192)) == -7 and gated_status(0, 47, 96, ld=(96, 192, 192)) == -6
+    assert norm_status(0, 48) == -7 and norm_status(52, 0) == -7
+    for shift in (0, 1, 47, 53, 100, 100 * 150 + 20):
+        assert norm_status(0, shift) == -6 and norm_status(shift, 0) == -6
