@@ -36,7 +36,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// V consecutive elements as they are in memory: one load of 2 to 16 bytes (two of 16 for 8 fp32).
+// V consecutive elements as they are in memory: one load of 2 to 16 bytes.
 // The address is a multiple of the load's size.
 template <typename IO, int V> struct Raw;
 template <> struct Raw<Bf16, 1> {
@@ -66,19 +66,6 @@ template <> struct Raw<Bf16, 4> {
     __device__ __forceinline__ void set(const float* v) { w = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])); }
     __device__ __forceinline__ void store(void* p) const { *static_cast<uint2*>(p) = w; }
 };
-template <> struct Raw<Bf16, 8> {
-    uint4 w;
-    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const uint4*>(p); }
-    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ float get(int k) const {
-        const uint32_t u = k < 2 ? w.x : k < 4 ? w.y : k < 6 ? w.z : w.w;
-        return (k & 1) ? bf16_hi(u) : bf16_lo(u);
-    }
-    __device__ __forceinline__ void set(const float* v) {
-        w = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
-    }
-    __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = w; }
-};
 template <> struct Raw<float, 1> {
     float w;
     __device__ __forceinline__ void load(const void* p) { w = *static_cast<const float*>(p); }
@@ -102,25 +89,6 @@ template <> struct Raw<float, 4> {
     __device__ __forceinline__ float get(int k) const { return k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w; }
     __device__ __forceinline__ void set(const float* v) { w = make_float4(v[0], v[1], v[2], v[3]); }
     __device__ __forceinline__ void store(void* p) const { *static_cast<float4*>(p) = w; }
-};
-template <> struct Raw<float, 8> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const void* p) {
-        a = static_cast<const float4*>(p)[0];
-        b = static_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
-    __device__ __forceinline__ float get(int k) const {
-        return k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : k == 3 ? a.w : k == 4 ? b.x : k == 5 ? b.y : k == 6 ? b.z : b.w;
-    }
-    __device__ __forceinline__ void set(const float* v) {
-        a = make_float4(v[0], v[1], v[2], v[3]);
-        b = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    __device__ __forceinline__ void store(void* p) const {
-        static_cast<float4*>(p)[0] = a;
-        static_cast<float4*>(p)[1] = b;
-    }
 };
 
 // The same from and to any element address: the hardware takes a wide access at any alignment (the

@@ -11,8 +11,8 @@
 // wave (lane swaps), the waves (LDS) and the tiles (through the workspace, see below), and each
 // thread then walks its positions from the state that enters them. So every element is read once and
 // written once at any shape: one long sequence fills the chip as well as many short ones.
-//  * Layout: V consecutive channels per lane (8 or 16 bytes), 64 / V lanes over the channels (rows of
-//    128 or 256 bytes), the other lanes and waves over the positions.
+//  * Layout: V consecutive channels per lane (two, which are 4 bytes in bf16 and 8 in fp32, or one), 64 / V lanes over
+//    the channels (rows of 128 or 256 bytes), the other lanes and waves over the positions.
 //  * A map whose positions contain a sequence start does not depend on the entering state: A = 0, and
 //    maps are applied and composed with the multiplication that gives 0 for a factor 0 whatever the
 //    other one is, so that NaN or infinity in one sequence never reaches the next.
@@ -263,17 +263,14 @@ __device__ __forceinline__ Raw<IO, V> ld_tile(__amdgpu_buffer_rsrc_t r, uint32_t
     } else if constexpr (sizeof(o) == 4) {
         const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, kPolicy);
         __builtin_memcpy(&o, &w, 4);
-    } else if constexpr (sizeof(o) == 8) {
+    } else {
+        static_assert(sizeof(o) == 8, "one or two channels");
         const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, vo, so, kPolicy);
         __builtin_memcpy(&o, &w, 8);
-    } else {
-        const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, vo, so, kPolicy);
-        __builtin_memcpy(&o, &w, 16);
     }
     return o;
 }
 using U2 = uint32_t __attribute__((vector_size(8)));
-using U4 = uint32_t __attribute__((vector_size(16)));
 template <typename IO, int V, int kPolicy>
 __device__ __forceinline__ void st_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so, const float* v) {
     Raw<IO, V> o;
@@ -286,14 +283,11 @@ __device__ __forceinline__ void st_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo, u
         uint32_t w;
         __builtin_memcpy(&w, &o, 4);
         __builtin_amdgcn_raw_buffer_store_b32(w, r, vo, so, kPolicy);
-    } else if constexpr (sizeof(o) == 8) {
+    } else {
+        static_assert(sizeof(o) == 8, "one or two channels");
         U2 w;
         __builtin_memcpy(&w, &o, 8);
         __builtin_amdgcn_raw_buffer_store_b64(w, r, vo, so, kPolicy);
-    } else {
-        U4 w;
-        __builtin_memcpy(&w, &o, 16);
-        __builtin_amdgcn_raw_buffer_store_b128(w, r, vo, so, kPolicy);
     }
 }
 
@@ -319,34 +313,17 @@ __device__ __forceinline__ Map pick(bool c, const Map& f, const Map& g) { return
 // and before: the map of the groups before this lane's in walking order, or after it with kBack.
 template <int CL, bool kBack>
 __device__ __forceinline__ void scan_rows(const Map& f, int lane, Map* total, Map* before) {
-    static_assert(CL == 16 || CL == 32 || CL == 64, "one, two or four position groups in a wave");
+    static_assert(CL == 32 || CL == 64, "one or two position groups in a wave");
     if constexpr (CL == 64) {
         *total = f;
         *before = identity();
-    } else if constexpr (CL == 32) {
+    } else {
         Map lo, hi;
         swap32(f.A, &lo.A, &hi.A);
         swap32(f.H, &lo.H, &hi.H);
         const bool upper = lane & 32;
         *total = kBack ? then(hi, lo) : then(lo, hi);
         *before = kBack ? pick(upper, identity(), hi) : pick(upper, lo, identity());
-    } else {
-        Map e, o, lo, hi;
-        swap16(f.A, &e.A, &o.A);
-        swap16(f.H, &e.H, &o.H);
-        const Map pair = kBack ? then(o, e) : then(e, o);
-        swap32(pair.A, &lo.A, &hi.A);
-        swap32(pair.H, &lo.H, &hi.H);
-        const bool odd = lane & 16, upper = lane & 32;
-        if constexpr (kBack) {
-            const Map b = pick(odd, identity(), o);
-            *total = then(hi, lo);
-            *before = pick(upper, b, then(hi, b));
-        } else {
-            const Map b = pick(odd, e, identity());
-            *total = then(lo, hi);
-            *before = pick(upper, then(lo, b), b);
-        }
     }
 }
 
@@ -511,10 +488,8 @@ __device__ __forceinline__ void forget(Raw<Bf16, V>& r) {
         uint32_t w = r.w;
         asm volatile("" : "+v"(w));
         r.w = static_cast<uint16_t>(w);
-    } else if constexpr (V == 2) {
-        asm volatile("" : "+v"(r.w));
     } else {
-        asm volatile("" : "+v"(r.w.x), "+v"(r.w.y));
+        asm volatile("" : "+v"(r.w));
     }
 }
 template <int V>
@@ -1247,10 +1222,6 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
     for (int v = 0; v < V; ++v) {
         float p, q;
         sum[v] = pt < a.N && live ? sum[v] : 0.0f;
-        if constexpr (CL == 16) {
-            swap16(sum[v], &p, &q);
-            sum[v] = p + q;
-        }
         if constexpr (CL < 64) {
             swap32(sum[v], &p, &q);
             sum[v] = p + q;
