@@ -84,9 +84,10 @@ int check_workspace(const vimscan_launch* l, size_t need, const Span (&ins)[N], 
 
 // Tile of the forward pass. Long tiles hand on half as often and share the work per tile among twice the
 // elements; short ones give more and lighter workgroups. Measured (bf16, us, 128 / 64 tokens): sequences
-// of 65537 x 1536 203 / 257, 16384 x 768 30.2 / 38.1, 512 x 197 x 768 132 / 140; but 1 x 1024 x 768
-// 9.1 / 6.8, 128 x 197 x 384 23.2 / 21.3, 8 x 1025 x 768 17.2 / 16.6 and, where sequences end with
-// the tile, 1024 x 64 x 768 87 / 80. In fp32 the same shapes choose alike.
+// of 65537 x 1536 188 / 235, 16384 x 768 29.0 / 38.3, 512 x 197 x 768 125 / 131; but 1 x 1024 x 768
+// 9.3 / 6.9, 128 x 197 x 384 23.1 / 21.3, 4 x 1025 x 768 12.9 / 11.3 and, where sequences end with
+// the tile, 1024 x 64 x 768 85 / 76. Near its border the rule can be a few percent off: 8 x 1025 x 768 takes 64
+// tokens, 16.0 / 17.0. In fp32 the same shapes choose alike.
 int64_t fwd_tile(int64_t tokens, int64_t length, int64_t ncb) {
     const int64_t wgs = (tokens + kGatedFwdTile - 1) / kGatedFwdTile * ncb;
     return length <= kGatedFwdTileSmall || (length <= 2048 && wgs < 2048) ? kGatedFwdTileSmall : kGatedFwdTile;

@@ -59,16 +59,18 @@ struct NormSpread {
     constexpr int rows() const { return threads() / (lanes * waves); }
 };
 // The spreads from narrow to wide; a row takes the first that holds it. Forward fewer waves with more of a row
-// each; backward, where a channel takes three times the registers, more waves from 1024 channels on (13056 x 1536
-// bf16: 86 us with 8 waves, 93 with 4; 4099 x 8192: 342 us with 16 waves, 577 with 8, and 173 with the weights'
-// gradients in LDS).
-constexpr NormSpread kNormForward[] = {{1, 16, 1, 4}, {1, 32, 1, 4}, {1, 64, 1, 4}, {2, 64, 1, 4}, {3, 64, 1, 4}, {4, 64, 1, 4},
-                                       {2, 64, 4, 4}, {4, 64, 4, 4}, {4, 64, 8, 4}, {4, 64, 16, 4}, {8, 64, 16, 4}};
-constexpr NormSpread kNormBackward[] = {{1, 16, 1, 4}, {1, 32, 1, 4}, {1, 64, 1, 4}, {2, 64, 1, 4}, {3, 64, 1, 4}, {4, 64, 1, 4},
-                                        {1, 64, 8, 4}, {1, 64, 16, 4}, {2, 64, 16, 4}, {4, 64, 16, 4}, {8, 64, 16, 4}};
+// each; backward, where a channel takes three times the registers, more waves past 1024 channels (all stages, fp32
+// residuals: 13056 x 1536 bf16 91 us with 8 waves, 93 with the forward's 4; 4099 x 8192 all bf16 176 us with 16
+// waves, which keep the weights' gradients in LDS, 251 with the forward's 8, which spill).
+constexpr NormSpread kNormForward[] = {{1, 16, 1, 4}, {1, 32, 1, 4}, {1, 64, 1, 4}, {2, 64, 1, 4},
+                                       {3, 64, 1, 4}, {4, 64, 1, 4}, {2, 64, 4, 4}, {4, 64, 4, 4},
+                                       {4, 64, 8, 4}, {4, 64, 16, 4}, {8, 64, 16, 4}};
+constexpr NormSpread kNormBackward[] = {{1, 16, 1, 4}, {1, 32, 1, 4}, {1, 64, 1, 4}, {2, 64, 1, 4},
+                                        {3, 64, 1, 4}, {4, 64, 1, 4}, {1, 64, 8, 4}, {1, 64, 16, 4},
+                                        {2, 64, 16, 4}, {4, 64, 16, 4}, {8, 64, 16, 4}};
 // fp32 rows whose width is no multiple of 4: single channels, either direction.
-constexpr NormSpread kNormSingles[] = {{4, 16, 1, 1}, {4, 32, 1, 1}, {4, 64, 1, 1}, {8, 64, 1, 1}, {4, 64, 4, 1}, {4, 64, 8, 1},
-                                       {8, 64, 8, 1}, {8, 64, 16, 1}, {16, 64, 16, 1}, {32, 64, 16, 1}};
+constexpr NormSpread kNormSingles[] = {{4, 16, 1, 1}, {4, 32, 1, 1}, {4, 64, 1, 1}, {8, 64, 1, 1}, {4, 64, 4, 1},
+                                       {4, 64, 8, 1}, {8, 64, 8, 1}, {8, 64, 16, 1}, {16, 64, 16, 1}, {32, 64, 16, 1}};
 
 // Plan of a block norm. A workgroup takes spread.rows() rows at a time.
 struct NormPlan {

@@ -178,7 +178,8 @@ __device__ __forceinline__ void ld_weight(const float* w, int D, float (&o)[S::N
 // eps) w_pre. Memory bounds it: a row stays in registers from its one read to its one write, and the
 // workgroups walk the rows so that the weights are read once per workgroup and not per row. Measured: 25216
 // x 768 bf16 with fp32 residuals 50 us (271 MB, 5.4 TB/s), 4099 x 8192 all bf16 49 us (269 MB, 5.5 TB/s),
-// 13056 x 1531 fp32 48 us with a gate and no pre-norm (5.0 TB/s); a copy of 256 MiB reaches 5.4 TB/s.
+// 13056 x 1531 fp32 48 us with a gate and no pre-norm (5.0 TB/s); a copy of 256 MiB reaches 5.4 TB/s. 1000 x 16384
+// bf16 51 us (4.5 TB/s); past 16384 channels 72 to 216 registers spill: 500 x 32768 119 us (1.9 TB/s).
 template <typename IO, typename RES, typename S>
 __global__ __launch_bounds__(S::kThreads) void k_norm_fwd(NormArgs a) {
     constexpr int NV = S::NV, L = S::L, W = S::W, V = S::V;
@@ -234,12 +235,15 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_fwd(NormArgs a) {
 
 // Backward: the row's stages again from its inputs (reading them costs less than saved statistics and
 // intermediates would), then the gradients against them. With g = dn w_pre: ds' = dsum + rho2 g - s rho2^3
-// mean(g s); the post-norm's likewise; the gate's through silu' = sg (1 + z (1 - sg)). Memory bounds it: 25216
-// x 768 bf16 82 us (426 MB, 5.2 TB/s), 13056 x 1531 fp32 83 us (400 MB, 4.8 TB/s). The weights' gradients
+// mean(g s); the post-norm's likewise; the gate's through silu' = sg (1 + z (1 - sg)). The weights' gradients
 // of a thread's channels stay with the thread over all its rows, are added up over the workgroup's rows at
-// the end and left for k_norm_cols: no atomics, the same bits every time. Past 4096 channels a thread's registers
-// are short (128 with 16 waves); LDS holds the weights' gradients up to 8192 channels: 4099 x 8192 bf16 173
-// us against 289 with spilled registers. Wider rows spill (1000 x 16384 bf16: 410 us).
+// the end and left for k_norm_cols: no atomics, the same bits every time. Memory bounds it up to 4096 channels:
+// 25216 x 768 bf16 83 us (426 MB, 5.1 TB/s), 25216 x 1024 123 us (568 MB, 4.6 TB/s, one wave a SIMD: 256 registers),
+// 13056 x 1531 fp32 84 us (400 MB, 4.7 TB/s). Past them a thread's registers are short (128 with 16 waves). LDS holds
+// the weights' gradients up to 8192 channels: 4099 x 8192 all bf16 174 us (537 MB, 3.1 TB/s) against 243 with all in
+// registers and spilled; widths there that are no multiple of 4 still spill 18 to 41 (4099 x 8191 bf16 294 us). Past
+// 8192 every form spills 227 to 1229 registers, and scratch memory bounds it: 1000 x 16384 bf16 405 us (360 MB),
+// 500 x 32768 882 us.
 template <typename IO, typename RES, typename S>
 __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
     constexpr int NV = S::NV, L = S::L, W = S::W, V = S::V;
@@ -477,9 +481,9 @@ void launch_singles(const NormArgs& a, const NormPlan& p, hipStream_t s) {
     launch_first<float, float, kBack, true, kNormSingles, std::size(kNormSingles)>(a, p, s);
 }
 
-// Widths that are no multiple of four: in bf16 vectors at any alignment are still twice as fast as single
-// channels (13056 x 1531: 76 us against 180 forward, 116 against 253 backward), in fp32, where a single
-// channel is a full access, they are slower (108 against 74 us, 163 against 110).
+// Widths that are no multiple of four: in bf16 vectors at any alignment are faster than single channels
+// (13056 x 1531, all stages: 75 us against 120 forward, 119 against 190 backward; 54 and 92 at 1536), in fp32, where
+// a single channel is a full access, they are slower (105 against 74 us, 161 against 132).
 void launch_typed(const NormArgs& a, const NormPlan& p, int io, bool back, hipStream_t s) {
     const bool whole = a.D % 4 == 0;
     if (io == VIMSCAN_F32) {

@@ -251,7 +251,7 @@ struct TileRows {
 
 // Cache policy of the rows' accesses. kOnce: the lines are not wanted again and are evicted first. Taken
 // where every row starts on a line, so that no two workgroups share one: 65537 x 1536 bf16 forward 188 us
-// instead of 203, 128 x 197 x 768 backward 67 instead of 72; where workgroups do share lines it makes them be
+// instead of 201, 128 x 197 x 768 backward 67 instead of 73; where workgroups do share lines it makes them be
 // fetched twice (32 x 1024 x 770: 81 us instead of 65).
 constexpr int kPlain = 0, kOnce = 2;
 template <typename IO, int V, int kPolicy>
@@ -343,10 +343,10 @@ struct ChainLds {
 };
 
 // A value handed over: two 64-bit words (second words apart, so that a wave's are contiguous), the value and
-// the value xor the dispatch's tag, each stored and loaded on its own (device-coherent, no order between them). A reader takes the value when the two
-// differ by exactly this dispatch's tag, so words of earlier dispatches, arbitrary bytes and half a
-// value never pass, the memory needs no clearing, and neither side waits for one access before the
-// next: a value costs its reader one trip to memory after it was stored.
+// the value xor the dispatch's tag, each stored and loaded on its own (device-coherent, no order between
+// them). A reader takes the value when the two differ by exactly this dispatch's tag, so words of earlier
+// dispatches, arbitrary bytes and half a value never pass, the memory needs no clearing, and neither side
+// waits for one access before the next: a value costs its reader one trip to memory after it was stored.
 // w: the wave's first word (the same for all lanes).
 __device__ __forceinline__ void hand_over(uint64_t* w, int64_t second, int lane, uint64_t tag, float x, float y) {
     const uint64_t v = __float_as_uint(x) | (static_cast<uint64_t>(__float_as_uint(y)) << 32);
@@ -822,10 +822,11 @@ __device__ __forceinline__ void bwd_alone(ChainLds& l, int j, int cb, uint64_t t
 
 // Forward pass: a tile of TILE positions x 64 channels. The maps compose as (A2, H2)(A1, H1) = (A2 A1, A2 H1 +
 // H2), so a tile needs only the state that enters it and no element is read twice. Measured: 1 x 65537 x
-// 1536 bf16 188 us (805 MB, 4.3 TB/s), 8 x 1025 x 768 bf16 16.5 us, 128 x 197 x 768 bf16 with saved states 39
+// 1536 bf16 188 us (805 MB, 4.3 TB/s), 8 x 1025 x 768 bf16 16.8 us, 128 x 197 x 768 bf16 with saved states 39
 // us (4.0 TB/s), 33k x 384 fp32 packed 45 us (4.5 TB/s). Bound: in fp32 memory; in bf16 the hand-over's
-// latency beside three exponentials, two reciprocals and a square root per element (the long case without a
-// hand-over: 163 us).
+// latency beside three exponentials, two reciprocals and a square root per element (as many tokens in sequences
+// of 128, which hand nothing over: 166 us). Rows off cache lines: 32 x 1024 x 770 bf16 65 us (202 MB, 3.1 TB/s), as
+// the halves of a line are wanted by workgroups of neighbouring ids, which run on different XCDs.
 template <typename IO, int V, int TILE, bool kChain, int kPolicy>
 __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_fwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = TILE / TG;
@@ -972,8 +973,9 @@ __global__ __launch_bounds__(256, TILE < 128 ? 5 : sizeof(IoElem<IO>) == 2 && V 
 // last one), d = dy + e is the state's and a d goes on to the position before. With u, a, m as above, s = sigmoid(r),
 // g = sigmoid(i): dx = d m g, di = d m x g (1 - g), w = d (u a h_prev - g x a^2 u / m), dr = w (1 - s),
 // dlam = sigmoid(lam) / softplus(lam) sum w. A tile takes half the forward's positions: it holds four
-// inputs and both walks. Measured: 128 x 197 x 768 bf16 64 us (271 MB, 4.2 TB/s), 33k x 384 fp32 packed 82 us
-// (358 MB, 4.4 TB/s). Bound: the vector unit's instructions and the hand-over's latency together.
+// inputs and both walks. Measured: 128 x 197 x 768 bf16 65 us (271 MB, 4.2 TB/s), 33k x 384 fp32 packed 83 us
+// (358 MB, 4.3 TB/s); rows off cache lines 32 x 1024 x 770 bf16 118 us (353 MB, 3.0 TB/s), single channels
+// 16 x 1000 x 333 bf16 41 us (75 MB, 1.8 TB/s). Bound: the vector unit's instructions and the hand-over's latency together.
 template <typename IO, int V, bool kChain, int kPolicy>
 __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void k_gated_bwd(GatedArgs a) {
     constexpr int CL = kGatedBlock / V, TG = 256 / CL, T = kGatedBwdTile / TG;
@@ -1068,7 +1070,10 @@ __global__ __launch_bounds__(256, sizeof(IoElem<IO>) == 2 && V > 1 ? 4 : 3) void
 #pragma unroll
         for (int k = T - 1; k >= 0; --k)
 #pragma unroll
-            for (int v = 0; v < V; ++v) e[v].H = k == T - 1 ? gr[k].get(v) : fmaf(av[k == T - 1 ? k : k + 1][v], e[v].H, gr[k].get(v));
+            for (int v = 0; v < V; ++v) {
+                const float own = gr[k].get(v);
+                e[v].H = k == T - 1 ? own : fmaf(av[k == T - 1 ? k : k + 1][v], e[v].H, own);
+            }
 #pragma unroll
         for (int v = 0; v < V; ++v) e[v].H *= av[0][v];
     } else {
@@ -1344,10 +1349,9 @@ bool record(const vimscan_launch* l, int k) {
     return hipEventRecord(static_cast<hipEvent_t>(l->scan_events[k]), static_cast<hipStream_t>(l->stream)) == hipSuccess;
 }
 
-// kVec channels per lane where every row of every tensor is aligned to them: two are enough to read rows
-// of 128 or 256 bytes a half wave, and leave a thread more positions of fewer channels than four (the work
-// per thread and channel outside the element loops: maps, waits, carries); measured 40 us with either at
-// 128 x 197 x 768 bf16 forward, 89 us against 136 us backward.
+// kVec channels per lane where every row of every tensor is aligned to them: half as many accesses as with one,
+// of rows of 128 or 256 bytes a half wave. Measured at 128 x 197 x 768, two channels and one: bf16 37 and 44 us
+// forward, 67 and 85 backward; fp32 59 and 65, 109 and 119.
 constexpr int kVec = 2;
 
 // Rows of one tensor, as far as the choice of a kernel goes.
@@ -1374,8 +1378,8 @@ void launch_fwd_any(const GatedArgs& a, const GatedPlan& p, hipStream_t s) {
     constexpr size_t e = sizeof(IoElem<IO>);
     const RowsOf rows[] = {{a.x, a.ld_x}, {a.r, a.ld_r}, {a.i, a.ld_i}, {a.y, a.D}};
     const bool vec = a.D % kVec == 0 && rows_at(rows, e, kVec * e), big = p.tile == kGatedFwdTile;
-    // small calls do not gain from kOnce: their inputs are often in the caches still (8 x 1025 x 768 bf16 15.7
-    // us, with it 16.7; 256 x 51 x 1536, 7,000 workgroups, 46.4 and 41.6)
+    // small calls do not gain from kOnce: their inputs are often in the caches still (8 x 1025 x 768 bf16 16.9
+    // us, with it 17.1; 256 x 51 x 1536, 5,000 workgroups, 46.0 and 41.4)
     const bool once = rows_at(rows, e, 128) && (big || p.wgs >= 2048);
     if (vec && big && once) launch_fwd<IO, kVec, kGatedFwdTile, kOnce>(a, p, s);
     else if (vec && once) launch_fwd<IO, kVec, kGatedFwdTileSmall, kOnce>(a, p, s);

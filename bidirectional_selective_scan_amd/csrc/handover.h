@@ -1,6 +1,6 @@
-// Device side of a hand-over between workgroups of one kernel: a publisher stores its values with
-// device-coherent stores, waits until they have completed and then stores the dispatch's tag; a
-// reader polls the tag word before it issues device-coherent loads of the values.
+// What hand-overs between workgroups of one kernel share: a tag of the dispatch, by which a reader knows that
+// what it reads was written by this dispatch. Each kernel describes its own protocol (the chunked scans a tag word
+// behind the values, the gated recurrence a tag within every value).
 #ifndef VIMSCAN_HANDOVER_H
 #define VIMSCAN_HANDOVER_H
 
@@ -10,7 +10,7 @@
 
 namespace vimscan_dev {
 
-// Reads of a tag word before a wait gives up (about a second).
+// Reads of a tag word before a wait of the chunked scans gives up (about a second).
 constexpr int kSpinLimit = 1 << 20;
 
 // llvm.amdgcn.dispatch.id: the dispatch packet's index in its queue, which the command processor
