@@ -13,7 +13,8 @@ def __getattr__(name):
     if name in ("bidir_fwd", "workspace_bytes", "status_string", "VimscanError", "lib_path",
                 "load_library", "launch_info", "gated_fwd", "gated_step", "gated_info", "block_norm", "norm_info",
                 "PreparedGated", "PreparedGatedGrad", "PreparedGatedStep", "PreparedBlockNorm",
-                "PreparedBlockNormGrad"):
+                "PreparedBlockNormGrad", "linattn_fwd", "linattn_step", "linattn_info", "PreparedLinAttn",
+                "PreparedLinAttnGrad", "PreparedLinAttnStep"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

@@ -52,7 +52,8 @@ EXPORTED = ("vimscan_bidir_fwd", "vimscan_bidir_conv_fwd", "vimscan_fwd", "vimsc
             "vimscan_workspace_bytes", "vimscan_status_string", "vimscan_version", "vimscan_ncssd_fwd",
             "vimscan_ncssd_plan", "vimscan_bidir_order_fwd", "vimscan_bidir_fwd_noalloc", "vimscan_wait_timeouts",
             "vimscan_gated_fwd", "vimscan_gated_bwd", "vimscan_gated_step", "vimscan_gated_plan", "vimscan_norm_fwd",
-            "vimscan_norm_bwd", "vimscan_norm_plan", "vimscan_gated_wait_reads", "vimscan_gated_alone")
+            "vimscan_norm_bwd", "vimscan_norm_plan", "vimscan_gated_wait_reads", "vimscan_gated_alone",
+            "vimscan_linattn_fwd", "vimscan_linattn_bwd", "vimscan_linattn_step", "vimscan_linattn_plan")
 
 # Size of the static scratch array behind vimscan_bidir_fwd_noalloc (VIMSCAN_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 96 << 20
@@ -98,8 +99,9 @@ def load_library():
             lib.vimscan_ncssd_plan.argtypes = [ctypes.POINTER(_Launch), ctypes.c_int64, ctypes.POINTER(_Plan)]
             lib.vimscan_wait_timeouts.restype = ctypes.c_int
             lib.vimscan_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
-            from . import block
+            from . import attention, block
             block.declare(lib)
+            attention.declare(lib)
             _lib = lib
     return _lib
 
@@ -376,10 +378,16 @@ def ncssd_fwd(x, B, C, m, seg_len: int = 0, out=None, chunk_len: int = 0, worksp
 _BLOCK_NAMES = ("GATED_STRIDE", "GatedInputs", "PreparedBlockNorm", "PreparedBlockNormGrad", "PreparedGated",
                 "PreparedGatedGrad", "PreparedGatedStep", "block_norm", "gated_alone", "gated_fwd", "gated_info", "gated_step",
                 "gated_wait_reads", "norm_info")
+# So are those of linear attention (attention.py).
+_ATTENTION_NAMES = ("LinAttnInputs", "PreparedLinAttn", "PreparedLinAttnGrad", "PreparedLinAttnStep", "linattn_fwd",
+                    "linattn_info", "linattn_step")
 
 
 def __getattr__(name):
     if name in _BLOCK_NAMES:
         from . import block
         return getattr(block, name)
+    if name in _ATTENTION_NAMES:
+        from . import attention
+        return getattr(attention, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

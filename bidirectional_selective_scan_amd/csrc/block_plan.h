@@ -11,8 +11,6 @@
 namespace vimscan_host {
 
 constexpr int kGatedStride = VIMSCAN_GATED_STRIDE;
-// Rows of a tile (128 at most) lie within the 2^31 bytes that one buffer resource's offsets span.
-constexpr int64_t kMaxRowStride = int64_t(1) << 22;
 // Workgroups of 256 threads: a grid holds fewer than 2^32 threads. (So few tiles also keep every position of
 // the last tile below 2^31.)
 constexpr int64_t kMaxGatedWgs = (int64_t(1) << 24) - 1;

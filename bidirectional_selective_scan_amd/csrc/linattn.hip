@@ -1,0 +1,511 @@
+// Linear attention with a decay for each head for AMD MI355X (gfx950): the entry points of include/vimscan.h
+// (vimscan_linattn_*) and the kernels around the passes (linattn_device.h).
+//
+// Forward: one pass. Where sequences and heads alone do not fill the chip, or are long, sequences are cut into segments: every
+// segment's own state first (k_lin_pass, kLocal), a fold of those over the sequence (k_lin_fold), then the pass
+// with every segment from its state.
+// Backward: the same states, and those of the gradient from the other end; then three passes, for dq, dk and dv.
+// The decays' gradient is exp(g_t) <S_{t-1}, D_t> = sum over u >= t of (q_u . dq_u - k_u . dk_u), from the segment's end, where it is
+// <S, E>. The dq and dk passes leave those products, without the pair of a token with itself, which is in both and
+// cancels; k_lin_decay_grad adds them up in fp64.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "linattn_device.h"
+#include "vimscan.h"
+
+namespace vimscan_dev {
+
+extern template void launch_lin_pass<Bf16, kLocal>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<Bf16, kForward>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<Bf16, kGradient>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kLocal>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kForward>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kGradient>(const LinArgs&, bool, hipStream_t);
+
+}  // namespace vimscan_dev
+
+namespace {
+
+using namespace vimscan_dev;
+using vimscan_host::LinPlan;
+
+// Replaces every segment's own state by the state it starts from, in the order of the walk (from the end: from the last
+// segment on): X = init; for each segment: its place <- X, X = decay X + (what was there). One element a thread.
+__global__ __launch_bounds__(256) void k_lin_fold(LinArgs a, float* states, const float* tot, const float* init, int from_end) {
+    const int64_t ks = static_cast<int64_t>(a.K) * a.V, per_seq = a.H * ks, all = a.nseq * per_seq;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; t < all; t += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t seq = t / per_seq, at = t - seq * per_seq, h = at / ks;
+        int64_t first = seq * a.segs, count = a.segs;
+        if (a.offsets) {
+            int64_t lo, hi;
+            lin_bounds(a, seq, &lo, &hi);
+            first = lin_base(a, seq);
+            count = (hi - lo + a.seg - 1) / a.seg;
+            if (count < 1) count = 1;
+        }
+        float x = init ? init[t] : 0.0f;
+        // (an empty sequence's one segment has no decay and adds nothing: both were written by its pass)
+        for (int64_t j = 0; j < count; ++j) {
+            const int64_t slot = first + (from_end ? count - 1 - j : j);
+            float* p = states + slot * per_seq + at;
+            const float mine = *p;
+            *p = x;
+            x = fmaf(tot[slot * a.H + h], x, mine);
+        }
+    }
+}
+
+struct DecayGradArgs {
+    const float* rq;     // [blocks][tokens][H]: q . dq and k . dk, pairs of a token with itself left out
+    const float* rk;
+    const float* cdot;   // [slots][H][blocks]: <S, E> at the segment's end
+    int32_t blocks;
+    float* by_token;     // [tokens][H] or NULL
+    float* by_head;      // [slots][H], the segments' sums, or NULL
+};
+
+__global__ __launch_bounds__(64 * kWaves) void k_lin_decay_grad(LinArgs a, DecayGradArgs d) {
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    if (task >= a.slots * a.H) return;
+    const int64_t slot = task / a.H, h = task - slot * a.H;
+    const LinSegment sg = lin_segment(a, slot);
+    double carry = 0.0, mine = 0.0;
+    if (sg.valid) {
+        for (int b = 0; b < d.blocks; ++b) carry += d.cdot[task * d.blocks + b];
+        for (int64_t at = 0; at < sg.n; at += 64) {
+            const int64_t i = sg.n - 1 - at - lane;       // walking position
+            const bool in = i >= 0;
+            const int64_t tok = in ? (a.rev ? sg.first + sg.n - 1 - i : sg.first + i) : 0;
+            double v = 0.0;
+            if (in)
+                for (int b = 0; b < d.blocks; ++b) {
+                    const int64_t k = (b * a.tokens + tok) * a.H + h;
+                    v += static_cast<double>(d.rq[k]) - static_cast<double>(d.rk[k]);
+                }
+            v = half_wave_sums(v);
+            const double low = lane_value(v, 31);
+            v += carry + (lane >= 32 ? low : 0.0);
+            carry = lane_value(v, 63);
+            if (in) {
+                if (d.by_token) d.by_token[tok * a.H + h] = static_cast<float>(v);
+                mine += v;
+            }
+        }
+    }
+    if (!d.by_head) return;
+    for (int m = 1; m < 64; m *= 2) mine += __shfl_xor(mine, m);
+    if (lane == 0) d.by_head[task] = static_cast<float>(mine);
+}
+
+// The gradient of a decay per head: the segments' sums in a fixed order. One workgroup a head.
+__global__ __launch_bounds__(256) void k_lin_head_sum(const float* part, int64_t slots, int64_t H, float* out) {
+    __shared__ double lds[256];
+    const int tid = static_cast<int>(threadIdx.x);
+    double s = 0.0;
+    for (int64_t k = tid; k < slots; k += 256) s += part[k * H + blockIdx.x];
+    lds[tid] = s;
+    for (int m = 128; m > 0; m /= 2) {
+        __syncthreads();
+        if (tid < m) lds[tid] += lds[tid + m];
+    }
+    if (tid == 0) out[blockIdx.x] = static_cast<float>(lds[0]);
+}
+
+// Gradients of shared rows: the sum over the heads of a group, in their order, rounded once.
+template <typename IO>
+__global__ __launch_bounds__(256) void k_lin_group_sum(const float* part, int64_t rows, int rep, int D, void* out) {
+    const int64_t all = rows * D;   // rows: tokens x groups
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; t < all; t += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = t / D, c = t - row * D;
+        const float* p = part + row * rep * D + c;
+        float s = 0.0f;
+        for (int r = 0; r < rep; ++r) s += p[static_cast<int64_t>(r) * D];
+        Raw<IO, 1> o;
+        o.set(&s);
+        o.store(static_cast<IoElem<IO>*>(out) + t);
+    }
+}
+
+// One token: S' = e^g S + k^T v, y = scale q S'. The states' traffic bounds it (8 bytes for 5 operations). A workgroup takes a
+// row's head and up to 4 CL of its value channels: CL lanes of V channels to a state row, the rows spread over the rest.
+struct LinStepArgs {
+    LinRows q, k, v;
+    int32_t H, dk, dv, blocks;
+    const float* g;
+    int64_t ld_g;
+    float scale;
+    float* state;
+    int64_t nslots;
+    const int32_t* slots_in;
+    const int32_t* slots_out;
+    void* y;
+};
+template <typename IO, int V, int CL>
+__global__ __launch_bounds__(256) void k_lin_step(LinStepArgs a) {
+    using E = IoElem<IO>;
+    constexpr int kRows = 256 / CL;
+    __shared__ float lds[kWaves][CL][V];
+    const int tid = static_cast<int>(threadIdx.x), cl = tid % CL, rg = tid / CL;
+    const int64_t id = blockIdx.x;
+    const int block = static_cast<int>(id % a.blocks);
+    const int64_t rest = id / a.blocks, h = rest % a.H, b = rest / a.H;
+    const int c = (block * CL + cl) * V;
+    const int64_t from = a.slots_in ? a.slots_in[b] : b;
+    const int64_t to = a.slots_out ? a.slots_out[b] : from;
+    const bool in = from >= 0 && from < a.nslots && to >= 0 && to < a.nslots;
+    const bool live = c < a.dv;
+    float sum[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+    if (in && live) {
+        const int64_t ks = static_cast<int64_t>(a.dk) * a.dv;
+        const float* src = a.state + (from * a.H + h) * ks + c;
+        float* dst = a.state + (to * a.H + h) * ks + c;
+        const E* q = static_cast<const E*>(a.q.p) + b * a.q.ld + h / a.q.div * a.q.hs;
+        const E* k = static_cast<const E*>(a.k.p) + b * a.k.ld + h / a.k.div * a.k.hs;
+        const E* vp = static_cast<const E*>(a.v.p) + b * a.v.ld + h * a.v.hs + c;
+        const float2 g = as_pair(log2_decay(a.ld_g ? a.g[b * a.ld_g + h] : a.g[h]));
+        const float dec = fast_exp2(g.x + g.y);
+        float val[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            Raw<IO, 1> x;
+            x.load(vp + v);
+            val[v] = x.get(0);
+        }
+#pragma unroll 4
+        for (int r = rg; r < a.dk; r += kRows) {
+            Raw<float, V> s;
+            s.load(src + static_cast<int64_t>(r) * a.dv);
+            Raw<IO, 1> qr, kr;
+            qr.load(q + r);
+            kr.load(k + r);
+            float n[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                n[v] = fmaf(dec, s.get(v), kr.get(0) * val[v]);
+                sum[v] = fmaf(qr.get(0), n[v], sum[v]);
+            }
+            s.set(n);
+            s.store(dst + static_cast<int64_t>(r) * a.dv);
+        }
+    }
+    // over the wave's rows, then over the waves in their order
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int m = CL; m < 64; m *= 2) sum[v] += __shfl_xor(sum[v], m);
+    const int wave = tid >> 6;
+    if ((tid & 63) < CL)
+#pragma unroll
+        for (int v = 0; v < V; ++v) lds[wave][cl][v] = sum[v];
+    __syncthreads();
+    if (tid >= CL || !live) return;
+    E* y = static_cast<E*>(a.y) + (b * a.H + h) * a.dv + c;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) s += lds[w][cl][v];
+        s *= a.scale;
+        Raw<IO, 1> o;
+        o.set(&s);
+        o.store(y + v);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host
+
+LinArgs common_args(const vimscan_linattn* p, const vimscan_launch* l, const LinPlan& pl) {
+    LinArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.H = static_cast<int32_t>(pl.H);
+    a.g = p->log_decay;
+    a.ld_g = p->ld_decay;
+    a.offsets = p->offsets;
+    a.tokens = pl.tokens;
+    a.Lp = pl.Lp;
+    a.seg = pl.seg > 0 ? pl.seg : 1;
+    a.nseq = static_cast<int32_t>(pl.nseq);
+    a.segs = static_cast<int32_t>(pl.segs);
+    a.split = pl.split;
+    a.rev = (l->flags & VIMSCAN_FLAG_REVERSE) ? 1 : 0;
+    a.slots = pl.slots;
+    a.key_scale = a.out_scale = 1.0f;
+    return a;
+}
+
+// The roles of a pass: reader, key, value.
+void set_roles(LinArgs* a, const LinRows& r, const LinRows& k, const LinRows& v, int64_t K, int64_t V) {
+    a->r = r;
+    a->k = k;
+    a->v = v;
+    a->K = static_cast<int32_t>(K);
+    a->V = static_cast<int32_t>(V);
+    a->blocks = static_cast<int32_t>(vimscan_host::lin_blocks(V));
+    a->waves = a->slots * a->H * a->blocks;
+}
+
+void run_pass(int io, bool vec, LinKind kind, const LinArgs& a, hipStream_t s) {
+    if (io == VIMSCAN_F32) {
+        if (kind == kLocal) launch_lin_pass<float, kLocal>(a, vec, s);
+        else if (kind == kForward) launch_lin_pass<float, kForward>(a, vec, s);
+        else launch_lin_pass<float, kGradient>(a, vec, s);
+    } else {
+        if (kind == kLocal) launch_lin_pass<Bf16, kLocal>(a, vec, s);
+        else if (kind == kForward) launch_lin_pass<Bf16, kForward>(a, vec, s);
+        else launch_lin_pass<Bf16, kGradient>(a, vec, s);
+    }
+}
+
+unsigned some_blocks(int64_t elements) {
+    const int64_t n = (elements + 255) / 256;
+    return static_cast<unsigned>(n < 65536 ? n : 65536);
+}
+
+void run_fold(const LinArgs& a, float* states, const float* tot, const float* init, bool from_end, hipStream_t s) {
+    const int64_t all = static_cast<int64_t>(a.nseq) * a.H * a.K * a.V;
+    hipLaunchKernelGGL(k_lin_fold, dim3(some_blocks(all)), dim3(256), 0, s, a, states, tot, init, from_end ? 1 : 0);
+}
+
+// Whether a dimension's pieces of consecutive channels are whole (load_channels).
+bool whole_pieces(int64_t d) { return d <= 32 ? d % 8 == 0 : d <= 64 ? d % 4 == 0 : d % 8 == 0; }
+// Whether bf16 rows start at multiples of four bytes.
+bool by_words(const void* p, int64_t ld, int64_t hs) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0 && hs % 2 == 0; }
+bool use_vectors(const vimscan_linattn* p, const vimscan_linattn_grad* g, const void* y, const LinPlan& pl, int io) {
+    if (!whole_pieces(pl.dk) || !whole_pieces(pl.dv)) return false;
+    if (io == VIMSCAN_F32) return true;
+    if (!by_words(p->q, p->ld_q, p->hs_q) || !by_words(p->k, p->ld_k, p->hs_k) || !by_words(p->v, p->ld_v, p->hs_v))
+        return false;
+    if (!g) return by_words(y, 0, 0);
+    return by_words(g->dy, g->dy ? g->ld_dy : 0, g->dy ? g->hs_dy : 0) && by_words(g->dq, 0, 0) && by_words(g->dk, 0, 0) &&
+           by_words(g->dv, 0, 0);
+}
+
+bool record(const vimscan_launch* l, int k) {
+    if (!l->scan_events[0] || !l->scan_events[1]) return true;
+    return hipEventRecord(static_cast<hipEvent_t>(l->scan_events[k]), static_cast<hipStream_t>(l->stream)) == hipSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+int vimscan_linattn_fwd(const vimscan_linattn* p, int64_t seg_len, void* y, float* h_last, const vimscan_launch* launch) {
+    if (!p || !launch) return VIMSCAN_ERR_NULL;
+    LinPlan pl;
+    int rc = vimscan_host::make_linattn_plan(launch, seg_len, p->heads, p->groups, p->offsets != nullptr, p->nseq, false, &pl);
+    if (rc != VIMSCAN_OK) return rc;
+    rc = vimscan_host::check_linattn_call(p, y, h_last, nullptr, launch, pl);
+    if (rc != VIMSCAN_OK || pl.waves == 0) return rc;
+    if (pl.tokens == 0 && !h_last) return VIMSCAN_OK;
+    const int io = launch->io_dtype;
+    const bool vec = use_vectors(p, nullptr, y, pl, io);
+    const int32_t rep = static_cast<int32_t>(pl.H / pl.G);
+    const LinRows q = {p->q, p->ld_q, p->hs_q, rep}, k = {p->k, p->ld_k, p->hs_k, rep}, v = {p->v, p->ld_v, p->hs_v, 1};
+    char* ws = static_cast<char*>(launch->workspace);
+    hipStream_t s = static_cast<hipStream_t>(launch->stream);
+    LinArgs a = common_args(p, launch, pl);
+    set_roles(&a, q, k, v, pl.dk, pl.dv);
+    if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
+    a.s0 = p->h0;
+    a.s0_row = pl.dv;
+    a.s0_col = 1;
+    if (pl.split) {
+        float* states = reinterpret_cast<float*>(ws + pl.off_s);
+        float* tot = reinterpret_cast<float*>(ws + pl.off_tot);
+        LinArgs b = a;
+        b.s_end = states;
+        b.tot = tot;
+        run_pass(io, vec, kLocal, b, s);
+        run_fold(a, states, tot, p->h0, false, s);
+        a.s0 = states;
+        a.s0_by_slot = 1;
+    }
+    a.out_scale = p->scale;
+    a.o = y;
+    a.s_end = h_last;
+    run_pass(io, vec, kForward, a, s);
+    if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
+    return VIMSCAN_OK;
+}
+
+int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan_linattn_grad* grad,
+                        const vimscan_launch* launch) {
+    if (!p || !grad || !launch) return VIMSCAN_ERR_NULL;
+    LinPlan pl;
+    int rc = vimscan_host::make_linattn_plan(launch, seg_len, p->heads, p->groups, p->offsets != nullptr, p->nseq, true, &pl);
+    if (rc != VIMSCAN_OK) return rc;
+    rc = vimscan_host::check_linattn_call(p, nullptr, nullptr, grad, launch, pl);
+    if (rc != VIMSCAN_OK) return rc;
+    hipStream_t s = static_cast<hipStream_t>(launch->stream);
+    const bool by_head = p->ld_decay == 0;
+    LinArgs a = common_args(p, launch, pl);
+    if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
+    if (pl.tokens == 0) {
+        // gradients of empty sequences' states, and of decays that no token has
+        if (pl.waves > 0 && grad->dh0) {
+            const LinRows none = {nullptr, 0, 0, 1};
+            set_roles(&a, none, none, none, pl.dk, pl.dv);
+            a.back = 1;
+            a.s0 = grad->dh_last;
+            a.s0_row = pl.dv;
+            a.s0_col = 1;
+            a.s_end = grad->dh0;
+            run_pass(launch->io_dtype, true, kGradient, a, s);
+        }
+        if (by_head && grad->dlog_decay)
+            hipLaunchKernelGGL(k_lin_head_sum, dim3(static_cast<unsigned>(pl.H)), dim3(256), 0, s,
+                               static_cast<const float*>(nullptr), int64_t(0), pl.H, grad->dlog_decay);
+        if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
+        return VIMSCAN_OK;
+    }
+    const int io = launch->io_dtype;
+    const bool vec = use_vectors(p, grad, nullptr, pl, io);
+    const int32_t rep = static_cast<int32_t>(pl.H / pl.G);
+    const LinRows q = {p->q, p->ld_q, p->hs_q, rep}, k = {p->k, p->ld_k, p->hs_k, rep}, v = {p->v, p->ld_v, p->hs_v, 1};
+    const LinRows dy = {grad->dy, grad->dy ? grad->ld_dy : 0, grad->dy ? grad->hs_dy : 0, 1};
+    char* ws = static_cast<char*>(launch->workspace);
+    auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    a.s0_row = pl.dv;
+    a.s0_col = 1;
+    if (pl.split) {
+        LinArgs b = a;
+        set_roles(&b, k, k, v, pl.dk, pl.dv);
+        b.s_end = at(pl.off_s);
+        b.tot = at(pl.off_tot);
+        run_pass(io, vec, kLocal, b, s);
+        run_fold(b, at(pl.off_s), at(pl.off_tot), p->h0, false, s);
+        b = a;
+        set_roles(&b, q, q, dy, pl.dk, pl.dv);
+        b.back = 1;
+        b.key_scale = p->scale;
+        b.s_end = at(pl.off_e);
+        run_pass(io, vec, kLocal, b, s);
+        run_fold(b, at(pl.off_e), at(pl.off_tot), grad->dh_last, true, s);
+    }
+    const bool decays = grad->dlog_decay != nullptr;
+    const float* s0 = pl.split ? at(pl.off_s) : p->h0;
+    const float* e0 = pl.split ? at(pl.off_e) : grad->dh_last;
+    const int32_t by_slot = pl.split;
+    const bool shared = rep > 1;
+    LinArgs b = a;   // dq: forward, the state transposed
+    set_roles(&b, dy, v, k, pl.dv, pl.dk);
+    b.s0 = s0;
+    b.s0_row = 1;
+    b.s0_col = pl.dv;
+    b.s0_by_slot = by_slot;
+    b.out_scale = p->scale;
+    b.o = shared ? at(pl.off_pq) : grad->dq;
+    b.o_f32 = shared;
+    if (decays) {
+        b.w = q;
+        b.dots = at(pl.off_rq);
+        b.e = e0;
+        b.e_row = 1;
+        b.e_col = pl.dv;
+        b.e_by_slot = by_slot;
+        b.cdot = at(pl.off_cd);
+    }
+    const int32_t qblocks = b.blocks;
+    run_pass(io, vec, kGradient, b, s);
+    b = a;           // dk: from the end, the gradient of the state transposed
+    set_roles(&b, v, dy, q, pl.dv, pl.dk);
+    b.back = 1;
+    b.key_scale = p->scale;
+    b.s0 = e0;
+    b.s0_row = 1;
+    b.s0_col = pl.dv;
+    b.s0_by_slot = by_slot;
+    b.o = shared ? at(pl.off_pk) : grad->dk;
+    b.o_f32 = shared;
+    if (decays) {
+        b.w = k;
+        b.dots = at(pl.off_rk);
+    }
+    run_pass(io, vec, kGradient, b, s);
+    b = a;           // dv, and the gradient of the state before the sequence
+    set_roles(&b, k, q, dy, pl.dk, pl.dv);
+    b.back = 1;
+    b.key_scale = p->scale;
+    b.s0 = e0;
+    b.s0_by_slot = by_slot;
+    b.s_end = grad->dh0;
+    b.o = grad->dv;
+    run_pass(io, vec, kGradient, b, s);
+    if (decays) {
+        DecayGradArgs d = {at(pl.off_rq), at(pl.off_rk), at(pl.off_cd), qblocks, by_head ? nullptr : grad->dlog_decay,
+                           by_head ? at(pl.off_hs) : nullptr};
+        const int64_t waves = pl.slots * pl.H;
+        hipLaunchKernelGGL(k_lin_decay_grad, dim3(static_cast<unsigned>((waves + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0, s,
+                           b, d);
+        if (by_head)
+            hipLaunchKernelGGL(k_lin_head_sum, dim3(static_cast<unsigned>(pl.H)), dim3(256), 0, s, d.by_head, pl.slots, pl.H,
+                               grad->dlog_decay);
+    }
+    if (shared) {
+        const int64_t rows = pl.tokens * pl.G;
+        const float* part[] = {at(pl.off_pq), at(pl.off_pk)};
+        void* out[] = {grad->dq, grad->dk};
+        for (int i = 0; i < 2; ++i) {
+            const dim3 grid(some_blocks(rows * pl.dk));
+            if (io == VIMSCAN_F32)
+                hipLaunchKernelGGL(k_lin_group_sum<float>, grid, dim3(256), 0, s, part[i], rows, rep, static_cast<int>(pl.dk), out[i]);
+            else
+                hipLaunchKernelGGL(k_lin_group_sum<Bf16>, grid, dim3(256), 0, s, part[i], rows, rep, static_cast<int>(pl.dk), out[i]);
+        }
+    }
+    if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
+    return VIMSCAN_OK;
+}
+
+int vimscan_linattn_step(const vimscan_linattn* p, float* state, int64_t nslots, const int32_t* slots_in,
+                         const int32_t* slots_out, void* y, const vimscan_launch* launch) {
+    const int rc = vimscan_host::check_linattn_step(p, state, nslots, slots_in, slots_out, y, launch);
+    if (rc != VIMSCAN_OK) return rc;
+    if (launch->batch == 0) return VIMSCAN_OK;
+    const int64_t H = p->heads, dv = launch->d_inner / H;
+    const int32_t rep = static_cast<int32_t>(H / p->groups);
+    LinStepArgs a;
+    a.q = {p->q, p->ld_q, p->hs_q, rep};
+    a.k = {p->k, p->ld_k, p->hs_k, rep};
+    a.v = {p->v, p->ld_v, p->hs_v, 1};
+    a.H = static_cast<int32_t>(H);
+    a.dk = static_cast<int32_t>(launch->d_state);
+    a.dv = static_cast<int32_t>(dv);
+    a.g = p->log_decay;
+    a.ld_g = p->ld_decay;
+    a.scale = p->scale;
+    a.state = state;
+    a.nslots = nslots;
+    a.slots_in = slots_in;
+    a.slots_out = slots_out;
+    a.y = y;
+    hipStream_t s = static_cast<hipStream_t>(launch->stream);
+    if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
+    // four channels a lane where every state row starts at 16 bytes
+    const bool vec = dv % 4 == 0 && reinterpret_cast<uintptr_t>(state) % 16 == 0;
+    const int wide = !vec ? 64 : dv <= 16 ? 16 : dv <= 32 ? 32 : 64;   // channels of a workgroup
+    a.blocks = static_cast<int32_t>((dv + wide - 1) / wide);
+    const dim3 grid(static_cast<unsigned>(launch->batch * H * a.blocks));
+    const bool f32 = launch->io_dtype == VIMSCAN_F32;
+    auto run = [&](auto io) {
+        using IO = decltype(io);
+        if (!vec) hipLaunchKernelGGL((k_lin_step<IO, 1, 64>), grid, dim3(256), 0, s, a);
+        else if (wide == 16) hipLaunchKernelGGL((k_lin_step<IO, 4, 4>), grid, dim3(256), 0, s, a);
+        else if (wide == 32) hipLaunchKernelGGL((k_lin_step<IO, 4, 8>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_lin_step<IO, 4, 16>), grid, dim3(256), 0, s, a);
+    };
+    if (f32) run(float{});
+    else run(Bf16{});
+    if (hipGetLastError() != hipSuccess || !record(launch, 1)) return VIMSCAN_ERR_HIP;
+    return VIMSCAN_OK;
+}
+
+}  // extern "C"

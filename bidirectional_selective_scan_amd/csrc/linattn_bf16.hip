@@ -1,0 +1,9 @@
+// The passes of linear attention in bf16 (linattn_device.h).
+
+#include "linattn_launch.h"
+
+namespace vimscan_dev {
+template void launch_lin_pass<Bf16, kLocal>(const LinArgs&, bool, hipStream_t);
+template void launch_lin_pass<Bf16, kForward>(const LinArgs&, bool, hipStream_t);
+template void launch_lin_pass<Bf16, kGradient>(const LinArgs&, bool, hipStream_t);
+}  // namespace vimscan_dev

@@ -1,0 +1,9 @@
+// The passes of linear attention in fp32 (linattn_device.h).
+
+#include "linattn_launch.h"
+
+namespace vimscan_dev {
+template void launch_lin_pass<float, kLocal>(const LinArgs&, bool, hipStream_t);
+template void launch_lin_pass<float, kForward>(const LinArgs&, bool, hipStream_t);
+template void launch_lin_pass<float, kGradient>(const LinArgs&, bool, hipStream_t);
+}  // namespace vimscan_dev

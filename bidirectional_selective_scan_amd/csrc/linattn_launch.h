@@ -1,0 +1,35 @@
+// Launches of the pass of linear attention: the instance for the head's dimensions.
+#ifndef VIMSCAN_LINATTN_LAUNCH_H
+#define VIMSCAN_LINATTN_LAUNCH_H
+
+#include "linattn_device.h"
+
+namespace vimscan_dev {
+
+template <typename IO, int NK, int NV, bool kVec, int kKind>
+void launch_lin_instance(const LinArgs& a, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>((a.waves + kWaves - 1) / kWaves));
+    hipLaunchKernelGGL((k_lin_pass<IO, NK, NV, kVec, kKind>), grid, dim3(64 * kWaves), 0, s, a);
+}
+template <typename IO, int NK, bool kVec, int kKind>
+void launch_lin_outputs(const LinArgs& a, hipStream_t s) {
+    if (vimscan_host::lin_output_tiles(a.V) == 2) launch_lin_instance<IO, NK, 2, kVec, kKind>(a, s);
+    else launch_lin_instance<IO, NK, 4, kVec, kKind>(a, s);
+}
+template <typename IO, bool kVec, int kKind>
+void launch_lin_dims(const LinArgs& a, hipStream_t s) {
+    switch (vimscan_host::lin_contract_tiles(a.K)) {
+        case 2: return launch_lin_outputs<IO, 2, kVec, kKind>(a, s);
+        case 4: return launch_lin_outputs<IO, 4, kVec, kKind>(a, s);
+        default: return launch_lin_outputs<IO, 8, kVec, kKind>(a, s);
+    }
+}
+template <typename IO, int kKind>
+void launch_lin_pass(const LinArgs& a, bool vec, hipStream_t s) {
+    if (vec) launch_lin_dims<IO, true, kKind>(a, s);
+    else launch_lin_dims<IO, false, kKind>(a, s);
+}
+
+}  // namespace vimscan_dev
+
+#endif  // VIMSCAN_LINATTN_LAUNCH_H

@@ -1,0 +1,48 @@
+// Host side of linear attention: execution plans and every argument check an entry point makes before
+// its first HIP call. Plain C++, as plan.h.
+#ifndef VIMSCAN_LINATTN_PLAN_H
+#define VIMSCAN_LINATTN_PLAN_H
+
+#include <cstddef>
+#include <cstdint>
+
+#include "vimscan.h"
+
+namespace vimscan_host {
+
+constexpr int64_t kLinMaxDim = 128;    // of dk and dv
+constexpr int kLinChunk = 32;          // tokens that a wave works on at once
+constexpr int kLinWaves = 4;           // waves of a workgroup, each with work of its own
+constexpr int64_t kMaxHeadStride = int64_t(1) << 38;
+// Workgroups of 256 threads: a grid holds fewer than 2^32 threads.
+constexpr int64_t kMaxLinWgs = (int64_t(1) << 24) - 1;
+
+// Tiles of 16 that a wave's state has over a contracted dimension (at least as wide as it) and over an
+// output dimension, of which a wave takes a block.
+constexpr int lin_contract_tiles(int64_t d) { return d <= 32 ? 2 : d <= 64 ? 4 : 8; }
+constexpr int lin_output_tiles(int64_t d) { return d <= 32 ? 2 : 4; }
+constexpr int64_t lin_blocks(int64_t d) { return (d + 16 * lin_output_tiles(d) - 1) / (16 * lin_output_tiles(d)); }
+
+struct LinPlan {
+    int64_t tokens, nseq, Lp;          // Lp: tokens per sequence, 0 when packed
+    int64_t H, G, dk, dv;
+    bool packed, split;
+    int64_t seg, segs, slots;          // split: tokens per segment, segments per uniform sequence; segments in all
+    int64_t waves;                     // of the pass that writes y (or dv)
+    // workspace: the segments' states and decays; backward also their gradients, the terms of the decays'
+    // gradient, and gradients of shared q and k by head
+    size_t off_s, off_e, off_tot, off_rq, off_rk, off_cd, off_hs, off_pq, off_pk, ws;
+};
+
+// Whether a segment's index space, base(q) = offsets[q] / seg + q, gives every sequence slots of its own: sequence
+// q has floor(offsets[q+1] / seg) - floor(offsets[q] / seg) + 1 >= ceil(length / seg) of them.
+int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, int64_t groups, bool packed, int64_t nseq,
+                      bool backward, LinPlan* p);
+int check_linattn_call(const vimscan_linattn* a, const void* y, const float* h_last, const vimscan_linattn_grad* grad,
+                       const vimscan_launch* l, const LinPlan& p);
+int check_linattn_step(const vimscan_linattn* a, const float* state, int64_t nslots, const int32_t* slots_in,
+                       const int32_t* slots_out, const void* y, const vimscan_launch* l);
+
+}  // namespace vimscan_host
+
+#endif  // VIMSCAN_LINATTN_PLAN_H

@@ -1,9 +1,10 @@
 /*
  * vimscan.h -- C ABI of the bidirectional selective scan on AMD MI355X (gfx950), with its
  * variants (directional convolution in front, forward only with the auxiliary swap, a given token
- * order) and the NC-SSD global-state form (declared further down), and of two operators of the
+ * order) and the NC-SSD global-state form (declared further down), and of the operators of the
  * blocks around such scans, each with its backward pass: the gated linear recurrence
- * (vimscan_gated_*) and the block norm (vimscan_norm_*), also declared further down.
+ * (vimscan_gated_*), the block norm (vimscan_norm_*), linear attention with a decay for each head
+ * (vimscan_linattn_*) and the layer norm (vimscan_layernorm_*), also declared further down.
  *
  * The operation (Vision Mamba page, section 2.2 "bidirectional state-space modelling": a
  * forward path over the tokens in raster order and a backward path over them in reverse, the
@@ -71,10 +72,10 @@ enum vimscan_status {
     VIMSCAN_ERR_CONV = -11,     /* vimscan_conv.k outside 1..4 */
     VIMSCAN_ERR_SCRATCH = -12,  /* vimscan_bidir_fwd_noalloc: the call needs more scratch than
                                    VIMSCAN_NOALLOC_SCRATCH_BYTES */
-    VIMSCAN_ERR_PARAM = -13     /* gated recurrence, block norm: c or eps is not positive and
-                                   finite, a row stride is below d_inner or at least 2^22, or
-                                   arguments that exclude each other (each entry point names its
-                                   own) */
+    VIMSCAN_ERR_PARAM = -13     /* gated recurrence, linear attention, norms: c or eps is not positive
+                                   and finite, scale not finite, a row stride is below the row's width
+                                   or at least 2^22, or arguments that exclude each other (each entry
+                                   point names its own) */
 };
 
 /* dtype of x, dt, z, B_*, C_* and y. */
@@ -96,8 +97,8 @@ enum vimscan_io_dtype { VIMSCAN_F32 = 0, VIMSCAN_BF16 = 1 };
    functions need it to size the forward-only plan; vimscan_bidir_fwd, vimscan_bidir_conv_fwd and
    vimscan_bidir_order_fwd reject it (VIMSCAN_ERR_FLAGS). */
 #define VIMSCAN_FLAG_FORWARD_ONLY 4
-/* vimscan_gated_fwd and vimscan_gated_bwd: every sequence is walked from its last token to its
-   first (nothing is flipped or copied). Only for them. */
+/* vimscan_gated_fwd, vimscan_gated_bwd, vimscan_linattn_fwd and vimscan_linattn_bwd: every sequence is
+   walked from its last token to its first (nothing is flipped or copied). Only for them. */
 #define VIMSCAN_FLAG_REVERSE 8
 /* vimscan_norm_fwd and vimscan_norm_bwd: the gate silu(z) multiplies the post-norm's output
    instead of its input. Only for them. */
@@ -109,7 +110,7 @@ typedef struct vimscan_launch {
     int64_t seqlen;         /* L >= 0 (the folded stream length when seg_len > 0) */
     int64_t d_inner;        /* Di >= 0 */
     int64_t d_state;        /* N; 16 for the scans; 16, 32 or 64 for vimscan_ncssd_fwd; 1 for the
-                               gated recurrence; 0 for the block norm */
+                               gated recurrence; dk for linear attention; 0 for the norms */
     int32_t io_dtype;       /* enum vimscan_io_dtype */
     int32_t flags;          /* VIMSCAN_FLAG_* bits */
     int64_t chunk_len;      /* 0: the library picks; > 0: tokens per chunk of the chunked scan,
@@ -453,6 +454,91 @@ int vimscan_norm_bwd(const vimscan_norm* p, const vimscan_norm_grad* grad, const
    seq_tokens = 1, chunk_len = rows per workgroup, chunks 1, workgroups, kernels (with every weight
    gradient wanted), workspace_bytes. Host only. */
 int vimscan_norm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan);
+
+/*
+ * Linear attention with a decay for each head: one fp32 state of dk x dv per head. For every sequence
+ * and head h, over the sequence's tokens t in walking order (memory order, or from the last token to the
+ * first with VIMSCAN_FLAG_REVERSE), q and k those of the head's group h / (heads / groups):
+ *   S_t = exp(g_t) S_{t-1} + k_t^T v_t,   S before the first token = h0[seq][h] (0 without h0)
+ *   y[t][h] = scale * q_t S_t;   h_last[seq][h] = S after the sequence's last token
+ * g_t is log_decay[h], the same for every token (ld_decay 0), or log_decay[t][h]. It is usually negative;
+ * below -200, -infinity among them, it counts as -200 (a factor that is 0 in fp32). Empty sequences, seg_len and offsets as for
+ * vimscan_gated_fwd. An infinity may come out as NaN. NaN and infinities of a token reach no token
+ * before it in walking order, no other head (but those that share the token's q and k) and no other
+ * sequence.
+ *
+ * launch->d_state is dk and launch->d_inner heads * dv, dk and dv 1 to 128 (VIMSCAN_ERR_SHAPE). groups
+ * divides heads. Token rows of q, k and v are ld_* elements apart (at least dk, dv; below 2^22), the heads
+ * or groups of a token hs_* elements (0 <= hs_* < 2^38): VIMSCAN_ERR_PARAM. So they may be slices of one projection's output, or
+ * one sequence in [heads][tokens][d] order. ld_decay is 0 or at least heads, below 2^22. h0, h_last, y and
+ * the gradients are dense. flags: VIMSCAN_FLAG_REVERSE only; chunk_len must be 0. tokens = batch * seqlen < 2^31.
+ */
+typedef struct vimscan_linattn {
+    const void* q;          /* [tokens][groups][dk] io dtype */
+    const void* k;          /* [tokens][groups][dk] */
+    const void* v;          /* [tokens][heads][dv] */
+    int64_t ld_q, ld_k, ld_v;
+    int64_t hs_q, hs_k, hs_v;
+    const float* log_decay; /* [heads] (ld_decay 0) or [tokens][heads], rows ld_decay apart */
+    int64_t ld_decay;
+    const float* h0;        /* [sequences][heads][dk][dv] or NULL */
+    const int32_t* offsets; /* [nseq + 1] or NULL */
+    int64_t nseq;           /* sequences when offsets is set */
+    int64_t heads, groups;
+    float scale;            /* finite */
+} vimscan_linattn;
+
+/* Forward pass: y [tokens][heads][dv] io dtype; h_last [sequences][heads][dk][dv] fp32 or NULL. They must
+   not overlap an input, each other or the workspace (of strided arrays the whole extent counts). Pointers
+   are aligned to their element size. Needs a workspace where long sequences are cut into segments that run
+   side by side (vimscan_linattn_plan). An empty call (no tokens) only writes h_last. */
+int vimscan_linattn_fwd(const vimscan_linattn* p, int64_t seg_len, void* y, float* h_last,
+                        const vimscan_launch* launch);
+
+/* Gradients of vimscan_linattn_fwd: dy and dh_last are those of y and h_last (either may be NULL: zero);
+   dq, dk [tokens][groups][dk], dv [tokens][heads][dv] io dtype, dense, must be set; dlog_decay (fp32, [heads], or
+   [tokens][heads] dense with ld_decay set) and dh0 may be NULL (not wanted). */
+typedef struct vimscan_linattn_grad {
+    const void* dy;         /* [tokens][heads][dv], tokens ld_dy, heads hs_dy apart */
+    int64_t ld_dy, hs_dy;
+    const float* dh_last;
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dlog_decay;
+    float* dh0;
+} vimscan_linattn_grad;
+
+/*
+ * Backward pass. With D_t = scale q_t^T dy_t + exp(g_{t+1}) D_{t+1} (behind the last token: dh_last):
+ *   dq_t = scale S_t dy_t,  dk_t = D_t v_t,  dv_t = k_t D_t,  dg_t = exp(g_t) <S_{t-1}, D_t>,
+ *   dh0 = exp(g) D at the first token
+ * dq and dk are summed over the heads of a group, dlog_decay [heads] over all tokens, in a fixed order: the
+ * same bits on every run. Nothing but the inputs is kept from the forward pass. The gradients
+ * must not overlap an input, each other or the workspace, which every call with tokens needs
+ * (vimscan_linattn_plan). A NaN or infinity may reach gradients of up to 31 tokens beyond those that
+ * depend on it, in its sequence and head.
+ */
+int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan_linattn_grad* grad,
+                        const vimscan_launch* launch);
+
+/*
+ * One token of launch->batch independent streams (launch->seqlen must be 1): row b takes its states from
+ * state[slots_in[b]], applies one step and writes the new ones to state[slots_out[b]] and y [batch][heads][dv].
+ * state is a pool of nslots blocks [heads][dk][dv], fp32; slots as for vimscan_gated_step: NULL slots_in:
+ * row b uses slot b, NULL slots_out: the slot it was read from; a row with a slot outside the pool is skipped
+ * and its y is zero; a slot that a row writes must not be read or written by another row. h0, offsets and nseq of *p are
+ * ignored; flags must be 0; no workspace.
+ */
+int vimscan_linattn_step(const vimscan_linattn* p, float* state, int64_t nslots, const int32_t* slots_in,
+                         const int32_t* slots_out, void* y, const vimscan_launch* launch);
+
+/* Plan of a vimscan_linattn_fwd (backward 0) or vimscan_linattn_bwd (backward 1) call: sequences; seq_tokens
+   (0 with offsets); chunk_len = tokens per segment, chunks = segments per sequence (with offsets: segments at
+   most), 1 and the sequence's tokens (0 with offsets) when sequences are not cut; workgroups of the pass that
+   writes the outputs; kernels (with every gradient wanted); workspace_bytes. packed: 1 when offsets are set. Host only. */
+int vimscan_linattn_plan(const vimscan_launch* launch, int64_t seg_len, int64_t heads, int64_t groups, int packed,
+                         int64_t nseq, int backward, vimscan_plan* plan);
 
 /* Fills *plan for a call with this launch and seg_len (workspace fields of launch are
    ignored). Host only; no HIP call. Returns VIMSCAN_OK or the error the call would return. */
