@@ -22,9 +22,11 @@ namespace vimscan_dev {
 extern template void launch_lin_pass<Bf16, kLocal>(const LinArgs&, bool, hipStream_t);
 extern template void launch_lin_pass<Bf16, kForward>(const LinArgs&, bool, hipStream_t);
 extern template void launch_lin_pass<Bf16, kGradient>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<Bf16, kGradientDots>(const LinArgs&, bool, hipStream_t);
 extern template void launch_lin_pass<float, kLocal>(const LinArgs&, bool, hipStream_t);
 extern template void launch_lin_pass<float, kForward>(const LinArgs&, bool, hipStream_t);
 extern template void launch_lin_pass<float, kGradient>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kGradientDots>(const LinArgs&, bool, hipStream_t);
 
 }  // namespace vimscan_dev
 
@@ -32,6 +34,7 @@ namespace {
 
 using namespace vimscan_dev;
 using vimscan_host::LinPlan;
+constexpr int kWaves = 4;   // waves of the workgroups of the kernels here
 
 // Replaces every segment's own state by the state it starts from, in the order of the walk (from the end: from the last
 // segment on): X = init; for each segment: its place <- X, X = decay X + (what was there). One element a thread.
@@ -256,11 +259,13 @@ void run_pass(int io, bool vec, LinKind kind, const LinArgs& a, hipStream_t s) {
     if (io == VIMSCAN_F32) {
         if (kind == kLocal) launch_lin_pass<float, kLocal>(a, vec, s);
         else if (kind == kForward) launch_lin_pass<float, kForward>(a, vec, s);
-        else launch_lin_pass<float, kGradient>(a, vec, s);
+        else if (kind == kGradient) launch_lin_pass<float, kGradient>(a, vec, s);
+        else launch_lin_pass<float, kGradientDots>(a, vec, s);
     } else {
         if (kind == kLocal) launch_lin_pass<Bf16, kLocal>(a, vec, s);
         else if (kind == kForward) launch_lin_pass<Bf16, kForward>(a, vec, s);
-        else launch_lin_pass<Bf16, kGradient>(a, vec, s);
+        else if (kind == kGradient) launch_lin_pass<Bf16, kGradient>(a, vec, s);
+        else launch_lin_pass<Bf16, kGradientDots>(a, vec, s);
     }
 }
 
@@ -274,13 +279,14 @@ void run_fold(const LinArgs& a, float* states, const float* tot, const float* in
     hipLaunchKernelGGL(k_lin_fold, dim3(some_blocks(all)), dim3(256), 0, s, a, states, tot, init, from_end ? 1 : 0);
 }
 
-// Whether a dimension's pieces of consecutive channels are whole (load_channels).
-bool whole_pieces(int64_t d) { return d <= 32 ? d % 8 == 0 : d <= 64 ? d % 4 == 0 : d % 8 == 0; }
-// Whether bf16 rows start at multiples of four bytes.
-bool by_words(const void* p, int64_t ld, int64_t hs) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0 && hs % 2 == 0; }
+// Whether rows are whole pieces of 16 bytes that start at multiples of four bytes (the hardware takes those as they are).
 bool use_vectors(const vimscan_linattn* p, const vimscan_linattn_grad* g, const void* y, const LinPlan& pl, int io) {
-    if (!whole_pieces(pl.dk) || !whole_pieces(pl.dv)) return false;
+    const int64_t n = io == VIMSCAN_F32 ? 4 : 8;
+    if (pl.dk % n != 0 || pl.dv % n != 0) return false;
     if (io == VIMSCAN_F32) return true;
+    auto by_words = [](const void* q, int64_t ld, int64_t hs) {
+        return reinterpret_cast<uintptr_t>(q) % 4 == 0 && ld % 2 == 0 && hs % 2 == 0;
+    };
     if (!by_words(p->q, p->ld_q, p->hs_q) || !by_words(p->k, p->ld_k, p->hs_k) || !by_words(p->v, p->ld_v, p->hs_v))
         return false;
     if (!g) return by_words(y, 0, 0);
@@ -414,7 +420,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
         b.cdot = at(pl.off_cd);
     }
     const int32_t qblocks = b.blocks;
-    run_pass(io, vec, kGradient, b, s);
+    run_pass(io, vec, decays ? kGradientDots : kGradient, b, s);
     b = a;           // dk: from the end, the gradient of the state transposed
     set_roles(&b, v, dy, q, pl.dv, pl.dk);
     b.back = 1;
@@ -429,7 +435,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
         b.w = k;
         b.dots = at(pl.off_rk);
     }
-    run_pass(io, vec, kGradient, b, s);
+    run_pass(io, vec, decays ? kGradientDots : kGradient, b, s);
     b = a;           // dv, and the gradient of the state before the sequence
     set_roles(&b, k, q, dy, pl.dk, pl.dv);
     b.back = 1;

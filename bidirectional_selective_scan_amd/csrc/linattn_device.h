@@ -19,9 +19,8 @@
 //   * the state has rows = key channels, columns = value channels; row m of its tile i is channel NK m + i, column m
 //     of its tile j is channel NV m + j, so a lane reads NK (or NV) consecutive channels of its tokens, and as the left
 //     operand of r S it is in place as well.
-// bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed keys) are split
-// into two bf16 parts, both multiplied: 16 of their 24 bits, 2^-17 relative, far below the outputs' rounding; one part alone
-// would leave 2^-9 in the state, which is fp32 in memory. fp32: fp32 matrix instructions.
+// bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed values) are split
+// into two or three bf16 parts, each multiplied: the decayed values, which make the state, into three, as it is fp32 in memory. fp32: fp32 matrix instructions.
 // Sums of g are in fp64, and their differences taken from a pair of fp32, so that a token of strong decay does not cost its
 // neighbours digits.
 #ifndef VIMSCAN_LINATTN_DEVICE_H
@@ -37,7 +36,6 @@
 namespace vimscan_dev {
 
 constexpr int kChunk = vimscan_host::kLinChunk;
-constexpr int kWaves = vimscan_host::kLinWaves;
 // An offset outside every buffer resource: the hardware gives 0 for such a load and drops such a store.
 constexpr uint32_t kOutside = 0x80000000u;
 constexpr int kRsrcFlags = 0x00020000;
@@ -52,7 +50,8 @@ using S2 = uint16_t __attribute__((ext_vector_type(2)));
 enum LinKind {
     kLocal,    // the state that a segment adds, from nothing
     kForward,  // the operator itself
-    kGradient  // a gradient, and its part of the decays'
+    kGradient,     // a gradient
+    kGradientDots  // a gradient, with its part of the decays'
 };
 
 // [tokens][heads / div][D] with strides in elements.
@@ -82,7 +81,7 @@ struct LinArgs {
     float* tot;                // kLocal: the segment's decay
     void* o;                   // [tokens][H][V], dense
     int32_t o_f32;             // in fp32 whatever the io type
-    // kGradient, where the decays' gradient is wanted: dots[block][token][head] = w . o without a token's pair with itself
+    // kGradientDots: dots[block][token][head] = w . o without a token's pair with itself
     LinRows w;
     float* dots;
     const float* e;            // gradient of the state behind the segment (as s0); cdot[slot][head][block] = <S, e>
@@ -162,7 +161,9 @@ __device__ __forceinline__ const float* lin_state(const float* p, int32_t by_slo
 }
 
 // ---------------------------------------------------------------------------------------------
-// Rows in registers
+// Rows. A chunk's rows of an array go from memory to registers in pieces of 16 bytes, consecutive lanes taking consecutive
+// pieces (a lane's own operands are 16 to 64 bytes of a row of its own: loaded as such, the address unit takes 64 rows
+// an instruction and bounds the pass), and from there to a tile in LDS, from which the operands are read.
 
 // 4 N consecutive channels of one token, from channel 4 N grp on.
 template <typename IO, int N> struct RowPart;
@@ -176,105 +177,119 @@ template <int N> struct RowPart<float, N> {
 };
 // N consecutive channels, from channel N col on, of the tokens 4 grp + 0..3 and 16 + 4 grp + 0..3 of a chunk.
 template <typename IO, int N> struct ColPart;
-template <int N> struct ColPart<Bf16, N> {
-    uint32_t w[8][N / 2];
-    __device__ __forceinline__ float get(int t, int k) const { return (k & 1) ? bf16_hi(w[t][k / 2]) : bf16_lo(w[t][k / 2]); }
-};
-template <int N> struct ColPart<float, N> {
-    float w[8][N];
-    __device__ __forceinline__ float get(int t, int k) const { return w[t][k]; }
-};
+template <int N> struct ColPart<Bf16, N> { uint32_t w[8][N / 2]; };
+template <int N> struct ColPart<float, N> { float w[8][N]; };
 
-// n dwords at an offset.
-template <int kDwords>
-__device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t rsrc, uint32_t vo, uint32_t* o) {
-    if constexpr (kDwords == 1) {
-        o[0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, vo, 0, 0);
-    } else if constexpr (kDwords == 2) {
-        const U2v w = __builtin_bit_cast(U2v, __builtin_amdgcn_raw_buffer_load_b64(rsrc, vo, 0, 0));
-        o[0] = w[0];
-        o[1] = w[1];
-    } else {
-        static_assert(kDwords % 4 == 0, "whole vectors");
+// A tile of kChunk rows of 16 N channels. Rows are 16 bytes longer than their channels, which spreads the lanes' rows over the banks.
+template <typename IO, int N>
+struct Tile {
+    static constexpr int e = sizeof(IoElem<IO>), kRow = 16 * N * e + 16, kBytes = kChunk * kRow;
+    static constexpr int kPieces = N * e, kLoads = kChunk * kPieces / 64;   // pieces of a row, loads of a lane
+    static constexpr int kChannels = 16 / e;                                // of a piece
+    // the lane's piece of its first row and of each that follows (its rows are 64 / kPieces apart)
+    __device__ __forceinline__ static int piece(int lane) { return lane % kPieces; }
+    __device__ __forceinline__ static int row(int lane, int k) { return lane / kPieces + k * (64 / kPieces); }
+
+    __device__ __forceinline__ static void put(char* tile, int lane, const U4 (&x)[kLoads]) {
+        char* p = tile + row(lane, 0) * kRow + piece(lane) * 16;
 #pragma unroll
-        for (int k = 0; k < kDwords / 4; ++k) {
-            const U4 w = __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, vo + 16 * k, 0, 0));
+        for (int k = 0; k < kLoads; ++k) *reinterpret_cast<U4*>(p + k * (64 / kPieces) * kRow) = x[k];
+    }
+    __device__ __forceinline__ static void part(const char* tile, int row, int grp, RowPart<IO, N>& o) {
+        const U4* p = reinterpret_cast<const U4*>(tile + row * kRow + 4 * N * e * grp);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[4 * k + j] = w[j];
+        for (int k = 0; k < N * e / 4; ++k) {
+            const U4 w = p[k];
+            __builtin_memcpy(&o.w[16 / e * k / (e == 2 ? 2 : 1)], &w, 16);
         }
     }
-}
-
-// N channels from channel c of a row at an offset, those past D read as 0. kVec: all or none of them are below D.
-template <typename IO, int N, bool kVec, typename W>
-__device__ __forceinline__ void load_channels(__amdgpu_buffer_rsrc_t rsrc, uint32_t row, int c, int D, W* out) {
-    constexpr int e = sizeof(IoElem<IO>);
-    uint32_t* o = reinterpret_cast<uint32_t*>(out);
-    if constexpr (kVec) {
-        load_dwords<N * e / 4>(rsrc, c < D ? row + static_cast<uint32_t>(c * e) : kOutside, o);
-    } else {
+    // row0: the row of the lane's first token, step: from one to the next
+    __device__ __forceinline__ static void columns(const char* tile, int row0, int step, int col, ColPart<IO, N>& o) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const uint32_t at = c + k < D ? row + static_cast<uint32_t>((c + k) * e) : kOutside;
-            if constexpr (e == 4) {
-                o[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
-            } else {
-                const uint32_t w = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0));
-                if (k & 1) o[k / 2] |= w << 16;
-                else o[k / 2] = w;
-            }
+        for (int k = 0; k < 8; ++k) {
+            const char* p = tile + (row0 + ((k & 4) * 4 + (k & 3)) * step) * kRow + N * e * col;
+            if constexpr (N * e == 4) __builtin_memcpy(o.w[k], __builtin_assume_aligned(p, 4), 4);
+            else if constexpr (N * e == 8) __builtin_memcpy(o.w[k], __builtin_assume_aligned(p, 8), 8);
+            else __builtin_memcpy(o.w[k], __builtin_assume_aligned(p, 16), N * e);
         }
     }
+};
+
+// A value that the compiler takes as new: what depends on it is formed anew in every chunk, in an instruction or two, and does not
+// take a register over the loop.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
-// One array's rows of a head: where they are, and a chunk of them as a buffer resource.
+// A lane's piece of a row at an offset in memory: kChannels channels from c on, those past D as 0. kVec: all or none are.
 template <typename IO, bool kVec>
+__device__ __forceinline__ U4 load_piece(__amdgpu_buffer_rsrc_t rsrc, uint32_t row, int c, int D) {
+    constexpr int e = sizeof(IoElem<IO>), n = 16 / e;
+    if constexpr (kVec) {
+        return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, c < D ? row + static_cast<uint32_t>(c * e) : kOutside, 0, 0));
+    } else {
+        U4 o = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const uint32_t at = c + k < D ? row + static_cast<uint32_t>((c + k) * e) : kOutside;
+            if constexpr (e == 4) o[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+            else o[k / 2] |= static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0))) << 16 * (k & 1);
+        }
+        return o;
+    }
+}
+
+// One array's rows of a head: where they are, and a chunk of them as a buffer resource. A lane's offsets in a chunk are
+// the same for every chunk; the resource moves.
+template <typename IO>
 struct HeadRows {
     uint64_t base;
     uint32_t ld;        // bytes from token to token
     int D;
-    __amdgpu_buffer_rsrc_t rsrc;
     __device__ __forceinline__ void init(const LinRows& x, int64_t h, int d) {
         constexpr int e = sizeof(IoElem<IO>);
         base = reinterpret_cast<uint64_t>(x.p) + static_cast<uint64_t>(h / x.div * x.hs * e);
         ld = static_cast<uint32_t>(x.ld * e);
         D = x.p ? d : 0;    // (an array that is absent reads as 0)
     }
-    // the rows of tokens first .. first + n, n <= kChunk
-    __device__ __forceinline__ void chunk(int64_t first, int n) {
+    // the rows of tokens first .. first + n, n <= kChunk (none: everything reads as 0)
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int64_t first, int n) const {
         constexpr int e = sizeof(IoElem<IO>);
         const int64_t at = uniform(static_cast<int64_t>(base + static_cast<uint64_t>(first) * ld));
-        rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, D > 0 ? (n - 1) * ld + D * e : 0, kRsrcFlags);
+        return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, D > 0 && n > 0 ? (n - 1) * ld + D * e : 0,
+                                                 kRsrcFlags);
     }
-    // the lane's part of row t of a chunk (t = its token in memory order; outside 0 .. n - 1: zeros)
-    template <int N>
-    __device__ __forceinline__ void part(int t, int grp, RowPart<IO, N>& o) const {
-        constexpr int e = sizeof(IoElem<IO>);
-        const uint32_t row = static_cast<uint32_t>(t) * ld;
-        // (pieces of N channels; of two rather eight at once)
-        constexpr int P = N == 2 ? 8 : N;
+    // a lane's pieces of a chunk, from channel c0 on
+    template <int N, bool kVec>
+    __device__ __forceinline__ void load(int64_t first, int n, int c0, int lane, U4 (&o)[Tile<IO, N>::kLoads]) const {
+        using T = Tile<IO, N>;
+        const auto rsrc = chunk(first, n);
+        const int c = c0 + T::piece(static_cast<int>(opaque(lane))) * T::kChannels;
+        const uint32_t row = static_cast<uint32_t>(T::row(static_cast<int>(opaque(lane)), 0)) * ld;
 #pragma unroll
-        for (int k = 0; k < 4 * N; k += P) load_channels<IO, P, kVec>(rsrc, row, 4 * N * grp + k, D, &o.w[k * e / 4]);
-    }
-    template <int N>
-    __device__ __forceinline__ void columns(int (&t)[8], int c, ColPart<IO, N>& o) const {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) load_channels<IO, N, kVec>(rsrc, static_cast<uint32_t>(t[k]) * ld, c, D, o.w[k]);
+        for (int k = 0; k < T::kLoads; ++k) o[k] = load_piece<IO, kVec>(rsrc, row + static_cast<uint32_t>(k * (64 / T::kPieces)) * ld, c, D);
     }
 };
 
 // ---------------------------------------------------------------------------------------------
-// Products. Two or three numbers that stand for one: in bf16 a value and its remainder.
+// Products. In bf16 a number in fp32 is the sum of kParts of bf16, each the rounding of what the ones before it leave: 2^-9,
+// 2^-18 or 2^-27 of it are lost.
 
+template <int kParts>
 struct Split8 {
-    U4 hi, lo;
+    U4 w[kParts];
+    // the pair (a, b) at dword i
+    __device__ __forceinline__ void pair(int i, float a, float b) {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+            const uint32_t h = bf16_pair(a, b);
+            w[p][i] = h;
+            a -= bf16_lo(h);
+            b -= bf16_hi(h);
+        }
+    }
 };
-// The pair (a, b) at dword i of a split operand.
-__device__ __forceinline__ void split_pair(Split8& s, int i, float a, float b) {
-    const uint32_t h = bf16_pair(a, b);
-    s.hi[i] = h;
-    s.lo[i] = bf16_pair(a - bf16_lo(h), b - bf16_hi(h));
-}
 __device__ __forceinline__ V4f mfma(U4 a, U4 b, V4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V8bf, a), __builtin_bit_cast(V8bf, b), c, 0, 0, 0);
 }
@@ -296,7 +311,7 @@ __device__ __forceinline__ U4 col_operand(const ColPart<Bf16, N>& p, int k) {
     return o;
 }
 
-// o += (state)^T (rows), for one tile of value channels and 16 tokens.
+// The scores of 16 keys (rows) and 16 readers (columns).
 template <typename IO, int NK>
 __device__ __forceinline__ V4f scores(const RowPart<IO, NK>& k, const RowPart<IO, NK>& r) {
     V4f c = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -364,24 +379,45 @@ __device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// The pass: one wave per segment, head and block of 16 NV output channels. NK tiles of 16 hold the K contracted
-// channels.
+// The pass: one wave (a workgroup) per segment, head and block of 16 NV output channels. NK tiles of 16 hold the K
+// contracted channels. A chunk's rows are loaded while the chunk before is worked on.
+
+// Waves a SIMD that the registers are cut for.
+template <typename IO, int NK, int NV> constexpr int kLinWavesPerSimd = vimscan_host::lin_waves_per_simd(sizeof(IoElem<IO>), NK, NV);
+
+template <typename IO, int NK, int NV, int kKind>
+struct LinTiles {
+    // The output's tile (fp32) is in place of the readers', and of what lies behind them.
+    static constexpr int kO = kKind == kLocal ? 0 : Tile<float, NV>::kBytes, kR = kKind == kLocal ? 0 : Tile<IO, NK>::kBytes;
+    static constexpr int kFirst = kO > kR ? kO : kR, kK = kFirst, kV = kK + Tile<IO, NK>::kBytes, kBytes = kV + Tile<IO, NV>::kBytes;
+};
 
 template <typename IO, int NK, int NV, bool kVec, int kKind>
-__global__ __launch_bounds__(64 * kWaves) void k_lin_pass(LinArgs a) {
+__global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass(LinArgs a) {
     constexpr bool kBf16 = sizeof(IoElem<IO>) == 2;
     constexpr int e = sizeof(IoElem<IO>);
-    __shared__ float2 sums[kWaves][kChunk];
-    const int lane = static_cast<int>(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    const int grp = lane >> 4, col = lane & 15;
-    const int64_t task = xcd_order(blockIdx.x, gridDim.x) * kWaves + wave;
-    if (task >= a.waves) return;
+    // parts of the decayed values, and of the state and the scores that are read. The state is fp32 in memory and goes through
+    // the values alone: three. Outputs in bf16 are not told from exact ones with two; the terms of the decays' gradient, which nearly
+    // cancel, need three.
+    constexpr int kValueParts = 3, kReadParts = kKind == kGradientDots ? 3 : 2;
+    using L = LinTiles<IO, NK, NV, kKind>;
+    using TK = Tile<IO, NK>;
+    using TV = Tile<IO, NV>;
+    using TO = Tile<float, NV>;
+    __shared__ __align__(16) char lds[L::kBytes];
+    __shared__ float2 sums[kChunk];
+    __shared__ float same[kKind == kGradientDots ? kChunk : 1];   // the scores of tokens with themselves
+    char* const tr = lds;
+    char* const tk = lds + L::kK;
+    char* const tv = lds + L::kV;
+    const int lane = static_cast<int>(threadIdx.x), grp = lane >> 4, col = lane & 15;
+    const int64_t task = xcd_order(blockIdx.x, gridDim.x);
     const int block = static_cast<int>(task % a.blocks);
     const int64_t rest = task / a.blocks, h = rest % a.H, slot = rest / a.H;
     const LinSegment sg = lin_segment(a, slot);
     if (!sg.valid) return;
     const bool desc = (a.rev != 0) != (a.back != 0);
-    const int c0 = block * 16 * NV, vc = c0 + NV * col, vr = c0 + 4 * NV * grp;   // the lane's value channels
+    const int c0 = block * 16 * NV, vc = c0 + NV * col;   // the block's and the lane's value channels
 
     // state: S[i][j][r] = channel NK (4 grp + r) + i, channel vc + j
     V4f S[NK][NV];
@@ -391,82 +427,83 @@ __global__ __launch_bounds__(64 * kWaves) void k_lin_pass(LinArgs a) {
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j) S[i][j] = V4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (s0) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int x = NK * (4 * grp + r) + i, y = vc + j;
-                    S[i][j][r] = s0 && x < a.K && y < a.V ? s0[x * a.s0_row + y * a.s0_col] : 0.0f;
-                }
+            for (int i = 0; i < NK; ++i)
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int x = NK * (4 * grp + r) + i, y = vc + j;
+                        if (x < a.K && y < a.V) S[i][j][r] = s0[x * a.s0_row + y * a.s0_col];
+                    }
+        }
     }
 
-    HeadRows<IO, kVec> R, K, V, W;
+    HeadRows<IO> R, K, V, W;
     R.init(a.r, h, a.K);
     K.init(a.k, h, a.K);
     V.init(a.v, h, a.V);
-    if constexpr (kKind == kGradient) W.init(a.w, h, a.V);
-    const bool dots = kKind == kGradient && a.dots;
+    if constexpr (kKind == kGradientDots) W.init(a.w, h, a.V);
 
+    // Chunk m holds 32 walking positions i, at its row i or, walking down, 31 - i. The tokens that a last chunk lacks
+    // are behind its rows; walking down the first chunk lacks them, before the first token. Either way they are at rows from
+    // cnt on, outside the resource: no keys, no values, no decay.
     const int64_t n = sg.n;
-    RowPart<IO, NK> rr[2], kr[2];
-    ColPart<IO, NK> kc;
-    ColPart<IO, NV> vcol;
-    float gv = 0.0f;
-    int64_t mem = 0;     // the chunk's lowest token
-    int cnt = 0;
-    auto place = [&](int64_t at, int64_t* first, int* c) {
-        *c = static_cast<int>(n - at < kChunk ? n - at : kChunk);
-        *first = desc ? sg.first + n - at - *c : sg.first + at;
+    const int chunks = static_cast<int>((n + kChunk - 1) / kChunk), lack = chunks * kChunk - static_cast<int>(n);
+    auto place = [&](int m, int64_t* first, int* c) {
+        *first = desc ? sg.first + n + lack - static_cast<int64_t>(m + 1) * kChunk : sg.first + static_cast<int64_t>(m) * kChunk;
+        *c = m >= chunks ? 0 : m == (desc ? 0 : chunks - 1) ? kChunk - lack : kChunk;
     };
-    // (walking position i of a chunk of c tokens is its row i or c - 1 - i)
-    auto load = [&](int64_t at) {
+    const int flip = desc ? kChunk - 1 : 0;               // (row of position i: i ^ flip)
+    const int my_row = (lane & (kChunk - 1)) ^ flip, row0 = col ^ flip, grow0 = (4 * grp) ^ flip, step = desc ? -1 : 1;
+    const uint32_t g_ld = static_cast<uint32_t>(a.ld_g) * 4;
+
+    U4 sr[kKind == kLocal ? 1 : TK::kLoads], sk[TK::kLoads], sv[TV::kLoads];
+    float gv = 0.0f;
+    // (past the last chunk: zeros, and no branch, behind which what is loaded would be waited for)
+    auto load = [&](int m) {
         int64_t first;
         int c;
-        place(at, &first, &c);
-        auto row = [&](int i) { return desc ? c - 1 - i : i; };
-        K.chunk(first, c);
-        V.chunk(first, c);
-        int t[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = row((k & 4) * 4 + 4 * grp + (k & 3));
-        if constexpr (kKind != kLocal) {
-            R.chunk(first, c);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                K.part(row(16 * j + col), grp, kr[j]);
-                R.part(row(16 * j + col), grp, rr[j]);
-            }
-        }
-        K.columns(t, NK * col, kc);
-        V.columns(t, vc, vcol);
-        // the decay of the chunk's walking position lane % 32; moved by one token where the walk goes back
-        const int i = lane & 31;
-        const int64_t w = at + i - (a.back ? 1 : 0);
-        gv = 0.0f;
-        if (i < c && w >= 0) {
-            const int64_t tok = desc ? sg.first + n - 1 - w : sg.first + w;
-            gv = a.ld_g ? a.g[tok * a.ld_g + h] : a.g[h];
-        }
+        place(m, &first, &c);
+        if constexpr (kKind != kLocal) R.template load<NK, kVec>(first, c, 0, lane, sr);
+        K.template load<NK, kVec>(first, c, 0, lane, sk);
+        V.template load<NV, kVec>(first, c, c0, lane, sv);
+        // the decay of the lane's position (of its half of the wave); moved by one token where the walk goes back, the segment's
+        // own tokens only
+        const int move = a.back ? (desc ? 1 : -1) : 0, rel = static_cast<int>(first - sg.first) + my_row + move;
+        const bool in = my_row < c && rel >= 0 && rel < static_cast<int>(n);
+        const int64_t at = uniform(reinterpret_cast<int64_t>(a.g) + ((first + move) * a.ld_g + h) * 4);
+        const auto gb = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, (kChunk - 1) * g_ld + 4, kRsrcFlags);
+        gv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gb, in ? my_row * g_ld : kOutside, 0, 0));
     };
 
     double all = 0.0;    // sum of the decays so far
-    if (n > 0) load(0);
-    for (int64_t at = 0; at < n; at += kChunk) {
-        place(at, &mem, &cnt);
+    if (chunks > 0) load(0);
+    for (int m = 0; m < chunks; ++m) {
+        int64_t mem;     // the chunk's lowest token, and how many it has
+        int cnt;
+        place(m, &mem, &cnt);
         // sums of the log decays over the chunk
         const double run = half_wave_sums(log2_decay(gv));
         const double total = lane_value(run, 31);
         const float2 end = as_pair(total);
         if (kKind == kLocal) all += total;
         wave_sync();
-        if (lane < kChunk) sums[wave][lane] = as_pair(run);
+        if constexpr (kKind != kLocal) TK::put(tr, lane, sr);
+        TK::put(tk, lane, sk);
+        TV::put(tv, lane, sv);
+        if (lane < kChunk) sums[lane] = as_pair(run);
         wave_sync();
-        float2 gs[8];    // of the lane's eight tokens
-#pragma unroll
-        for (int k = 0; k < 8; ++k) gs[k] = sums[wave][(k & 4) * 4 + 4 * grp + (k & 3)];
+        load(m + 1);
 
         V4f O[2][NV];
         [[maybe_unused]] float P[2][2][4];   // [key tile][reader tile], rows of keys
         if constexpr (kKind != kLocal) {
+            RowPart<IO, NK> rr[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) TK::part(tr, row0 + 16 * j * step, grp, rr[j]);
             // r S_in, then its decay
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -477,15 +514,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_lin_pass(LinArgs a) {
                 if constexpr (kBf16) {
 #pragma unroll
                     for (int s = 0; s < NK / 2; ++s) {
-                        Split8 st;
+                        Split8<kReadParts> st;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) split_pair(st, i, S[2 * s][v][i], S[2 * s + 1][v][i]);
+                        for (int i = 0; i < 4; ++i) st.pair(i, S[2 * s][v][i], S[2 * s + 1][v][i]);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const U4 x = row_operand<NK>(rr[j], s);
-                            O[j][v] = mfma(st.hi, x, O[j][v]);
-                            O[j][v] = mfma(st.lo, x, O[j][v]);
-                        }
+                        for (int p = 0; p < kReadParts; ++p)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) O[j][v] = mfma(st.w[p], row_operand<NK>(rr[j], s), O[j][v]);
                     }
                 } else {
 #pragma unroll
@@ -499,242 +534,247 @@ __global__ __launch_bounds__(64 * kWaves) void k_lin_pass(LinArgs a) {
             float2 gt[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                gt[j] = sums[wave][16 * j + col];
-                const float into = fast_exp2(gt[j].x + gt[j].y);
+                gt[j] = sums[16 * j + col];
+                const float into = fast_exp2(gt[j].x + gt[j].y) * a.out_scale;
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) O[j][v][r] *= into;
             }
             // scores, decayed; a pair of a token and an earlier one is left out by selection (it may be NaN)
+            const float scale = a.key_scale * a.out_scale;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+                RowPart<IO, NK> kr;
+                TK::part(tk, row0 + 16 * i * step, grp, kr);
+                float2 gs[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) gs[r] = sums[16 * i + 4 * grp + r];
 #pragma unroll
                 for (int j = i; j < 2; ++j) {
-                    const V4f x = scores<IO, NK>(kr[i], rr[j]);
+                    const V4f x = scores<IO, NK>(kr, rr[j]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float d = decay_between(gt[j], gs[4 * i + r]) * (x[r] * a.key_scale);
+                        const float d = decay_between(gt[j], gs[r]) * (x[r] * scale);
                         P[i][j][r] = i < j || 4 * grp + r <= col ? d : 0.0f;
+                        if constexpr (kKind == kGradientDots) {
+                            // (a token's own score apart: it is added where the output is written)
+                            if (i == j && 4 * grp + r == col) same[16 * i + col] = d;
+                            P[i][j][r] = i < j || 4 * grp + r < col ? d : 0.0f;
+                        }
                     }
                 }
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) P[1][0][r] = 0.0f;
         }
-        // keys decayed to the chunk's end, as operands over the tokens
-        float out[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = decay_between(end, gs[k]) * a.key_scale;
-        [[maybe_unused]] U4 vop[NV];
-        [[maybe_unused]] Split8 kop[NK];
-        [[maybe_unused]] ColPart<IO, NK> kd;
-        [[maybe_unused]] ColPart<IO, NV> vd;
-        bool finite = true;
-        if constexpr (kBf16) {
+        // The numbers of the chunk's columns, in bf16 as operands over the tokens.
+        U4 vop[NV], kop[NK];
+        ColPart<IO, NV> vcol;
+        TV::columns(tv, grow0, step, col, vcol);
+        if constexpr (kBf16)
 #pragma unroll
             for (int j = 0; j < NV; ++j) vop[j] = col_operand<NV>(vcol, j);
-#pragma unroll
-            for (int i = 0; i < NK; ++i)
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    split_pair(kop[i], m, kc.get(2 * m, i) * out[2 * m], kc.get(2 * m + 1, i) * out[2 * m + 1]);
-            if constexpr (kKind == kForward) {
-                S2 most = {0, 0};
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-#pragma unroll
-                    for (int j = 0; j < NV / 2; ++j)
-                        most = __builtin_elementwise_max(most, __builtin_bit_cast(S2, vcol.w[k][j] & 0x7fff7fffu));
-                finite = most[0] < 0x7f80 && most[1] < 0x7f80;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-#pragma unroll
-                for (int i = 0; i < NK; ++i) kd.w[k][i] = kc.w[k][i] * out[k];
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    vd.w[k][j] = vcol.w[k][j];
-                    if constexpr (kKind == kForward) finite = finite && __builtin_fabsf(vcol.w[k][j]) < __builtin_inff();
-                }
-            }
-        }
-        // the next chunk's numbers are on their way during the products that follow
-        if (at + kChunk < n) load(at + kChunk);
 
         if constexpr (kKind != kLocal) {
             // o += P v
-            auto add = [&](const float (&p)[2][2][4], int j) {
+            auto add = [&](int j, const U4 (&vo)[NV], const ColPart<IO, NV>& vw) {
                 if constexpr (kBf16) {
-                    Split8 x;
+                    Split8<kReadParts> x;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) split_pair(x, m, p[m / 2][j][2 * (m & 1)], p[m / 2][j][2 * (m & 1) + 1]);
+                    for (int m = 0; m < 4; ++m) x.pair(m, P[m / 2][j][2 * (m & 1)], P[m / 2][j][2 * (m & 1) + 1]);
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        O[j][v] = mfma(vop[v], x.hi, O[j][v]);
-                        O[j][v] = mfma(vop[v], x.lo, O[j][v]);
-                    }
+                    for (int q = 0; q < kReadParts; ++q)
+#pragma unroll
+                        for (int v = 0; v < NV; ++v) O[j][v] = mfma(vo[v], x.w[q], O[j][v]);
                 } else {
 #pragma unroll
                     for (int i = 0; i <= j; ++i)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
 #pragma unroll
-                            for (int v = 0; v < NV; ++v) O[j][v] = mfma(vd.w[4 * i + r][v], p[i][j][r], O[j][v]);
+                            for (int v = 0; v < NV; ++v) O[j][v] = mfma(vw.w[4 * i + r][v], P[i][j][r], O[j][v]);
                 }
             };
-            if constexpr (kKind == kForward) {
-                if (__all(finite)) {
-                    add(P, 0);
-                    add(P, 1);
+            bool finite = true;
+            if constexpr (kKind == kForward && kBf16) {
+                S2 most = {0, 0};
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) most = __builtin_elementwise_max(most, __builtin_bit_cast(S2, vop[j][k] & 0x7fff7fffu));
+                finite = most[0] < 0x7f80 && most[1] < 0x7f80;
+            } else if constexpr (kKind == kForward) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) finite = finite && __builtin_fabsf(vcol.w[k][j]) < __builtin_inff();
+            }
+            if (kKind != kForward || __builtin_expect(__all(finite), 1)) {
+                add(0, vop, vcol);
+                add(1, vop, vcol);
+            } else {
+                // a NaN or infinity among the values must not reach the tokens before it, as 0 times it would:
+                // the product without them, then they alone, token by token
+                U4 vo[NV];
+                ColPart<IO, NV> vw;
+                if constexpr (kBf16) {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const uint32_t w = opaque(vop[v][m]);   // (else formed before the branch, for every chunk)
+                            vo[v][m] = ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) |
+                                       ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+                        }
                 } else {
-                    // a NaN or infinity among the values must not reach the tokens before it, as 0 times it would:
-                    // the product without them, then they alone, token by token
-                    if constexpr (kBf16) {
-                        U4 keep[NV];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
 #pragma unroll
                         for (int v = 0; v < NV; ++v) {
-                            keep[v] = vop[v];
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const uint32_t w = vop[v][m];
-                                vop[v][m] = ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) |
-                                            ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
-                            }
+                            const float w = __uint_as_float(opaque(__float_as_uint(vcol.w[k][v])));
+                            vw.w[k][v] = __builtin_fabsf(w) < __builtin_inff() ? w : 0.0f;
                         }
-                        add(P, 0);
-                        add(P, 1);
-#pragma unroll
-                        for (int v = 0; v < NV; ++v) vop[v] = keep[v];
-                    } else {
-                        ColPart<IO, NV> keep = vd;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-#pragma unroll
-                            for (int v = 0; v < NV; ++v)
-                                if (!(__builtin_fabsf(vd.w[k][v]) < __builtin_inff())) vd.w[k][v] = 0.0f;
-                        add(P, 0);
-                        add(P, 1);
-                        vd = keep;
-                    }
-                    HeadRows<IO, kVec> X = V;
-                    X.chunk(mem, cnt);
-                    for (int s = 0; s < cnt; ++s) {
-                        RowPart<IO, NV> x;
-                        const uint32_t row = static_cast<uint32_t>(desc ? cnt - 1 - s : s) * X.ld;
-#pragma unroll
-                        for (int k = 0; k < 4 * NV; k += NV)
-                            load_channels<IO, NV, kVec>(X.rsrc, row, vr + k, X.D, &x.w[k * e / 4]);
-                        const int from = ((s & 15) >> 2) * 16 + col;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float p = 0.0f;
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const float there = __shfl(P[i][j][r], from);
-                                    if (i == (s >> 4) && r == (s & 3)) p = there;
-                                }
-#pragma unroll
-                            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const float xv = x.get(NV * r + v);
-                                    if (s <= 16 * j + col && !(__builtin_fabsf(xv) < __builtin_inff()))
-                                        O[j][v][r] = fmaf(p, xv, O[j][v][r]);
-                                }
-                        }
-                    }
                 }
-            } else {
-                if (dots) {
-                    // without the pairs of a token with itself; then those
-                    float own[2][2][4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const bool same = i == j && 4 * grp + r == col;
-                                own[i][j][r] = same ? P[i][j][r] : 0.0f;
-                                P[i][j][r] = same ? 0.0f : P[i][j][r];
-                            }
-                    W.chunk(mem, cnt);
+                add(0, vo, vw);
+                add(1, vo, vw);
+                for (int s = 0; s < kChunk; ++s) {
+                    RowPart<IO, NV> x;
+                    TV::part(tv, s ^ flip, grp, x);
+                    const int from = ((s & 15) >> 2) * 16 + col;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int i = 16 * j + col, row = desc ? cnt - 1 - i : i;
-                        RowPart<IO, NV> w;
+                        float p = 0.0f;
 #pragma unroll
-                        for (int k = 0; k < 4 * NV; k += NV)
-                            load_channels<IO, NV, kVec>(W.rsrc, static_cast<uint32_t>(row) * W.ld, vr + k, W.D, &w.w[k * e / 4]);
-                        add(P, j);
-                        float dot = 0.0f;
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float there = __shfl(P[i][j][r], from);
+                                if (i == (s >> 4) && r == (s & 3)) p = there;
+                            }
 #pragma unroll
                         for (int v = 0; v < NV; ++v)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) dot = fmaf(O[j][v][r], w.get(NV * r + v), dot);
-                        dot = over_groups(dot) * a.out_scale;
-                        if (grp == 0 && i < cnt)
-                            a.dots[(static_cast<int64_t>(block) * a.tokens + mem + row) * a.H + h] = dot;
-                        add(own, j);
+                            for (int r = 0; r < 4; ++r) {
+                                const float xv = x.get(NV * r + v);
+                                if (s <= 16 * j + col && !(__builtin_fabsf(xv) < __builtin_inff()))
+                                    O[j][v][r] = fmaf(p, xv, O[j][v][r]);
+                            }
                     }
-                } else {
-                    add(P, 0);
-                    add(P, 1);
                 }
             }
-            // o is written: row t is 4 NV consecutive channels of the lane
-            const int oe = a.o_f32 ? 4 : e;
-            const int64_t stride = static_cast<int64_t>(a.H) * a.V * oe;
-            const int64_t dst = uniform(reinterpret_cast<int64_t>(a.o) + mem * stride + h * a.V * oe);
-            const __amdgpu_buffer_rsrc_t orsrc = __builtin_amdgcn_make_buffer_rsrc(
-                reinterpret_cast<void*>(dst), 0, static_cast<uint32_t>((cnt - 1) * stride + a.V * oe), kRsrcFlags);
+            // The output goes through a tile of its own, so that consecutive lanes write consecutive pieces of rows.
+            wave_sync();
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int i = 16 * j + col;
-                const uint32_t row = static_cast<uint32_t>(desc ? cnt - 1 - i : i) * static_cast<uint32_t>(stride);
+                float* p = reinterpret_cast<float*>(tr + (row0 + 16 * j * step) * TO::kRow) + 4 * NV * grp;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int c = vr + NV * r;
-                    float x[NV];
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) x[v] = O[j][v][r] * a.out_scale;
-                    if (!kBf16 || a.o_f32) {
+                    for (int v = 0; v < NV; ++v) p[NV * r + v] = O[j][v][r];
+            }
+            wave_sync();
+            const int oe = a.o_f32 ? 4 : e;
+            const uint32_t o_ld = static_cast<uint32_t>(a.H) * a.V * oe;
+            const int64_t dst = uniform(reinterpret_cast<int64_t>(a.o) + mem * static_cast<int64_t>(o_ld) + h * a.V * oe);
+            const auto ob = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(dst), 0,
+                                                              static_cast<uint32_t>((cnt - 1) * o_ld + a.V * oe), kRsrcFlags);
+            [[maybe_unused]] const auto wb = W.chunk(mem, kKind == kGradientDots ? cnt : 0);
+            // 2 NV lanes to a row, eight channels each
+            constexpr int kLanes = 2 * NV, kRows = 64 / kLanes;
+            const int oc = c0 + static_cast<int>(opaque(lane)) % kLanes * 8;
 #pragma unroll
-                        for (int v = 0; v < NV; ++v)
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[v]), orsrc,
-                                                                  c + v < a.V ? row + (c + v) * 4 : kOutside, 0, 0);
-                    } else if constexpr (kVec && NV == 4) {
-                        const U2v w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(U2v, w), orsrc, c < a.V ? row + c * 2 : kOutside, 0, 0);
-                    } else if constexpr (kVec && NV == 2) {
-                        __builtin_amdgcn_raw_buffer_store_b32(bf16_pair(x[0], x[1]), orsrc, c < a.V ? row + c * 2 : kOutside, 0, 0);
-                    } else {
+            for (int k = 0; k < kChunk / kRows; ++k) {
+                const int row = static_cast<int>(opaque(lane)) / kLanes + k * kRows;
+                const char* src = tr + row * TO::kRow + lane % kLanes * 32;
+                float x[8];
+                __builtin_memcpy(x, __builtin_assume_aligned(src, 16), 16);
+                __builtin_memcpy(x + 4, __builtin_assume_aligned(src + 16, 16), 16);
+                if constexpr (kKind == kGradientDots) {
+                    // w . o, then the token's own pair
+                    constexpr int kW = 8 * e / 16, nw = 16 / e;
+                    U4 w[kW], v[kW];
 #pragma unroll
-                        for (int v = 0; v < NV; ++v)
-                            __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(x[v]), orsrc, c + v < a.V ? row + (c + v) * 2 : kOutside, 0, 0);
+                    for (int q = 0; q < kW; ++q) {
+                        w[q] = load_piece<IO, kVec>(wb, static_cast<uint32_t>(row) * W.ld, oc + q * nw, W.D);
+                        v[q] = *reinterpret_cast<const U4*>(tv + row * TV::kRow + lane % kLanes * 8 * e + q * 16);
                     }
+                    auto value = [&](const U4 (&u)[kW], int c) {
+                        if constexpr (kBf16) return (c & 1) ? bf16_hi(u[0][c / 2]) : bf16_lo(u[0][c / 2]);
+                        else return __uint_as_float(u[c / 4][c % 4]);
+                    };
+                    float dot = 0.0f;
+                    const float p = same[row ^ flip];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        dot = fmaf(x[c], value(w, c), dot);
+                        x[c] = fmaf(p, value(v, c), x[c]);
+                    }
+#pragma unroll
+                    for (int q = 1; q < kLanes; q *= 2) dot += __shfl_xor(dot, q);
+                    if (lane % kLanes == 0 && row < cnt) a.dots[(static_cast<int64_t>(block) * a.tokens + mem + row) * a.H + h] = dot;
+                }
+                const uint32_t at = static_cast<uint32_t>(row) * o_ld;
+                if (!kBf16 || a.o_f32) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if constexpr (kVec) {
+                            U4 w;
+                            __builtin_memcpy(&w, x + 4 * q, 16);
+                            __builtin_amdgcn_raw_buffer_store_b128(w, ob, oc + 4 * q < a.V ? at + (oc + 4 * q) * 4 : kOutside, 0, 0);
+                        } else {
+#pragma unroll
+                            for (int c = 4 * q; c < 4 * q + 4; ++c)
+                                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[c]), ob, oc + c < a.V ? at + (oc + c) * 4 : kOutside, 0, 0);
+                        }
+                    }
+                } else if constexpr (kVec) {
+                    const U4 w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
+                    __builtin_amdgcn_raw_buffer_store_b128(w, ob, oc < a.V ? at + oc * 2 : kOutside, 0, 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(x[c]), ob, oc + c < a.V ? at + (oc + c) * 2 : kOutside, 0, 0);
                 }
             }
         }
-        // S = e^{G_end} S + keys^T values
+        // S = e^{G_end} S + keys^T (values, decayed to the chunk's end)
         const float keep = fast_exp2(end.x + end.y);
+        float out[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = decay_between(end, sums[(k & 4) * 4 + 4 * grp + (k & 3)]) * a.key_scale;
+        ColPart<IO, NK> kc;
+        TK::columns(tk, grow0, step, col, kc);
+        if constexpr (kBf16)
+#pragma unroll
+            for (int i = 0; i < NK; ++i) kop[i] = col_operand<NK>(kc, i);
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[i][j][r] *= keep;
-                if constexpr (kBf16) {
-                    S[i][j] = mfma(kop[i].hi, vop[j], S[i][j]);
-                    S[i][j] = mfma(kop[i].lo, vop[j], S[i][j]);
-                } else {
+        if constexpr (kBf16) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) S[i][j] = mfma(kd.w[k][i], vd.w[k][j], S[i][j]);
-                }
+            for (int j = 0; j < NV; ++j) {
+                Split8<kValueParts> vd;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) vd.pair(q, bf16_lo(vop[j][q]) * out[2 * q], bf16_hi(vop[j][q]) * out[2 * q + 1]);
+#pragma unroll
+                for (int p = 0; p < kValueParts; ++p)
+#pragma unroll
+                    for (int i = 0; i < NK; ++i) S[i][j] = mfma(kop[i], vd.w[p], S[i][j]);
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const float x = vcol.w[k][j] * out[k];
+#pragma unroll
+                    for (int i = 0; i < NK; ++i) S[i][j] = mfma(kc.w[k][i], x, S[i][j]);
+                }
+        }
     }
 
     // what is left: the decay of the last token, where decays were moved; the segment's or sequence's state
@@ -745,7 +785,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_lin_pass(LinArgs a) {
         const float2 p = as_pair(g);
         rest_decay = fast_exp2(p.x + p.y);
     }
-    if constexpr (kKind == kGradient) {
+    if constexpr (kKind == kGradientDots) {
         if (a.cdot) {
             const float* ep = lin_state(a.e, a.e_by_slot, slot, sg.seq, a, h);
             float sum = 0.0f;

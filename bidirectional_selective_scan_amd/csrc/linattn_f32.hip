@@ -6,4 +6,5 @@ namespace vimscan_dev {
 template void launch_lin_pass<float, kLocal>(const LinArgs&, bool, hipStream_t);
 template void launch_lin_pass<float, kForward>(const LinArgs&, bool, hipStream_t);
 template void launch_lin_pass<float, kGradient>(const LinArgs&, bool, hipStream_t);
+template void launch_lin_pass<float, kGradientDots>(const LinArgs&, bool, hipStream_t);
 }  // namespace vimscan_dev

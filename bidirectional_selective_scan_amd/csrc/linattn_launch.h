@@ -8,8 +8,7 @@ namespace vimscan_dev {
 
 template <typename IO, int NK, int NV, bool kVec, int kKind>
 void launch_lin_instance(const LinArgs& a, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>((a.waves + kWaves - 1) / kWaves));
-    hipLaunchKernelGGL((k_lin_pass<IO, NK, NV, kVec, kKind>), grid, dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((k_lin_pass<IO, NK, NV, kVec, kKind>), dim3(static_cast<unsigned>(a.waves)), dim3(64), 0, s, a);
 }
 template <typename IO, int NK, bool kVec, int kKind>
 void launch_lin_outputs(const LinArgs& a, hipStream_t s) {

@@ -80,7 +80,7 @@ int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, i
     if (p->nseq == 0) return VIMSCAN_OK;
     const int64_t length = packed ? up(p->tokens, p->nseq) : p->Lp;
     const int64_t blocks = lin_blocks(p->dv), qblocks = lin_blocks(p->dk);
-    const int64_t most_waves = kMaxLinWgs * kLinWaves / ((blocks > qblocks ? blocks : qblocks) * heads);
+    const int64_t most_waves = kMaxLinWaves / ((blocks > qblocks ? blocks : qblocks) * heads);
     if (p->nseq > most_waves) return VIMSCAN_ERR_SHAPE;
     p->seg = segment(length, p->nseq * heads * blocks);
     // (packed sequences may be longer than their mean)
@@ -207,7 +207,7 @@ int vimscan_linattn_plan(const vimscan_launch* launch, int64_t seg_len, int64_t 
     plan->seq_tokens = p.Lp;
     plan->chunk_len = p.seg;
     plan->chunks = p.nseq == 0 ? 0 : p.split && packed ? p.slots : p.segs;
-    plan->workgroups = up(p.waves, kLinWaves);
+    plan->workgroups = p.waves;
     // forward: the pass, where it is split after the segments' states and their fold; backward: the same
     // states and those of the gradients, three passes, the decays' gradient (and its sum over the
     // tokens), the sums over shared heads

@@ -12,16 +12,20 @@ namespace vimscan_host {
 
 constexpr int64_t kLinMaxDim = 128;    // of dk and dv
 constexpr int kLinChunk = 32;          // tokens that a wave works on at once
-constexpr int kLinWaves = 4;           // waves of a workgroup, each with work of its own
 constexpr int64_t kMaxHeadStride = int64_t(1) << 38;
-// Workgroups of 256 threads: a grid holds fewer than 2^32 threads.
-constexpr int64_t kMaxLinWgs = (int64_t(1) << 24) - 1;
+// Workgroups of 64 threads (a wave) and of 256: a grid holds fewer than 2^32 threads.
+constexpr int64_t kMaxLinWaves = (int64_t(1) << 26) - 1, kMaxLinWgs = (int64_t(1) << 24) - 1;
 
 // Tiles of 16 that a wave's state has over a contracted dimension (at least as wide as it) and over an
 // output dimension, of which a wave takes a block.
 constexpr int lin_contract_tiles(int64_t d) { return d <= 32 ? 2 : d <= 64 ? 4 : 8; }
 constexpr int lin_output_tiles(int64_t d) { return d <= 32 ? 2 : 4; }
 constexpr int64_t lin_blocks(int64_t d) { return (d + 16 * lin_output_tiles(d) - 1) / (16 * lin_output_tiles(d)); }
+
+// Waves a SIMD that the registers of a pass are cut for (512 a SIMD lane; measured: cut for more, they spill).
+constexpr int lin_waves_per_simd(int bytes, int nk, int nv) {
+    return bytes == 4 ? (nk * nv <= 4 ? 3 : nk * nv <= 8 ? 2 : 1) : nk * nv <= 4 ? 4 : nk * nv <= 8 ? 3 : nk * nv <= 16 ? 2 : 1;
+}
 
 struct LinPlan {
     int64_t tokens, nseq, Lp;          // Lp: tokens per sequence, 0 when packed
