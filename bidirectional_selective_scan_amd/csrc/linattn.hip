@@ -19,14 +19,14 @@
 
 namespace vimscan_dev {
 
-extern template void launch_lin_pass<Bf16, kLocal>(const LinArgs&, bool, hipStream_t);
-extern template void launch_lin_pass<Bf16, kForward>(const LinArgs&, bool, hipStream_t);
-extern template void launch_lin_pass<Bf16, kGradient>(const LinArgs&, bool, hipStream_t);
-extern template void launch_lin_pass<Bf16, kGradientDots>(const LinArgs&, bool, hipStream_t);
-extern template void launch_lin_pass<float, kLocal>(const LinArgs&, bool, hipStream_t);
-extern template void launch_lin_pass<float, kForward>(const LinArgs&, bool, hipStream_t);
-extern template void launch_lin_pass<float, kGradient>(const LinArgs&, bool, hipStream_t);
-extern template void launch_lin_pass<float, kGradientDots>(const LinArgs&, bool, hipStream_t);
+extern template void launch_lin_pass<Bf16, kLocal>(const LinPasses&, bool, hipStream_t);
+extern template void launch_lin_pass<Bf16, kForward>(const LinPasses&, bool, hipStream_t);
+extern template void launch_lin_pass<Bf16, kGradient>(const LinPasses&, bool, hipStream_t);
+extern template void launch_lin_pass<Bf16, kGradientDots>(const LinPasses&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kLocal>(const LinPasses&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kForward>(const LinPasses&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kGradient>(const LinPasses&, bool, hipStream_t);
+extern template void launch_lin_pass<float, kGradientDots>(const LinPasses&, bool, hipStream_t);
 
 }  // namespace vimscan_dev
 
@@ -36,6 +36,7 @@ using namespace vimscan_dev;
 using vimscan_host::LinPlan;
 constexpr int kWaves = 4;   // waves of the workgroups of the kernels here
 
+constexpr int kFoldAhead = 8;
 // Replaces every segment's own state by the state it starts from, in the order of the walk (from the end: from the last
 // segment on): X = init; for each segment: its place <- X, X = decay X + (what was there). One element a thread.
 __global__ __launch_bounds__(256) void k_lin_fold(LinArgs a, float* states, const float* tot, const float* init, int from_end) {
@@ -52,12 +53,22 @@ __global__ __launch_bounds__(256) void k_lin_fold(LinArgs a, float* states, cons
         }
         float x = init ? init[t] : 0.0f;
         // (an empty sequence's one segment has no decay and adds nothing: both were written by its pass)
-        for (int64_t j = 0; j < count; ++j) {
-            const int64_t slot = first + (from_end ? count - 1 - j : j);
-            float* p = states + slot * per_seq + at;
-            const float mine = *p;
-            *p = x;
-            x = fmaf(tot[slot * a.H + h], x, mine);
+        const int64_t from = first + (from_end ? count - 1 : 0), step = from_end ? -1 : 1;
+        for (int64_t j = 0; j < count; j += kFoldAhead) {
+            // as many loads on their way at once
+            float mine[kFoldAhead], dec[kFoldAhead];
+#pragma unroll
+            for (int k = 0; k < kFoldAhead; ++k) {
+                const int64_t slot = from + (j + k < count ? j + k : count - 1) * step;
+                mine[k] = states[slot * per_seq + at];
+                dec[k] = tot[slot * a.H + h];
+            }
+#pragma unroll
+            for (int k = 0; k < kFoldAhead; ++k)
+                if (j + k < count) {
+                    states[(from + (j + k) * step) * per_seq + at] = x;
+                    x = fmaf(dec[k], x, mine[k]);
+                }
         }
     }
 }
@@ -240,6 +251,9 @@ LinArgs common_args(const vimscan_linattn* p, const vimscan_launch* l, const Lin
     a.split = pl.split;
     a.rev = (l->flags & VIMSCAN_FLAG_REVERSE) ? 1 : 0;
     a.slots = pl.slots;
+    // (q, k, v and one more array of v's size, against the 256 MB of the memory-side cache)
+    const int64_t e = l->io_dtype == VIMSCAN_F32 ? 4 : 2;
+    a.once = pl.tokens * e * (2 * pl.G * pl.dk + 2 * pl.H * pl.dv) > (int64_t(256) << 20);
     a.key_scale = a.out_scale = 1.0f;
     return a;
 }
@@ -255,18 +269,30 @@ void set_roles(LinArgs* a, const LinRows& r, const LinRows& k, const LinRows& v,
     a->waves = a->slots * a->H * a->blocks;
 }
 
-void run_pass(int io, bool vec, LinKind kind, const LinArgs& a, hipStream_t s) {
+void run_passes(int io, bool vec, LinKind kind, const LinPasses& p, hipStream_t s) {
     if (io == VIMSCAN_F32) {
-        if (kind == kLocal) launch_lin_pass<float, kLocal>(a, vec, s);
-        else if (kind == kForward) launch_lin_pass<float, kForward>(a, vec, s);
-        else if (kind == kGradient) launch_lin_pass<float, kGradient>(a, vec, s);
-        else launch_lin_pass<float, kGradientDots>(a, vec, s);
+        if (kind == kLocal) launch_lin_pass<float, kLocal>(p, vec, s);
+        else if (kind == kForward) launch_lin_pass<float, kForward>(p, vec, s);
+        else if (kind == kGradient) launch_lin_pass<float, kGradient>(p, vec, s);
+        else launch_lin_pass<float, kGradientDots>(p, vec, s);
     } else {
-        if (kind == kLocal) launch_lin_pass<Bf16, kLocal>(a, vec, s);
-        else if (kind == kForward) launch_lin_pass<Bf16, kForward>(a, vec, s);
-        else if (kind == kGradient) launch_lin_pass<Bf16, kGradient>(a, vec, s);
-        else launch_lin_pass<Bf16, kGradientDots>(a, vec, s);
+        if (kind == kLocal) launch_lin_pass<Bf16, kLocal>(p, vec, s);
+        else if (kind == kForward) launch_lin_pass<Bf16, kForward>(p, vec, s);
+        else if (kind == kGradient) launch_lin_pass<Bf16, kGradient>(p, vec, s);
+        else launch_lin_pass<Bf16, kGradientDots>(p, vec, s);
     }
+}
+void run_pass(int io, bool vec, LinKind kind, const LinArgs& a, hipStream_t s) {
+    LinPasses p;
+    std::memset(&p, 0, sizeof(p));
+    p.count = 1;
+    p.a[0] = a;
+    run_passes(io, vec, kind, p, s);
+}
+// Whether two passes can be one launch: the same instance, equally many waves.
+bool alike(const LinArgs& a, const LinArgs& b) {
+    return vimscan_host::lin_contract_tiles(a.K) == vimscan_host::lin_contract_tiles(b.K) &&
+           vimscan_host::lin_output_tiles(a.V) == vimscan_host::lin_output_tiles(b.V) && a.waves == b.waves;
 }
 
 unsigned some_blocks(int64_t elements) {
@@ -420,7 +446,9 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
         b.cdot = at(pl.off_cd);
     }
     const int32_t qblocks = b.blocks;
-    run_pass(io, vec, decays ? kGradientDots : kGradient, b, s);
+    LinPasses three;
+    std::memset(&three, 0, sizeof(three));
+    three.a[0] = b;
     b = a;           // dk: from the end, the gradient of the state transposed
     set_roles(&b, v, dy, q, pl.dv, pl.dk);
     b.back = 1;
@@ -435,7 +463,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
         b.w = k;
         b.dots = at(pl.off_rk);
     }
-    run_pass(io, vec, decays ? kGradientDots : kGradient, b, s);
+    three.a[1] = b;
     b = a;           // dv, and the gradient of the state before the sequence
     set_roles(&b, k, q, dy, pl.dk, pl.dv);
     b.back = 1;
@@ -444,7 +472,10 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     b.s0_by_slot = by_slot;
     b.s_end = grad->dh0;
     b.o = grad->dv;
-    run_pass(io, vec, kGradient, b, s);
+    three.a[2] = b;
+    three.count = alike(three.a[0], b) ? 3 : 2;
+    run_passes(io, vec, decays ? kGradientDots : kGradient, three, s);
+    if (three.count == 2) run_pass(io, vec, kGradient, b, s);
     if (decays) {
         DecayGradArgs d = {at(pl.off_rq), at(pl.off_rk), at(pl.off_cd), qblocks, by_head ? nullptr : grad->dlog_decay,
                            by_head ? at(pl.off_hs) : nullptr};

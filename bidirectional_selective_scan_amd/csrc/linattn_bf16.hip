@@ -3,8 +3,8 @@
 #include "linattn_launch.h"
 
 namespace vimscan_dev {
-template void launch_lin_pass<Bf16, kLocal>(const LinArgs&, bool, hipStream_t);
-template void launch_lin_pass<Bf16, kForward>(const LinArgs&, bool, hipStream_t);
-template void launch_lin_pass<Bf16, kGradient>(const LinArgs&, bool, hipStream_t);
-template void launch_lin_pass<Bf16, kGradientDots>(const LinArgs&, bool, hipStream_t);
+template void launch_lin_pass<Bf16, kLocal>(const LinPasses&, bool, hipStream_t);
+template void launch_lin_pass<Bf16, kForward>(const LinPasses&, bool, hipStream_t);
+template void launch_lin_pass<Bf16, kGradient>(const LinPasses&, bool, hipStream_t);
+template void launch_lin_pass<Bf16, kGradientDots>(const LinPasses&, bool, hipStream_t);
 }  // namespace vimscan_dev

@@ -16,9 +16,10 @@
 //   * the scores are formed transposed, rows = key tokens, columns = reader tokens: a lane holds the tokens 4 grp + 0..3
 //     of a column, which is how the next product (values times scores) takes its right operand;
 //   * o is formed transposed too, rows = channels: a lane ends with 4 NV consecutive channels of one token;
-//   * the state has rows = key channels, columns = value channels; row m of its tile i is channel NK m + i, column m
-//     of its tile j is channel NV m + j, so a lane reads NK (or NV) consecutive channels of its tokens, and as the left
-//     operand of r S it is in place as well.
+//   * the state has rows = key channels, columns = value channels. Column m of its tile j is channel NV m + j, row 4 grp + r
+//     of its tile i is channel 4 NK grp + 8 (i / 2) + 2 r + i % 2: a lane's rows are the 4 NK consecutive channels that it
+//     reads of a key or reader, in an order in which pairs of tiles are in place as the left operand of r S, and
+//     as columns they are read in pairs.
 // bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed values) are split
 // into two or three bf16 parts, each multiplied: the decayed values, which make the state, into three, as it is fp32 in memory. fp32: fp32 matrix instructions.
 // Sums of g are in fp64, and their differences taken from a pair of fp32, so that a token of strong decay does not cost its
@@ -29,6 +30,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "block_device.h"
 #include "linattn_plan.h"
@@ -71,6 +73,7 @@ struct LinArgs {
     int64_t tokens, Lp, seg;
     int32_t nseq, segs, split, rev;
     int64_t slots, waves;
+    int32_t once;              // inputs that are not kept in the caches
     int32_t back;              // walk from the segment's end (on top of rev), decays moved by one
     float key_scale, out_scale;
     // state before the segment: of its sequence or, by_slot, of itself; NULL: 0. Element (i, j) is at i row + j col
@@ -88,6 +91,12 @@ struct LinArgs {
     int64_t e_row, e_col;
     int32_t e_by_slot;
     float* cdot;
+};
+
+// Passes of one launch: equally many waves each, of the same instance.
+struct LinPasses {
+    int32_t count;
+    LinArgs a[3];
 };
 
 // A segment of a sequence, in tokens: walking positions w0 .. w0 + n of the sequence, at rows first .. first + n.
@@ -175,7 +184,7 @@ template <int N> struct RowPart<float, N> {
     float w[4 * N];
     __device__ __forceinline__ float get(int k) const { return w[k]; }
 };
-// N consecutive channels, from channel N col on, of the tokens 4 grp + 0..3 and 16 + 4 grp + 0..3 of a chunk.
+// N channels of the tokens 4 grp + 0..3 and 16 + 4 grp + 0..3 of a chunk.
 template <typename IO, int N> struct ColPart;
 template <int N> struct ColPart<Bf16, N> { uint32_t w[8][N / 2]; };
 template <int N> struct ColPart<float, N> { float w[8][N]; };
@@ -203,7 +212,7 @@ struct Tile {
             __builtin_memcpy(&o.w[16 / e * k / (e == 2 ? 2 : 1)], &w, 16);
         }
     }
-    // row0: the row of the lane's first token, step: from one to the next
+    // of the values: channels N col on. row0: the row of the lane's first token, step: from one to the next
     __device__ __forceinline__ static void columns(const char* tile, int row0, int step, int col, ColPart<IO, N>& o) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -211,6 +220,15 @@ struct Tile {
             if constexpr (N * e == 4) __builtin_memcpy(o.w[k], __builtin_assume_aligned(p, 4), 4);
             else if constexpr (N * e == 8) __builtin_memcpy(o.w[k], __builtin_assume_aligned(p, 8), 8);
             else __builtin_memcpy(o.w[k], __builtin_assume_aligned(p, 16), N * e);
+        }
+    }
+    // of the keys: channel i is that of row col of the state's tile i
+    __device__ __forceinline__ static void state_columns(const char* tile, int row0, int step, int col, ColPart<IO, N>& o) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const char* p = tile + (row0 + ((k & 4) * 4 + (k & 3)) * step) * kRow + (4 * N * (col / 4) + 2 * (col % 4)) * e;
+#pragma unroll
+            for (int i = 0; i < N; i += 2) __builtin_memcpy(&o.w[k][i * e / 4], __builtin_assume_aligned(p + 4 * i * e, 2 * e), 2 * e);
         }
     }
 };
@@ -222,12 +240,25 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
     return v;
 }
 
-// A lane's piece of a row at an offset in memory: kChannels channels from c on, those past D as 0. kVec: all or none are.
-template <typename IO, bool kVec>
+// The offset in a row of a piece that starts at channel c, for rows of D channels: whole or outside.
+template <typename T>
+__device__ __forceinline__ uint32_t piece_at(int c, int D) { return c < D ? static_cast<uint32_t>(c * sizeof(IoElem<T>)) : kOutside; }
+// Cache policy of the passes' loads. kOnce: the lines are not kept. Calls whose inputs do not fit the memory-side cache take it:
+// lines that are kept throw out others, written ones among them, for nothing (k and v of 1 x 65537 x 24 x 64 x 64, 403 MB,
+// in the segments' states: 123 us kept, 90 us not); those that fit are read again by the passes that follow (128 x 197 x 12 x 64 x 64,
+// backward 147 us kept, 161 us not).
+constexpr int kKeep = 0, kOnce = 2;
+template <int kPolicy>
+__device__ __forceinline__ U4 load_b128(__amdgpu_buffer_rsrc_t rsrc, uint32_t at) {
+    return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, kPolicy));
+}
+// A lane's piece of a row: kChannels channels from c on, those past D as 0. kVec: all or none are, and the offset is the piece's
+// own; else it is the row's.
+template <typename IO, bool kVec, int kPolicy = kKeep>
 __device__ __forceinline__ U4 load_piece(__amdgpu_buffer_rsrc_t rsrc, uint32_t row, int c, int D) {
     constexpr int e = sizeof(IoElem<IO>), n = 16 / e;
     if constexpr (kVec) {
-        return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, c < D ? row + static_cast<uint32_t>(c * e) : kOutside, 0, 0));
+        return load_b128<kPolicy>(rsrc, row);
     } else {
         U4 o = {0, 0, 0, 0};
 #pragma unroll
@@ -260,15 +291,21 @@ struct HeadRows {
         return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, D > 0 && n > 0 ? (n - 1) * ld + D * e : 0,
                                                  kRsrcFlags);
     }
-    // a lane's pieces of a chunk, from channel c0 on
+    // where a lane's first row of a chunk is; kVec: its piece of it, from channel c0 on
     template <int N, bool kVec>
-    __device__ __forceinline__ void load(int64_t first, int n, int c0, int lane, U4 (&o)[Tile<IO, N>::kLoads]) const {
+    __device__ __forceinline__ uint32_t at(int c0, int lane) const {
+        using T = Tile<IO, N>;
+        return T::row(lane, 0) * ld + (kVec ? piece_at<IO>(c0 + T::piece(lane) * T::kChannels, D) : 0u);
+    }
+    // a lane's pieces of a chunk
+    template <int N, bool kVec, int kPolicy>
+    __device__ __forceinline__ void load(int64_t first, int n, uint32_t at, int c0, int lane, U4 (&o)[Tile<IO, N>::kLoads]) const {
         using T = Tile<IO, N>;
         const auto rsrc = chunk(first, n);
-        const int c = c0 + T::piece(static_cast<int>(opaque(lane))) * T::kChannels;
-        const uint32_t row = static_cast<uint32_t>(T::row(static_cast<int>(opaque(lane)), 0)) * ld;
+        const uint32_t row = opaque(at);
 #pragma unroll
-        for (int k = 0; k < T::kLoads; ++k) o[k] = load_piece<IO, kVec>(rsrc, row + static_cast<uint32_t>(k * (64 / T::kPieces)) * ld, c, D);
+        for (int k = 0; k < T::kLoads; ++k)
+            o[k] = load_piece<IO, kVec, kPolicy>(rsrc, row + static_cast<uint32_t>(k * (64 / T::kPieces)) * ld, c0 + T::piece(lane) * T::kChannels, D);
     }
 };
 
@@ -298,9 +335,10 @@ __device__ __forceinline__ V4f mfma(float a, float b, V4f c) { return __builtin_
 // The operand of step s (32 channels) of a token's part.
 template <int N>
 __device__ __forceinline__ U4 row_operand(const RowPart<Bf16, N>& p, int s) {
-    constexpr int m = N / 2;
-    return U4{p.w[s], p.w[m + s], p.w[2 * m + s], p.w[3 * m + s]};
+    return U4{p.w[4 * s], p.w[4 * s + 1], p.w[4 * s + 2], p.w[4 * s + 3]};
 }
+// The channel, among a lane's 4 NK, of row r of its four and tile i of the state.
+__device__ __forceinline__ constexpr int state_channel(int i, int r) { return 8 * (i / 2) + 2 * r + i % 2; }
 // Channel k of the eight tokens, as an operand over the tokens.
 template <int N>
 __device__ __forceinline__ U4 col_operand(const ColPart<Bf16, N>& p, int k) {
@@ -379,6 +417,42 @@ __device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
 }
 
 // ---------------------------------------------------------------------------------------------
+// A wave's state and arrays [K][V] of fp32, element (x, y) at x row + y col: four consecutive numbers at a time where they are
+// (one at a time a wave's start and end cost microseconds), else one.
+template <int NK, int NV, typename F4, typename F1>
+__device__ __forceinline__ void state_elements(const void* p, int K, int V, int64_t row, int64_t col, int grp, int vc, F4&& four, F1&& one) {
+    const bool at16 = reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    if (NV == 4 && col == 1 && at16 && V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int x = 4 * NK * grp + state_channel(i, r);
+                if (x < K && vc < V) four(x * row + vc, [&](int k, auto&& f) { f(i, k, r); });
+            }
+    } else if (row == 1 && at16 && K % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < NK; i += 2)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; r += 2) {   // channels 8 (i / 2) + 2 r + 0..3: tiles i, i + 1 of rows r, r + 1
+                    const int x = 4 * NK * grp + state_channel(i, r);
+                    if (x < K && vc + j < V) four(x + (vc + j) * col, [&](int k, auto&& f) { f(i + k % 2, j, r + k / 2); });
+                }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int x = 4 * NK * grp + state_channel(i, r), y = vc + j;
+                    if (x < K && y < V) one(x * row + y * col, i, j, r);
+                }
+    }
+}
+
 // The pass: one wave (a workgroup) per segment, head and block of 16 NV output channels. NK tiles of 16 hold the K
 // contracted channels. A chunk's rows are loaded while the chunk before is worked on.
 
@@ -393,7 +467,7 @@ struct LinTiles {
 };
 
 template <typename IO, int NK, int NV, bool kVec, int kKind>
-__global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass(LinArgs a) {
+__global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass(LinPasses passes) {
     constexpr bool kBf16 = sizeof(IoElem<IO>) == 2;
     constexpr int e = sizeof(IoElem<IO>);
     // parts of the decayed values, and of the state and the scores that are read. The state is fp32 in memory and goes through
@@ -411,7 +485,11 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
     char* const tk = lds + L::kK;
     char* const tv = lds + L::kV;
     const int lane = static_cast<int>(threadIdx.x), grp = lane >> 4, col = lane & 15;
-    const int64_t task = xcd_order(blockIdx.x, gridDim.x);
+    // (the passes of a head side by side: they read the same rows)
+    int64_t task = xcd_order(blockIdx.x, gridDim.x);
+    const int which = static_cast<int>(task % passes.count);
+    const LinArgs& a = passes.a[which];
+    task /= passes.count;
     const int block = static_cast<int>(task % a.blocks);
     const int64_t rest = task / a.blocks, h = rest % a.H, slot = rest / a.H;
     const LinSegment sg = lin_segment(a, slot);
@@ -419,7 +497,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
     const bool desc = (a.rev != 0) != (a.back != 0);
     const int c0 = block * 16 * NV, vc = c0 + NV * col;   // the block's and the lane's value channels
 
-    // state: S[i][j][r] = channel NK (4 grp + r) + i, channel vc + j
+    // state, over e^scaled: S[i][j][r] = key channel 4 NK grp + state_channel(i, r), value channel vc + j
     V4f S[NK][NV];
     const int64_t ks = static_cast<int64_t>(a.K) * a.V;
     {
@@ -428,17 +506,14 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         for (int i = 0; i < NK; ++i)
 #pragma unroll
             for (int j = 0; j < NV; ++j) S[i][j] = V4f{0.0f, 0.0f, 0.0f, 0.0f};
-        if (s0) {
+        if (s0)
+            state_elements<NK, NV>(s0, a.K, a.V, a.s0_row, a.s0_col, grp, vc,
+                [&](int64_t at, auto&& place) {
+                    const V4f w = *reinterpret_cast<const V4f*>(s0 + at);
 #pragma unroll
-            for (int i = 0; i < NK; ++i)
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int x = NK * (4 * grp + r) + i, y = vc + j;
-                        if (x < a.K && y < a.V) S[i][j][r] = s0[x * a.s0_row + y * a.s0_col];
-                    }
-        }
+                    for (int k = 0; k < 4; ++k) place(k, [&](int i, int j, int r) { S[i][j][r] = w[k]; });
+                },
+                [&](int64_t at, int i, int j, int r) { S[i][j][r] = s0[at]; });
     }
 
     HeadRows<IO> R, K, V, W;
@@ -459,6 +534,14 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
     const int flip = desc ? kChunk - 1 : 0;               // (row of position i: i ^ flip)
     const int my_row = (lane & (kChunk - 1)) ^ flip, row0 = col ^ flip, grow0 = (4 * grp) ^ flip, step = desc ? -1 : 1;
     const uint32_t g_ld = static_cast<uint32_t>(a.ld_g) * 4;
+    const uint32_t r_at = R.template at<NK, kVec>(0, lane), k_at = K.template at<NK, kVec>(0, lane);
+    const uint32_t v_at = V.template at<NV, kVec>(c0, lane);
+    // the output's rows: 2 NV lanes to a row, eight channels each
+    constexpr int kLanes = 2 * NV, kRows = 64 / kLanes;
+    const int orow = lane / kLanes, oc = c0 + lane % kLanes * 8, oe = a.o_f32 ? 4 : e;
+    const uint32_t o_ld = static_cast<uint32_t>(a.H) * a.V * oe;
+    const uint32_t o_at = orow * o_ld + (kVec ? (oc < a.V ? static_cast<uint32_t>(oc * oe) : kOutside) : 0u);
+    [[maybe_unused]] const uint32_t w_at = orow * W.ld + (kVec ? piece_at<IO>(oc, W.D) : 0u);
 
     U4 sr[kKind == kLocal ? 1 : TK::kLoads], sk[TK::kLoads], sv[TV::kLoads];
     float gv = 0.0f;
@@ -467,9 +550,14 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         int64_t first;
         int c;
         place(m, &first, &c);
-        if constexpr (kKind != kLocal) R.template load<NK, kVec>(first, c, 0, lane, sr);
-        K.template load<NK, kVec>(first, c, 0, lane, sk);
-        V.template load<NV, kVec>(first, c, c0, lane, sv);
+        auto rows = [&](auto policy) {
+            constexpr int kPolicy = decltype(policy)::value;
+            if constexpr (kKind != kLocal) R.template load<NK, kVec, kPolicy>(first, c, r_at, 0, lane, sr);
+            K.template load<NK, kVec, kPolicy>(first, c, k_at, 0, lane, sk);
+            V.template load<NV, kVec, kPolicy>(first, c, v_at, c0, lane, sv);
+        };
+        if (kVec && a.once) rows(std::integral_constant<int, kOnce>{});
+        else rows(std::integral_constant<int, kKeep>{});
         // the decay of the lane's position (of its half of the wave); moved by one token where the walk goes back, the segment's
         // own tokens only
         const int move = a.back ? (desc ? 1 : -1) : 0, rel = static_cast<int>(first - sg.first) + my_row + move;
@@ -479,24 +567,27 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         gv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gb, in ? my_row * g_ld : kOutside, 0, 0));
     };
 
-    double all = 0.0;    // sum of the decays so far
+    double all = 0.0;      // sum of the log decays so far (in units of log 2, as all here)
+    double scaled = 0.0;   // that since the state was scaled
     if (chunks > 0) load(0);
     for (int m = 0; m < chunks; ++m) {
         int64_t mem;     // the chunk's lowest token, and how many it has
         int cnt;
         place(m, &mem, &cnt);
         // sums of the log decays over the chunk
-        const double run = half_wave_sums(log2_decay(gv));
+        double run = half_wave_sums(log2_decay(gv));
         const double total = lane_value(run, 31);
-        const float2 end = as_pair(total);
         if (kKind == kLocal) all += total;
+        run += scaled;
         wave_sync();
         if constexpr (kKind != kLocal) TK::put(tr, lane, sr);
         TK::put(tk, lane, sk);
         TV::put(tv, lane, sv);
         if (lane < kChunk) sums[lane] = as_pair(run);
+        const double after = scaled + total;
         wave_sync();
         load(m + 1);
+        __builtin_amdgcn_sched_barrier(0);   // (else the compiler moves loads down behind the products)
 
         V4f O[2][NV];
         [[maybe_unused]] float P[2][2][4];   // [key tile][reader tile], rows of keys
@@ -528,7 +619,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
 #pragma unroll
                         for (int i = 0; i < NK; ++i)
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) O[j][v] = mfma(S[i][v][r], rr[j].w[NK * r + i], O[j][v]);
+                            for (int j = 0; j < 2; ++j) O[j][v] = mfma(S[i][v][r], rr[j].w[state_channel(i, r)], O[j][v]);
                 }
             }
             float2 gt[2];
@@ -674,18 +765,15 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                     for (int v = 0; v < NV; ++v) p[NV * r + v] = O[j][v][r];
             }
             wave_sync();
-            const int oe = a.o_f32 ? 4 : e;
-            const uint32_t o_ld = static_cast<uint32_t>(a.H) * a.V * oe;
             const int64_t dst = uniform(reinterpret_cast<int64_t>(a.o) + mem * static_cast<int64_t>(o_ld) + h * a.V * oe);
             const auto ob = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(dst), 0,
                                                               static_cast<uint32_t>((cnt - 1) * o_ld + a.V * oe), kRsrcFlags);
-            [[maybe_unused]] const auto wb = W.chunk(mem, kKind == kGradientDots ? cnt : 0);
-            // 2 NV lanes to a row, eight channels each
-            constexpr int kLanes = 2 * NV, kRows = 64 / kLanes;
-            const int oc = c0 + static_cast<int>(opaque(lane)) % kLanes * 8;
+            [[maybe_unused]] const auto wb = W.chunk(mem, kKind == kGradientDots && a.dots ? cnt : 0);
+            const uint32_t ox = opaque(o_at);
+            [[maybe_unused]] const uint32_t wx = opaque(w_at);
 #pragma unroll
             for (int k = 0; k < kChunk / kRows; ++k) {
-                const int row = static_cast<int>(opaque(lane)) / kLanes + k * kRows;
+                const int row = orow + k * kRows;
                 const char* src = tr + row * TO::kRow + lane % kLanes * 32;
                 float x[8];
                 __builtin_memcpy(x, __builtin_assume_aligned(src, 16), 16);
@@ -693,35 +781,39 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                 if constexpr (kKind == kGradientDots) {
                     // w . o, then the token's own pair
                     constexpr int kW = 8 * e / 16, nw = 16 / e;
-                    U4 w[kW], v[kW];
-#pragma unroll
-                    for (int q = 0; q < kW; ++q) {
-                        w[q] = load_piece<IO, kVec>(wb, static_cast<uint32_t>(row) * W.ld, oc + q * nw, W.D);
-                        v[q] = *reinterpret_cast<const U4*>(tv + row * TV::kRow + lane % kLanes * 8 * e + q * 16);
-                    }
                     auto value = [&](const U4 (&u)[kW], int c) {
                         if constexpr (kBf16) return (c & 1) ? bf16_hi(u[0][c / 2]) : bf16_lo(u[0][c / 2]);
                         else return __uint_as_float(u[c / 4][c % 4]);
                     };
-                    float dot = 0.0f;
+                    if (a.dots) {
+                        U4 w[kW];
+#pragma unroll
+                        for (int q = 0; q < kW; ++q)
+                            w[q] = load_piece<IO, kVec>(wb, !kVec ? wx + static_cast<uint32_t>(k * kRows) * W.ld : q == 0 || oc + nw < W.D ? wx + static_cast<uint32_t>(k * kRows) * W.ld + q * 16 : kOutside,
+                                                        oc + q * nw, W.D);
+                        float dot = 0.0f;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) dot = fmaf(x[c], value(w, c), dot);
+#pragma unroll
+                        for (int q = 1; q < kLanes; q *= 2) dot += __shfl_xor(dot, q);
+                        if (lane % kLanes == 0 && row < cnt) a.dots[(static_cast<int64_t>(block) * a.tokens + mem + row) * a.H + h] = dot;
+                    }
+                    U4 v[kW];
+#pragma unroll
+                    for (int q = 0; q < kW; ++q) v[q] = *reinterpret_cast<const U4*>(tv + row * TV::kRow + lane % kLanes * 8 * e + q * 16);
                     const float p = same[row ^ flip];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        dot = fmaf(x[c], value(w, c), dot);
-                        x[c] = fmaf(p, value(v, c), x[c]);
-                    }
-#pragma unroll
-                    for (int q = 1; q < kLanes; q *= 2) dot += __shfl_xor(dot, q);
-                    if (lane % kLanes == 0 && row < cnt) a.dots[(static_cast<int64_t>(block) * a.tokens + mem + row) * a.H + h] = dot;
+                    for (int c = 0; c < 8; ++c) x[c] = fmaf(p, value(v, c), x[c]);
                 }
-                const uint32_t at = static_cast<uint32_t>(row) * o_ld;
+                const uint32_t at = ox + static_cast<uint32_t>(k * kRows) * o_ld;
                 if (!kBf16 || a.o_f32) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         if constexpr (kVec) {
+                            // (in fp32 rows of whole pieces may end between the two)
                             U4 w;
                             __builtin_memcpy(&w, x + 4 * q, 16);
-                            __builtin_amdgcn_raw_buffer_store_b128(w, ob, oc + 4 * q < a.V ? at + (oc + 4 * q) * 4 : kOutside, 0, 0);
+                            __builtin_amdgcn_raw_buffer_store_b128(w, ob, q == 0 || oc + 4 < a.V ? at + 16 * q : kOutside, 0, 0);
                         } else {
 #pragma unroll
                             for (int c = 4 * q; c < 4 * q + 4; ++c)
@@ -730,7 +822,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                     }
                 } else if constexpr (kVec) {
                     const U4 w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
-                    __builtin_amdgcn_raw_buffer_store_b128(w, ob, oc < a.V ? at + oc * 2 : kOutside, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(w, ob, at, 0, 0);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
@@ -738,22 +830,30 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                 }
             }
         }
-        // S = e^{G_end} S + keys^T (values, decayed to the chunk's end)
-        const float keep = fast_exp2(end.x + end.y);
+        // S = e^{G_end} S + keys^T (values, decayed to the chunk's end). S is held over the decay since it was last scaled, so that
+        // it need not be scaled in every chunk: the values are decayed to that point instead, which for more than 2^-16
+        // costs no digits and stays in range.
+        float2 end = make_float2(0.0f, 0.0f);
+        scaled = after;
+        if (!(after > -16.0 && after < 16.0)) {
+            end = as_pair(after);
+            scaled = 0.0;
+            const float keep = fast_exp2(end.x + end.y);
+#pragma unroll
+            for (int i = 0; i < NK; ++i)
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[i][j][r] *= keep;
+        }
         float out[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) out[k] = decay_between(end, sums[(k & 4) * 4 + 4 * grp + (k & 3)]) * a.key_scale;
         ColPart<IO, NK> kc;
-        TK::columns(tk, grow0, step, col, kc);
+        TK::state_columns(tk, grow0, step, col, kc);
         if constexpr (kBf16)
 #pragma unroll
             for (int i = 0; i < NK; ++i) kop[i] = col_operand<NK>(kc, i);
-#pragma unroll
-        for (int i = 0; i < NK; ++i)
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[i][j][r] *= keep;
         if constexpr (kBf16) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -777,7 +877,17 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         }
     }
 
-    // what is left: the decay of the last token, where decays were moved; the segment's or sequence's state
+    // what is left: the state's scale; the decay of the last token, where decays were moved; the segment's or sequence's state
+    {
+        const float2 p = as_pair(scaled);
+        const float keep = fast_exp2(p.x + p.y);
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[i][j][r] *= keep;
+    }
     float rest_decay = 1.0f;
     if (a.back && n > 0) {
         const int64_t tok = desc ? sg.first : sg.first + n - 1;
@@ -789,15 +899,14 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         if (a.cdot) {
             const float* ep = lin_state(a.e, a.e_by_slot, slot, sg.seq, a, h);
             float sum = 0.0f;
+            if (ep)
+                state_elements<NK, NV>(ep, a.K, a.V, a.e_row, a.e_col, grp, vc,
+                    [&](int64_t at, auto&& place) {
+                        const V4f w = *reinterpret_cast<const V4f*>(ep + at);
 #pragma unroll
-            for (int i = 0; i < NK; ++i)
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int x = NK * (4 * grp + r) + i, y = vc + j;
-                        if (ep && x < a.K && y < a.V) sum = fmaf(S[i][j][r], ep[x * a.e_row + y * a.e_col], sum);
-                    }
+                        for (int k = 0; k < 4; ++k) place(k, [&](int i, int j, int r) { sum = fmaf(S[i][j][r], w[k], sum); });
+                    },
+                    [&](int64_t at, int i, int j, int r) { sum = fmaf(S[i][j][r], ep[at], sum); });
             sum = over_groups(sum);
             for (int m = 1; m < 16; m *= 2) sum += __shfl_xor(sum, m);
             if (lane == 0) a.cdot[(slot * a.H + h) * a.blocks + block] = sum;
@@ -810,21 +919,20 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
     const bool write = a.s_end && (kKind == kLocal || (a.back ? sg.head : sg.last));
     if (write) {
         float* dst = a.s_end + ((kKind == kLocal ? slot : sg.seq) * a.H + h) * ks;
+        state_elements<NK, NV>(dst, a.K, a.V, a.V, 1, grp, vc,
+            [&](int64_t at, auto&& place) {
+                V4f w;
 #pragma unroll
-        for (int i = 0; i < NK; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int x = NK * (4 * grp + r) + i;
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    if (x < a.K && vc + j < a.V) dst[static_cast<int64_t>(x) * a.V + vc + j] = S[i][j][r] * rest_decay;
-            }
+                for (int k = 0; k < 4; ++k) place(k, [&](int i, int j, int r) { w[k] = S[i][j][r] * rest_decay; });
+                *reinterpret_cast<V4f*>(dst + at) = w;
+            },
+            [&](int64_t at, int i, int j, int r) { dst[at] = S[i][j][r] * rest_decay; });
     }
 }
 
 // Queues a pass on a grid of its waves.
 template <typename IO, int kKind>
-void launch_lin_pass(const LinArgs& a, bool vec, hipStream_t s);
+void launch_lin_pass(const LinPasses& p, bool vec, hipStream_t s);
 
 }  // namespace vimscan_dev
 

@@ -20,17 +20,17 @@ int check_dims(const vimscan_launch* l, int64_t heads, int64_t groups) {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Segments: waves enough for every SIMD of the chip (1024) twice, of at least two chunks each.
-int64_t segment(int64_t length, int64_t waves) {
-    constexpr int64_t kEnough = 1024, kTarget = 2048, kLeast = 2 * kLinChunk, kMost = 4096;
-    int64_t seg = kMost;
-    if (waves < kEnough) {
-        const int64_t parts = up(kTarget, waves);
-        seg = up(up(length, parts), kLinChunk) * kLinChunk;
-        if (seg < kLeast) seg = kLeast;
-        if (seg > kMost) seg = kMost;
-    }
-    return seg;
+// Tokens per segment, or 0: sequences stay whole. As many segments as fill the chip's places for waves (1024 SIMDs) once and do not
+// start a second round. The segments' own states and their fold cost about as much as 0.6 of the pass and three chunks: where that is
+// not less than the chunks saved, sequences stay whole.
+int64_t segment(int64_t length, int64_t waves, int64_t places) {
+    constexpr int64_t kLeast = 2, kMost = 128;   // chunks
+    const int64_t chunks = up(length, kLinChunk), parts = places / waves;
+    if (parts < 2) return chunks > kMost ? kMost * kLinChunk : 0;
+    int64_t seg = up(chunks, parts);
+    if (seg < kLeast) seg = kLeast;
+    if (seg > kMost) seg = kMost;
+    return 10 * chunks <= 16 * seg + 30 ? 0 : seg * kLinChunk;
 }
 
 // The whole extent of [tokens][heads][d] with strides.
@@ -78,13 +78,14 @@ int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, i
     p->dk = l->d_state;
     p->dv = l->d_inner / heads;
     if (p->nseq == 0) return VIMSCAN_OK;
-    const int64_t length = packed ? up(p->tokens, p->nseq) : p->Lp;
+    // (packed sequences: the longest is taken to be twice the mean)
+    const int64_t twice = packed ? 2 * up(p->tokens, p->nseq) : 0, length = !packed ? p->Lp : twice < p->tokens ? twice : p->tokens;
     const int64_t blocks = lin_blocks(p->dv), qblocks = lin_blocks(p->dk);
     const int64_t most_waves = kMaxLinWaves / ((blocks > qblocks ? blocks : qblocks) * heads);
     if (p->nseq > most_waves) return VIMSCAN_ERR_SHAPE;
-    p->seg = segment(length, p->nseq * heads * blocks);
-    // (packed sequences may be longer than their mean)
-    p->split = packed ? p->tokens > p->seg && length > p->seg / 2 : p->Lp > p->seg;
+    const int per_simd = lin_waves_per_simd(static_cast<int>(io_bytes(l)), lin_contract_tiles(p->dk), lin_output_tiles(p->dv));
+    p->seg = segment(length, p->nseq * heads * blocks, 1024 * per_simd);
+    p->split = p->seg > 0;
     p->segs = p->split && !packed ? up(p->Lp, p->seg) : 1;
     p->slots = !p->split ? p->nseq : packed ? p->tokens / p->seg + p->nseq : p->nseq * p->segs;
     if (!p->split) p->seg = p->Lp;
