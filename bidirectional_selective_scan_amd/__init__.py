@@ -14,7 +14,8 @@ def __getattr__(name):
                 "load_library", "launch_info", "gated_fwd", "gated_step", "gated_info", "block_norm", "norm_info",
                 "PreparedGated", "PreparedGatedGrad", "PreparedGatedStep", "PreparedBlockNorm",
                 "PreparedBlockNormGrad", "linattn_fwd", "linattn_step", "linattn_info", "PreparedLinAttn",
-                "PreparedLinAttnGrad", "PreparedLinAttnStep"):
+                "PreparedLinAttnGrad", "PreparedLinAttnStep", "layer_norm", "layernorm_info", "PreparedLayerNorm",
+                "PreparedLayerNormGrad"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

@@ -1,11 +1,13 @@
-"""The recurrent block's operators as differentiable torch functions: forward and backward both run
-the library's kernels (see ``block``). Gradients of gradients are not defined and raise."""
+"""The block operators as differentiable torch functions: forward and backward both run the library's
+kernels (see ``block`` and ``attention``). Gradients of gradients are not defined and raise."""
 from __future__ import annotations
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from .block import GatedInputs, PreparedBlockNorm, PreparedBlockNormGrad, PreparedGated, PreparedGatedGrad
+from .attention import LinAttnInputs, PreparedLinAttn, PreparedLinAttnGrad
+from .block import (GatedInputs, PreparedBlockNorm, PreparedBlockNormGrad, PreparedGated, PreparedGatedGrad,
+                    PreparedLayerNorm, PreparedLayerNormGrad)
 
 
 class _GatedRecurrence(torch.autograd.Function):
@@ -66,3 +68,63 @@ def block_norm(x, z=None, w_post=None, residual=None, gamma=None, w_pre=None, ep
     """Differentiable (sum, n) of the block norm (arguments as ``PreparedBlockNorm``; n is None without
     w_pre) in x, z, w_post, residual, gamma and w_pre."""
     return _BlockNorm.apply(x, z, w_post, residual, gamma, w_pre, float(eps), bool(gate_after), res_dtype)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, eps, res_dtype, with_sum):
+        call = PreparedLayerNorm(x, residual, weight, bias, eps, res_dtype, with_sum=with_sum)
+        call()
+        ctx.save_for_backward(x, residual, weight, bias)
+        ctx.scalars = (eps, res_dtype)
+        ctx.set_materialize_grads(False)
+        return call.sum, call.n
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dsum, dn):
+        x, residual, weight, bias = ctx.saved_tensors
+        eps, res_dtype = ctx.scalars
+        dsum = None if dsum is None else dsum.contiguous()
+        dn = None if dn is None else dn.contiguous()
+        g = PreparedLayerNormGrad(x, residual, weight, bias, dsum, dn, eps, res_dtype,
+                                  weights=ctx.needs_input_grad[2] or ctx.needs_input_grad[3])
+        g()
+        return g.dx, g.dresidual, g.dweight, g.dbias, None, None, None
+
+
+def layer_norm(x, residual=None, weight=None, bias=None, eps: float = 1e-5, res_dtype=None, with_sum=None):
+    """Differentiable (sum, n) of the layer norm (arguments as ``PreparedLayerNorm``; sum is None without a residual, unless
+    ``with_sum``) in x, residual, weight and bias."""
+    return _LayerNorm.apply(x, residual, weight, bias, float(eps), res_dtype, with_sum)
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, h0, offsets, scale, seg_len, reverse):
+        inp = LinAttnInputs(q, k, v, log_decay, scale, h0, seg_len, offsets, reverse)
+        call = PreparedLinAttn(inp)
+        call()
+        ctx.save_for_backward(q, k, v, log_decay, h0, offsets)
+        ctx.scalars = (inp.scale, seg_len, reverse)
+        ctx.set_materialize_grads(False)
+        return call.y, call.h_last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh_last):
+        q, k, v, log_decay, h0, offsets = ctx.saved_tensors
+        scale, seg_len, reverse = ctx.scalars
+        inp = LinAttnInputs(q, k, v, log_decay, scale, h0, seg_len, offsets, reverse)
+        dy = None if dy is None else dy.contiguous()
+        dh_last = None if dh_last is None else dh_last.contiguous()
+        g = PreparedLinAttnGrad(inp, dy, dh_last, decays=ctx.needs_input_grad[3])
+        g()
+        return g.dq, g.dk, g.dv, g.dlog_decay, g.dh0, None, None, None, None
+
+
+def linear_attention(q, k, v, log_decay, scale=None, h0=None, seg_len: int = 0, offsets=None, reverse: bool = False):
+    """Differentiable (y, h_last) of linear attention with a decay for each head (arguments as ``PreparedLinAttn``) in q, k,
+    v, log_decay and h0."""
+    return _LinearAttention.apply(q, k, v, log_decay, h0, offsets, None if scale is None else float(scale), int(seg_len),
+                                  bool(reverse))

@@ -53,7 +53,8 @@ EXPORTED = ("vimscan_bidir_fwd", "vimscan_bidir_conv_fwd", "vimscan_fwd", "vimsc
             "vimscan_ncssd_plan", "vimscan_bidir_order_fwd", "vimscan_bidir_fwd_noalloc", "vimscan_wait_timeouts",
             "vimscan_gated_fwd", "vimscan_gated_bwd", "vimscan_gated_step", "vimscan_gated_plan", "vimscan_norm_fwd",
             "vimscan_norm_bwd", "vimscan_norm_plan", "vimscan_gated_wait_reads", "vimscan_gated_alone",
-            "vimscan_linattn_fwd", "vimscan_linattn_bwd", "vimscan_linattn_step", "vimscan_linattn_plan")
+            "vimscan_linattn_fwd", "vimscan_linattn_bwd", "vimscan_linattn_step", "vimscan_linattn_plan",
+            "vimscan_layernorm_fwd", "vimscan_layernorm_bwd", "vimscan_layernorm_plan")
 
 # Size of the static scratch array behind vimscan_bidir_fwd_noalloc (VIMSCAN_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 96 << 20
@@ -376,8 +377,8 @@ def ncssd_fwd(x, B, C, m, seg_len: int = 0, out=None, chunk_len: int = 0, worksp
 
 # The recurrent block's operators (block.py, which uses the helpers above) are part of this interface.
 _BLOCK_NAMES = ("GATED_STRIDE", "GatedInputs", "PreparedBlockNorm", "PreparedBlockNormGrad", "PreparedGated",
-                "PreparedGatedGrad", "PreparedGatedStep", "block_norm", "gated_alone", "gated_fwd", "gated_info", "gated_step",
-                "gated_wait_reads", "norm_info")
+                "PreparedGatedGrad", "PreparedGatedStep", "PreparedLayerNorm", "PreparedLayerNormGrad", "block_norm", "gated_alone", "gated_fwd", "gated_info", "gated_step",
+                "gated_wait_reads", "layer_norm", "layernorm_info", "norm_info")
 # So are those of linear attention (attention.py).
 _ATTENTION_NAMES = ("LinAttnInputs", "PreparedLinAttn", "PreparedLinAttnGrad", "PreparedLinAttnStep", "linattn_fwd",
                     "linattn_info", "linattn_step")

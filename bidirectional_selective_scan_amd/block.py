@@ -1,5 +1,5 @@
-"""Binding of the recurrent block's operators: the gated linear recurrence (``vimscan_gated_*``) and
-the block norm (``vimscan_norm_*``) of include/vimscan.h, each with its backward pass.
+"""Binding of the recurrent block's operators: the gated linear recurrence (``vimscan_gated_*``), the block
+norm (``vimscan_norm_*``) and the layer norm (``vimscan_layernorm_*``) of include/vimscan.h, each with its backward pass.
 
 As in ``binding``: a Prepared* object validates once and owns its output tensors, calling it queues
 the kernels (one ctypes call) and does not synchronise. Work goes to torch's current stream for the
@@ -41,6 +41,16 @@ class _NormGrad(ctypes.Structure):
                 ("dresidual", _vp), ("dw_post", _vp), ("dgamma", _vp), ("dw_pre", _vp)]
 
 
+class _LayerNorm(ctypes.Structure):
+    _fields_ = [("x", _vp), ("ld_x", _i64), ("residual", _vp), ("weight", _vp), ("bias", _vp), ("eps", ctypes.c_float),
+                ("res_dtype", ctypes.c_int32)]
+
+
+class _LayerNormGrad(ctypes.Structure):
+    _fields_ = [("dsum", _vp), ("dn", _vp), ("dx", _vp), ("ld_dx", _i64), ("dresidual", _vp), ("dweight", _vp),
+                ("dbias", _vp)]
+
+
 def declare(lib):
     """Argument types of this module's entry points on an opened library."""
     launch = ctypes.POINTER(_b._Launch)
@@ -54,7 +64,11 @@ def declare(lib):
     lib.vimscan_norm_fwd.argtypes = [ctypes.POINTER(_Norm), _vp, _vp, launch]
     lib.vimscan_norm_bwd.argtypes = [ctypes.POINTER(_Norm), ctypes.POINTER(_NormGrad), launch]
     lib.vimscan_norm_plan.argtypes = [launch, ctypes.c_int, plan]
-    for f in (lib.vimscan_gated_fwd, lib.vimscan_gated_bwd, lib.vimscan_gated_step, lib.vimscan_gated_plan,
+    lib.vimscan_layernorm_fwd.argtypes = [ctypes.POINTER(_LayerNorm), _vp, _vp, launch]
+    lib.vimscan_layernorm_bwd.argtypes = [ctypes.POINTER(_LayerNorm), ctypes.POINTER(_LayerNormGrad), launch]
+    lib.vimscan_layernorm_plan.argtypes = [launch, ctypes.c_int, plan]
+    for f in (lib.vimscan_layernorm_fwd, lib.vimscan_layernorm_bwd, lib.vimscan_layernorm_plan, lib.vimscan_gated_fwd,
+              lib.vimscan_gated_bwd, lib.vimscan_gated_step, lib.vimscan_gated_plan,
               lib.vimscan_gated_wait_reads, lib.vimscan_gated_alone, lib.vimscan_norm_fwd, lib.vimscan_norm_bwd,
               lib.vimscan_norm_plan):
         f.restype = ctypes.c_int
@@ -498,4 +512,117 @@ def norm_info(rows, d, io_dtype="bf16", backward=False) -> dict:
     launch = _b.make_launch(rows, 1, d, 0, code)
     plan = _b._Plan()
     _b._check(_b.load_library().vimscan_norm_plan(ctypes.byref(launch), int(backward), ctypes.byref(plan)))
+    return _plan_dict(plan)
+
+
+# ------------------------------------------------------------------------------------------
+# Layer norm
+
+
+class _LayerNormInputs:
+    def __init__(self, x, residual, weight, bias, eps, res_dtype):
+        if x.dim() < 1:
+            raise ValueError("x must be (..., d)")
+        dev = x.device
+        if dev.type != "cuda":
+            raise ValueError("inputs must be on a GPU device")
+        self.io = _b._io_code(x.dtype)
+        self.dev, self.dtype, self.shape = dev, x.dtype, tuple(x.shape)
+        self.rows = 1
+        for v in x.shape[:-1]:
+            self.rows *= v
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            if t is not None:
+                _check_tensor(t, name, dev, torch.float32, (x.shape[-1],))
+        if residual is not None:
+            if res_dtype is not None and res_dtype != residual.dtype:
+                raise ValueError("res_dtype is the residual's dtype")
+            res_dtype = residual.dtype
+            _check_tensor(residual, "residual", dev, res_dtype, self.shape)
+        self.res_dtype = x.dtype if res_dtype is None else res_dtype
+        self.tensors = (x, residual, weight, bias)
+        self.struct = _LayerNorm(_ptr(x), row_stride(x, "x"), _ptr(residual), _ptr(weight), _ptr(bias), float(eps),
+                                 _b._io_code(self.res_dtype))
+
+    def launch(self, stream):
+        return _b.make_launch(self.rows, 1, self.shape[-1], 0, self.io, 0, stream=stream)
+
+
+class PreparedLayerNorm(_Call):
+    """Layer norm with the residual add in front of it (vimscan_layernorm_fwd). Per row of x (..., D):
+
+        sum = x + residual,  n = (sum - mean) / sqrt(mean((sum - mean)^2) + eps) weight + bias
+
+    residual, weight and bias may be None, which leaves them out. x: float32 or bfloat16, rows evenly spaced;
+    weight, bias: (D,) float32; residual like x, contiguous, in x's dtype or float32. Calling it fills ``n`` (x's dtype) and
+    ``sum`` (the residual's dtype, without one res_dtype or x's; None unless ``with_sum``, which is by default whether
+    there is a residual) and returns both. ``out_sum`` may be the residual itself."""
+
+    def __init__(self, x, residual=None, weight=None, bias=None, eps: float = 1e-5, res_dtype=None, out_sum=None,
+                 out_n=None, with_sum=None, stream=None):
+        lib = _b.load_library()
+        inp = _LayerNormInputs(x, residual, weight, bias, eps, res_dtype)
+        if with_sum is None:
+            with_sum = residual is not None or out_sum is not None
+        if not with_sum and out_sum is not None:
+            raise ValueError("without the sum there must be no out_sum")
+        self.sum = _output(out_sum, "out_sum", inp.dev, inp.res_dtype, inp.shape) if with_sum else None
+        self.n = _output(out_n, "out_n", inp.dev, inp.dtype, inp.shape)
+        launch = inp.launch(_stream_of(inp.dev, stream))
+        args = (ctypes.byref(inp.struct), _ptr(self.sum), _ptr(self.n), ctypes.byref(launch))
+        own = [t for t, gv in ((self.sum, out_sum), (self.n, out_n)) if t is not gv]
+        self._prepare(inp.dev, stream, launch, lib.vimscan_layernorm_fwd, args, own, (inp,))
+
+    def __call__(self):
+        self._queue()
+        return self.sum, self.n
+
+
+class PreparedLayerNormGrad(_Call):
+    """Gradients of a layer norm (vimscan_layernorm_bwd) from its inputs and the gradients dsum and dn of its
+    outputs (None: zero). Calling it fills ``dx``, ``dresidual`` and the sums over the rows ``dweight`` and ``dbias``
+    (float32; ``weights`` false leaves them out); those of absent inputs are None."""
+
+    def __init__(self, x, residual=None, weight=None, bias=None, dsum=None, dn=None, eps: float = 1e-5, res_dtype=None,
+                 weights: bool = True, workspace=None, stream=None):
+        lib = _b.load_library()
+        if dsum is not None and residual is None and res_dtype is None:
+            res_dtype = dsum.dtype
+        inp = _LayerNormInputs(x, residual, weight, bias, eps, res_dtype)
+        dev, D = inp.dev, inp.shape[-1]
+        if dsum is not None:
+            _check_tensor(dsum, "dsum", dev, inp.res_dtype, inp.shape)
+        if dn is not None:
+            _check_tensor(dn, "dn", dev, inp.dtype, inp.shape)
+        self.dx = torch.empty(inp.shape, dtype=inp.dtype, device=dev)
+        self.dresidual = torch.empty(inp.shape, dtype=inp.res_dtype, device=dev) if residual is not None else None
+        self.dweight, self.dbias = (torch.empty(D, dtype=torch.float32, device=dev) if weights and t is not None else None
+                                    for t in (weight, bias))
+        launch = inp.launch(_stream_of(dev, stream))
+        plan = _b._Plan()
+        _b._check(lib.vimscan_layernorm_plan(ctypes.byref(launch), 1, ctypes.byref(plan)))
+        self.plan = _plan_dict(plan)
+        ws = _workspace(workspace, plan.workspace_bytes, dev, launch)
+        g = _LayerNormGrad(_ptr(dsum), _ptr(dn), _ptr(self.dx), D, _ptr(self.dresidual), _ptr(self.dweight), _ptr(self.dbias))
+        args = (ctypes.byref(inp.struct), ctypes.byref(g), ctypes.byref(launch))
+        own = [self.dx, self.dresidual, self.dweight, self.dbias] + ([ws] if ws is not workspace else [])
+        self._prepare(dev, stream, launch, lib.vimscan_layernorm_bwd, args, own, (inp, g, dsum, dn, ws))
+
+    def __call__(self):
+        self._queue()
+        return self.dx
+
+
+def layer_norm(x, residual=None, weight=None, bias=None, eps: float = 1e-5, res_dtype=None, with_sum=None):
+    """The layer norm on the GPU: (sum, n); arguments as ``PreparedLayerNorm``. Queued on torch's current
+    stream; does not synchronise."""
+    return PreparedLayerNorm(x, residual, weight, bias, eps, res_dtype, with_sum=with_sum)()
+
+
+def layernorm_info(rows, d, io_dtype="bf16", backward=False) -> dict:
+    """The library's plan for a layer norm of this shape (host only; vimscan_layernorm_plan)."""
+    code = _b.VIMSCAN_BF16 if io_dtype == "bf16" else _b.VIMSCAN_F32
+    launch = _b.make_launch(rows, 1, d, 0, code)
+    plan = _b._Plan()
+    _b._check(_b.load_library().vimscan_layernorm_plan(ctypes.byref(launch), int(backward), ctypes.byref(plan)))
     return _plan_dict(plan)

@@ -1,4 +1,4 @@
-// Host side of the gated recurrence and the block norm (see block_plan.h).
+// Host side of the gated recurrence, the block norm and the layer norm (see block_plan.h).
 
 #include "block_plan.h"
 
@@ -141,15 +141,15 @@ int check_gated_step(const vimscan_gated* g, const float* state, int64_t nslots,
     return any_meet(outs, ins) || meet(outs[0], outs[1]) ? VIMSCAN_ERR_ALIAS : VIMSCAN_OK;
 }
 
-int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p) {
-    const int rc = check_launch(l, 0, VIMSCAN_FLAG_GATE_AFTER);
-    if (rc != VIMSCAN_OK) return rc;
+namespace {
+
+int plan_rows(const vimscan_launch* l, bool backward, int weights, NormPlan* p) {
     if (l->d_inner > kNormMaxWidth) return VIMSCAN_ERR_SHAPE;
     std::memset(p, 0, sizeof(*p));
     p->rows = l->batch * l->seqlen;
     p->D = l->d_inner;
     if (p->rows == 0 || p->D == 0) return VIMSCAN_OK;
-    // enough workgroups for every CU's waves; fewer, each with more rows, where every one leaves three rows
+    // enough workgroups for every CU's waves; fewer, each with more rows, where every one leaves two or three rows
     // of partial weight gradients
     const int64_t most = p->D <= 256 ? 2048 : 512;
     const int64_t at_once = l->io_dtype == VIMSCAN_F32 && p->D % 4 != 0 ? rows_at_once(kNormSingles, p->D)
@@ -158,8 +158,20 @@ int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p) {
     const int64_t turns = (p->rows + at_once - 1) / at_once;
     p->wgs = turns < most ? turns : most;
     p->rows_per_wg = (turns + p->wgs - 1) / p->wgs * at_once;
-    if (backward) p->ws = up256(static_cast<size_t>(p->wgs) * 3 * p->D * sizeof(float));
+    if (backward) p->ws = up256(static_cast<size_t>(p->wgs) * weights * p->D * sizeof(float));
     return VIMSCAN_OK;
+}
+
+}  // namespace
+
+int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p) {
+    const int rc = check_launch(l, 0, VIMSCAN_FLAG_GATE_AFTER);
+    return rc != VIMSCAN_OK ? rc : plan_rows(l, backward, 3, p);
+}
+
+int make_layernorm_plan(const vimscan_launch* l, bool backward, NormPlan* p) {
+    const int rc = check_launch(l, 0, 0);
+    return rc != VIMSCAN_OK ? rc : plan_rows(l, backward, 2, p);
 }
 
 int check_norm_call(const vimscan_norm* n, const void* sum, const void* out, const vimscan_norm_grad* g,
@@ -225,6 +237,56 @@ int check_norm_call(const vimscan_norm* n, const void* sum, const void* out, con
     return any_meet(w, rin) || any_meet(w, rout) ? VIMSCAN_ERR_ALIAS : VIMSCAN_OK;
 }
 
+int check_layernorm_call(const vimscan_layernorm* n, const void* sum, const void* out, const vimscan_layernorm_grad* g,
+                         const vimscan_launch* l, const NormPlan& p) {
+    const int64_t rows = p.rows, d = l->d_inner;
+    const size_t e = io_bytes(l);
+    if (n->res_dtype != VIMSCAN_F32 && n->res_dtype != l->io_dtype) return VIMSCAN_ERR_DTYPE;
+    const size_t re = n->res_dtype == VIMSCAN_F32 ? 4 : 2;
+    if (!positive(n->eps)) return VIMSCAN_ERR_PARAM;
+    if (!good_stride(n->ld_x, d)) return VIMSCAN_ERR_PARAM;
+    if (rows == 0 || d == 0) {  // pointers may be NULL; an empty backward pass still zeroes weight gradients
+        if (!g || d == 0) return VIMSCAN_OK;
+    } else if (!n->x || (!g && !out)) {
+        return VIMSCAN_ERR_NULL;
+    }
+    if (g) {
+        if ((g->dweight && !n->weight) || (g->dbias && !n->bias)) return VIMSCAN_ERR_PARAM;
+        if (rows > 0 && g->dresidual && !n->residual) return VIMSCAN_ERR_PARAM;
+        if (g->dx && !good_stride(g->ld_dx, d)) return VIMSCAN_ERR_PARAM;
+    }
+    const void* io[] = {n->x, out, g ? g->dn : nullptr, g ? g->dx : nullptr};
+    for (const void* q : io)
+        if (!is_aligned(q, e)) return VIMSCAN_ERR_ALIGN;
+    const void* rs[] = {n->residual, sum, g ? g->dsum : nullptr, g ? g->dresidual : nullptr};
+    for (const void* q : rs)
+        if (!is_aligned(q, re)) return VIMSCAN_ERR_ALIGN;
+    const void* w4[] = {n->weight, n->bias, g ? g->dweight : nullptr, g ? g->dbias : nullptr};
+    for (const void* q : w4)
+        if (!is_aligned(q, 4)) return VIMSCAN_ERR_ALIGN;
+    const Span res = dense_span(n->residual, rows, d, re);
+    const Span ins[] = {rows_span(n->x, rows, n->ld_x, d, e), dense_span(n->weight, 1, d, 4), dense_span(n->bias, 1, d, 4)};
+    if (!g) {
+        const Span outs[] = {dense_span(sum, rows, d, re), dense_span(out, rows, d, e)};
+        if (any_meet(outs, ins) || meet(outs[0], outs[1]) || meet(outs[1], res)) return VIMSCAN_ERR_ALIAS;
+        return sum != n->residual && meet(outs[0], res) ? VIMSCAN_ERR_ALIAS : VIMSCAN_OK;
+    }
+    const Span dsum = dense_span(g->dsum, rows, d, re), dres = dense_span(g->dresidual, rows, d, re);
+    const Span rin[] = {res, dsum, dense_span(g->dn, rows, d, e)};
+    const Span outs[] = {rows_span(g->dx, rows, g->ld_dx, d, e), dense_span(g->dweight, 1, d, 4), dense_span(g->dbias, 1, d, 4)};
+    const Span rout[] = {dres};
+    if (any_meet(outs, ins) || any_meet(outs, rin) || any_meet(outs, rout) || any_meet(rout, ins) || meet(dres, res) ||
+        meet(dres, rin[2]))
+        return VIMSCAN_ERR_ALIAS;
+    if (g->dresidual != g->dsum && meet(dres, dsum)) return VIMSCAN_ERR_ALIAS;
+    if (meet(outs[0], outs[1]) || meet(outs[0], outs[2]) || meet(outs[1], outs[2])) return VIMSCAN_ERR_ALIAS;
+    if (!g->dweight && !g->dbias) return VIMSCAN_OK;
+    const int rc = check_workspace(l, p.ws, ins, outs);
+    if (rc != VIMSCAN_OK || p.ws == 0) return rc;
+    const Span w[] = {{l->workspace, p.ws}};
+    return any_meet(w, rin) || any_meet(w, rout) ? VIMSCAN_ERR_ALIAS : VIMSCAN_OK;
+}
+
 }  // namespace vimscan_host
 
 using namespace vimscan_host;
@@ -248,11 +310,9 @@ int vimscan_gated_plan(const vimscan_launch* launch, int64_t seg_len, int packed
     return VIMSCAN_OK;
 }
 
-int vimscan_norm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan) {
-    if (!plan) return VIMSCAN_ERR_NULL;
-    NormPlan p;
-    const int rc = make_norm_plan(launch, backward != 0, &p);
-    if (rc != VIMSCAN_OK) return rc;
+namespace {
+
+void tell_rows(const NormPlan& p, int backward, vimscan_plan* plan) {
     std::memset(plan, 0, sizeof(*plan));
     plan->sequences = p.rows;
     plan->seq_tokens = p.rows > 0 ? 1 : 0;
@@ -261,7 +321,24 @@ int vimscan_norm_plan(const vimscan_launch* launch, int backward, vimscan_plan* 
     plan->workgroups = p.wgs;
     plan->kernels = p.wgs == 0 ? 0 : (backward ? 2 : 1);
     plan->workspace_bytes = p.ws;
-    return VIMSCAN_OK;
+}
+
+}  // namespace
+
+int vimscan_norm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan) {
+    if (!plan) return VIMSCAN_ERR_NULL;
+    NormPlan p;
+    const int rc = make_norm_plan(launch, backward != 0, &p);
+    if (rc == VIMSCAN_OK) tell_rows(p, backward, plan);
+    return rc;
+}
+
+int vimscan_layernorm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan) {
+    if (!plan) return VIMSCAN_ERR_NULL;
+    NormPlan p;
+    const int rc = make_layernorm_plan(launch, backward != 0, &p);
+    if (rc == VIMSCAN_OK) tell_rows(p, backward, plan);
+    return rc;
 }
 
 }  // extern "C"

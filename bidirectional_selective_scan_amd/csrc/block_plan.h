@@ -1,4 +1,4 @@
-// Host side of the recurrent block's operators (gated recurrence, block norm): execution plans and
+// Host side of the recurrent block's operators (gated recurrence, block norm, layer norm): execution plans and
 // every argument check an entry point makes before its first HIP call. Plain C++, as plan.h.
 #ifndef VIMSCAN_BLOCK_PLAN_H
 #define VIMSCAN_BLOCK_PLAN_H
@@ -74,10 +74,14 @@ constexpr NormSpread kNormSingles[] = {{4, 16, 1, 1}, {4, 32, 1, 1}, {4, 64, 1, 
 struct NormPlan {
     int64_t rows, D;
     int64_t wgs, rows_per_wg;      // workgroups launched, and the rows that the first of them takes
-    size_t ws;                     // three rows of partial weight gradients for each
+    size_t ws;                     // rows of partial weight gradients for each (three; of a layer norm two)
 };
 
 int make_norm_plan(const vimscan_launch* l, bool backward, NormPlan* p);
+// Of a layer norm: the same spreads, two rows of partial weight gradients.
+int make_layernorm_plan(const vimscan_launch* l, bool backward, NormPlan* p);
+int check_layernorm_call(const vimscan_layernorm* n, const void* sum, const void* out, const vimscan_layernorm_grad* grad,
+                         const vimscan_launch* l, const NormPlan& p);
 int check_norm_call(const vimscan_norm* n, const void* sum, const void* out, const vimscan_norm_grad* grad,
                     const vimscan_launch* l, const NormPlan& p);
 

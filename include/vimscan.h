@@ -456,6 +456,48 @@ int vimscan_norm_bwd(const vimscan_norm* p, const vimscan_norm_grad* grad, const
 int vimscan_norm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan);
 
 /*
+ * Layer norm, with the residual add in front of it. Per row (token) of d_inner channels:
+ *   s = x + residual                                                    (residual; else s = x)
+ *   n = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps) * weight + bias   (weight, bias: each optional)
+ * All in fp32, rounded once at the outputs (n is formed from s before its rounding).
+ * Rows: launch->batch * seqlen; width d_inner <= 32768 (VIMSCAN_ERR_SHAPE); d_state must be 0, chunk_len and
+ * flags 0. x rows are ld_x elements apart; residual, sum and n are dense. residual and sum have
+ * res_dtype (VIMSCAN_F32, or io_dtype: VIMSCAN_ERR_DTYPE otherwise), n io_dtype; weight and bias are fp32 [d_inner].
+ */
+typedef struct vimscan_layernorm {
+    const void* x;
+    int64_t ld_x;
+    const void* residual;
+    const float* weight;
+    const float* bias;
+    float eps;              /* > 0, finite */
+    int32_t res_dtype;
+} vimscan_layernorm;
+
+/* Forward pass: writes n and, when set, s to sum, which may be the residual's own memory; any other overlap with
+   an input, or of sum with n, is VIMSCAN_ERR_ALIAS. One kernel, no workspace. */
+int vimscan_layernorm_fwd(const vimscan_layernorm* p, void* sum, void* n, const vimscan_launch* launch);
+
+/* Gradients of vimscan_layernorm_fwd. dsum (res_dtype, dense) and dn (io dtype, dense) are those of its outputs,
+   either may be NULL (zero). dx (io dtype, rows ld_dx apart), dresidual (res_dtype, dense; only with
+   residual: VIMSCAN_ERR_PARAM), dweight and dbias (fp32 [d_inner], sums over the rows in a fixed order; only with weight,
+   bias) may each be NULL (not wanted). dresidual may be dsum's own memory. Recomputes the row's norm from
+   x and residual. Needs a workspace when dweight or dbias is wanted (vimscan_layernorm_plan). */
+typedef struct vimscan_layernorm_grad {
+    const void* dsum;
+    const void* dn;
+    void* dx;
+    int64_t ld_dx;
+    void* dresidual;
+    float* dweight;
+    float* dbias;
+} vimscan_layernorm_grad;
+int vimscan_layernorm_bwd(const vimscan_layernorm* p, const vimscan_layernorm_grad* grad, const vimscan_launch* launch);
+
+/* Plan of a vimscan_layernorm_fwd (backward 0) or vimscan_layernorm_bwd (backward 1) call, as vimscan_norm_plan. */
+int vimscan_layernorm_plan(const vimscan_launch* launch, int backward, vimscan_plan* plan);
+
+/*
  * Linear attention with a decay for each head: one fp32 state of dk x dv per head. For every sequence
  * and head h, over the sequence's tokens t in walking order (memory order, or from the last token to the
  * first with VIMSCAN_FLAG_REVERSE), q and k those of the head's group h / (heads / groups):
