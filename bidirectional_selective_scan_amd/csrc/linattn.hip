@@ -473,7 +473,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     b.s_end = grad->dh0;
     b.o = grad->dv;
     three.a[2] = b;
-    three.count = alike(three.a[0], b) ? 3 : 2;
+    three.count = !decays && alike(three.a[0], b) ? 3 : 2;
     run_passes(io, vec, decays ? kGradientDots : kGradient, three, s);
     if (three.count == 2) run_pass(io, vec, kGradient, b, s);
     if (decays) {

@@ -20,8 +20,8 @@
 //     of its tile i is channel 4 NK grp + 8 (i / 2) + 2 r + i % 2: a lane's rows are the 4 NK consecutive channels that it
 //     reads of a key or reader, in an order in which pairs of tiles are in place as the left operand of r S, and
 //     as columns they are read in pairs.
-// bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed values) are split
-// into two or three bf16 parts, each multiplied: the decayed values, which make the state, into three, as it is fp32 in memory. fp32: fp32 matrix instructions.
+// bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed values) are one to three bf16
+// parts, each multiplied: three where what comes of them is fp32 in memory. fp32: fp32 matrix instructions.
 // Sums of g are in fp64, and their differences taken from a pair of fp32, so that a token of strong decay does not cost its
 // neighbours digits.
 #ifndef VIMSCAN_LINATTN_DEVICE_H
@@ -310,23 +310,20 @@ struct HeadRows {
 };
 
 // ---------------------------------------------------------------------------------------------
-// Products. In bf16 a number in fp32 is the sum of kParts of bf16, each the rounding of what the ones before it leave: 2^-9,
-// 2^-18 or 2^-27 of it are lost.
+// Products. In bf16 a number in fp32 is the sum of one to three bf16 parts, each the rounding of what the ones before it
+// leave: at most 2^-8, 2^-17 or 2^-26 of it are lost.
 
-template <int kParts>
-struct Split8 {
-    U4 w[kParts];
-    // the pair (a, b) at dword i
-    __device__ __forceinline__ void pair(int i, float a, float b) {
+// Four pairs of numbers as an operand: the next part of each, which is taken from them.
+__device__ __forceinline__ U4 next_part(float (&x)[8]) {
+    U4 w;
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) {
-            const uint32_t h = bf16_pair(a, b);
-            w[p][i] = h;
-            a -= bf16_lo(h);
-            b -= bf16_hi(h);
-        }
+    for (int i = 0; i < 4; ++i) {
+        w[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+        x[2 * i] -= bf16_lo(w[i]);
+        x[2 * i + 1] -= bf16_hi(w[i]);
     }
-};
+    return w;
+}
 __device__ __forceinline__ V4f mfma(U4 a, U4 b, V4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V8bf, a), __builtin_bit_cast(V8bf, b), c, 0, 0, 0);
 }
@@ -470,10 +467,10 @@ template <typename IO, int NK, int NV, bool kVec, int kKind>
 __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass(LinPasses passes) {
     constexpr bool kBf16 = sizeof(IoElem<IO>) == 2;
     constexpr int e = sizeof(IoElem<IO>);
-    // parts of the decayed values, and of the state and the scores that are read. The state is fp32 in memory and goes through
-    // the values alone: three. Outputs in bf16 are not told from exact ones with two; the terms of the decays' gradient, which nearly
-    // cancel, need three.
-    constexpr int kValueParts = 3, kReadParts = kKind == kGradientDots ? 3 : 2;
+    // bf16: how many parts. The scores and the state, where they are read, take one where only an output in bf16 comes of
+    // them: their rounding, 2^-8 of a term at most and random, is below the output's own. The terms of the decays' gradient, in fp32,
+    // nearly cancel: three. The decayed values make the state, which is fp32 in memory: three.
+    constexpr int kReadParts = kKind == kGradientDots ? 3 : 1, kValueParts = 3;
     using L = LinTiles<IO, NK, NV, kKind>;
     using TK = Tile<IO, NK>;
     using TV = Tile<IO, NV>;
@@ -605,13 +602,16 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                 if constexpr (kBf16) {
 #pragma unroll
                     for (int s = 0; s < NK / 2; ++s) {
-                        Split8<kReadParts> st;
+                        float x[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) st.pair(i, S[2 * s][v][i], S[2 * s + 1][v][i]);
+                        for (int i = 0; i < 8; ++i) x[i] = S[2 * s + i % 2][v][i / 2];
+                        auto part = [&] {
+                            const U4 w = next_part(x);
 #pragma unroll
-                        for (int p = 0; p < kReadParts; ++p)
+                            for (int j = 0; j < 2; ++j) O[j][v] = mfma(w, row_operand<NK>(rr[j], s), O[j][v]);
+                        };
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) O[j][v] = mfma(st.w[p], row_operand<NK>(rr[j], s), O[j][v]);
+                        for (int p = 0; p < kReadParts; ++p) part();
                     }
                 } else {
 #pragma unroll
@@ -671,13 +671,16 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
             // o += P v
             auto add = [&](int j, const U4 (&vo)[NV], const ColPart<IO, NV>& vw) {
                 if constexpr (kBf16) {
-                    Split8<kReadParts> x;
+                    float x[8];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) x.pair(m, P[m / 2][j][2 * (m & 1)], P[m / 2][j][2 * (m & 1) + 1]);
+                    for (int i = 0; i < 8; ++i) x[i] = P[i / 4][j][i % 4];
+                    auto part = [&] {
+                        const U4 w = next_part(x);
 #pragma unroll
-                    for (int q = 0; q < kReadParts; ++q)
+                        for (int v = 0; v < NV; ++v) O[j][v] = mfma(vo[v], w, O[j][v]);
+                    };
 #pragma unroll
-                        for (int v = 0; v < NV; ++v) O[j][v] = mfma(vo[v], x.w[q], O[j][v]);
+                    for (int p = 0; p < kReadParts; ++p) part();
                 } else {
 #pragma unroll
                     for (int i = 0; i <= j; ++i)
@@ -768,7 +771,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
             const int64_t dst = uniform(reinterpret_cast<int64_t>(a.o) + mem * static_cast<int64_t>(o_ld) + h * a.V * oe);
             const auto ob = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(dst), 0,
                                                               static_cast<uint32_t>((cnt - 1) * o_ld + a.V * oe), kRsrcFlags);
-            [[maybe_unused]] const auto wb = W.chunk(mem, kKind == kGradientDots && a.dots ? cnt : 0);
+            [[maybe_unused]] const auto wb = W.chunk(mem, kKind == kGradientDots ? cnt : 0);
             const uint32_t ox = opaque(o_at);
             [[maybe_unused]] const uint32_t wx = opaque(w_at);
 #pragma unroll
@@ -785,7 +788,6 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                         if constexpr (kBf16) return (c & 1) ? bf16_hi(u[0][c / 2]) : bf16_lo(u[0][c / 2]);
                         else return __uint_as_float(u[c / 4][c % 4]);
                     };
-                    if (a.dots) {
                         U4 w[kW];
 #pragma unroll
                         for (int q = 0; q < kW; ++q)
@@ -797,7 +799,6 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
 #pragma unroll
                         for (int q = 1; q < kLanes; q *= 2) dot += __shfl_xor(dot, q);
                         if (lane % kLanes == 0 && row < cnt) a.dots[(static_cast<int64_t>(block) * a.tokens + mem + row) * a.H + h] = dot;
-                    }
                     U4 v[kW];
 #pragma unroll
                     for (int q = 0; q < kW; ++q) v[q] = *reinterpret_cast<const U4*>(tv + row * TV::kRow + lane % kLanes * 8 * e + q * 16);
@@ -857,13 +858,19 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         if constexpr (kBf16) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                Split8<kValueParts> vd;
+                float x[8];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) vd.pair(q, bf16_lo(vop[j][q]) * out[2 * q], bf16_hi(vop[j][q]) * out[2 * q + 1]);
+                for (int q = 0; q < 4; ++q) {
+                    x[2 * q] = bf16_lo(vop[j][q]) * out[2 * q];
+                    x[2 * q + 1] = bf16_hi(vop[j][q]) * out[2 * q + 1];
+                }
+                auto part = [&] {
+                    const U4 w = next_part(x);
 #pragma unroll
-                for (int p = 0; p < kValueParts; ++p)
+                    for (int i = 0; i < NK; ++i) S[i][j] = mfma(kop[i], w, S[i][j]);
+                };
 #pragma unroll
-                    for (int i = 0; i < NK; ++i) S[i][j] = mfma(kop[i], vd.w[p], S[i][j]);
+                for (int p = 0; p < kValueParts; ++p) part();
             }
         } else {
 #pragma unroll

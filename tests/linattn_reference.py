@@ -7,22 +7,25 @@ factors may be off by:
     ULP (2 |D| + dk + dv + tokens + 64): the decay's exponent, of magnitude up to |D| log2 e, is rounded twice and its
         exponential has an ulp or two; a term passes through at most dk + dv + tokens additions, each half an ulp
         of a partial sum that the magnitudes bound; 64 more for its other roundings (scales, decays of whole chunks)
-    2^-16 in bf16: the fp32 factors of a product are split into two bf16 parts, which leaves 2^-18 of each; a term has at most three
+    2^-16 in bf16, where fp32 factors of a product are the sum of three bf16 parts (2^-26 lost of each; the bound is that of two)
+    2^-8 more in bf16 for outputs that are bf16 themselves and enter no fp32 output (y, dv; dq and dk where no gradient of the
+        decays is formed): a term's score, or the state it is read from, is rounded to one bf16 part, half a step of which is 2^-8
 Outputs in bf16 add their rounding, at most 2^-8 of the value."""
 import numpy as np
 
 from block_reference import TINY, ULP
 
 SPLIT = 2.0 ** -16
+ONE_PART = 2.0 ** -8
 
 
 def rows_of(lo, hi, reverse):
     return np.arange(hi - 1, lo - 1, -1) if reverse else np.arange(lo, hi)
 
 
-def linattn(q, k, v, g, scale, bounds, h0=None, reverse=False, dy=None, dh_last=None, bf16=False):
+def linattn(q, k, v, g, scale, bounds, h0=None, reverse=False, dy=None, dh_last=None, bf16=False, decays=True):
     """q, k (tokens, G, dk), v (tokens, H, dv), g (tokens, H) or (H,), h0 and dh_last (sequences, H, dk, dv), all
-    float64. Returns a dict of name -> (value, bound); gradients where dy or dh_last is given."""
+    float64. Returns a dict of name -> (value, bound); gradients where dy or dh_last is given (decays: the decays' among them)."""
     n, G, dk = q.shape
     H, dv = v.shape[1:]
     rep = H // G
@@ -65,13 +68,16 @@ def linattn(q, k, v, g, scale, bounds, h0=None, reverse=False, dy=None, dh_last=
         whole = np.exp(end)[..., None]
         wholeR = whole * (ULP * (2 * np.abs(end)[..., None] + c) + extra)
         aQ, aK, aV, aS0 = np.abs(Q), np.abs(K), np.abs(V), np.abs(S0)
+        one = ONE_PART if bf16 else 0.0
+        MO, intoO, leftO = MR + one * M, intoR + one * into, leftR + one * left
+        MG, intoG, leftG = (MR, intoR, leftR) if decays else (MO, intoO, leftO)
 
         def T(t):
             return t.transpose(0, 2, 1)
 
         A, aA = Q @ T(K), aQ @ T(aK)
         put("y", rows, (scale * ((A * M) @ V + into * (Q @ S0))).transpose(1, 0, 2),
-            abs(scale) * ((aA * MR) @ aV + intoR * (aQ @ aS0)).transpose(1, 0, 2))
+            abs(scale) * ((aA * MO) @ aV + intoO * (aQ @ aS0)).transpose(1, 0, 2))
         put("h_last", j, whole * S0 + T(K * left) @ V, wholeR * aS0 + T(aK * leftR) @ aV)
         if not grads:
             continue
@@ -80,13 +86,13 @@ def linattn(q, k, v, g, scale, bounds, h0=None, reverse=False, dy=None, dh_last=
         aY, aE = np.abs(Y), np.abs(E)
         P, aP = Y @ T(V), aY @ T(aV)
         dq = (P * M) @ K + into * (Y @ T(S0))
-        dq_e = (aP * MR) @ aK + intoR * (aY @ T(aS0))
+        dq_e = (aP * MG) @ aK + intoG * (aY @ T(aS0))
         put("dq", rows, dq.transpose(1, 0, 2), dq_e.transpose(1, 0, 2))
         dk_ = T(P * M) @ Q + left * (V @ T(E))
-        dk_e = T(aP * MR) @ aQ + leftR * (aV @ T(aE))
+        dk_e = T(aP * MG) @ aQ + leftG * (aV @ T(aE))
         put("dk", rows, dk_.transpose(1, 0, 2), dk_e.transpose(1, 0, 2))
         put("dv", rows, (T(A * M) @ Y + left * (K @ E)).transpose(1, 0, 2),
-            (T(aA * MR) @ aY + leftR * (aK @ aE)).transpose(1, 0, 2))
+            (T(aA * MO) @ aY + leftO * (aK @ aE)).transpose(1, 0, 2))
         put("dh0", j, T(Q * into) @ Y + whole * E, T(aQ * intoR) @ aY + wholeR * aE)
         # dg_t: pairs s < t <= u, the initial state read at u >= t, the final gradient of s < t, both
         pairs, pairs_e = A * P * M, aA * aP * MR

@@ -53,13 +53,16 @@ class Problem:
         return PreparedLinAttn(self.q, self.k, self.v, self.g, self.scale, self.h0, self.seg_len, self.offsets,
                                self.reverse, **kw)
 
-    def want(self, grads):
+    def want_without_decays(self):
+        return self.want(True, False)
+
+    def want(self, grads, decays=True):
         g = f64(self.g)
         g = g if g.ndim == 1 else g.reshape(self.n, self.H)
         flat = [f64(t).reshape(self.n, *t.shape[2:]) for t in (self.q, self.k, self.v, self.dy)]
         return ref.linattn(flat[0], flat[1], flat[2], g, float(np.float32(self.dk ** -0.5 if self.scale is None else self.scale)),
                            self.bounds, None if self.h0 is None else f64(self.h0), self.reverse, flat[3] if grads else None,
-                           f64(self.dh_last) if grads and self.dh_last is not None else None, self.bf16)
+                           f64(self.dh_last) if grads and self.dh_last is not None else None, self.bf16, decays)
 
     def check(self, what=""):
         want = self.want(True)
@@ -80,6 +83,28 @@ class Problem:
 def test_lengths(io, dk, dv):
     for length in (1, 2, 31, 32, 33, 64, 70, 130):
         Problem((2, length), 2, 2, dk, dv, io, seed=length).check(f"length {length}")
+
+
+def test_bf16_outputs_are_near_their_own_rounding():
+    """In the 2-norm: a rounding of values spread over a binade has a relative error of at most 2^-8 / sqrt(3); an output
+    in bf16 has its own and, term by term at random, that of its scores or of the state."""
+    p = Problem((4, 300), 4, 4, 64, 64, "bf16", seed=30)
+    want = p.want(True)
+    call = p.forward()
+    call()
+    for decays in (True, False):
+        g = PreparedLinAttnGrad(call, p.dy, p.dh_last, decays=decays)
+        g()
+        for name, t in (("y", call.y), ("dq", g.dq), ("dk", g.dk), ("dv", g.dv)):
+            ref_v = want[name][0]
+            err = np.linalg.norm(f64(t).reshape(ref_v.shape) - ref_v) / np.linalg.norm(ref_v)
+            assert err <= 2.0 ** -8 / 3 ** 0.5 * 2 ** 0.5, (name, err)
+        for name, t in (("h_last", call.h_last), ("dh0", g.dh0)) + ((("dg", g.dlog_decay),) if decays else ()):
+            ref_v = want[name][0]
+            err = np.linalg.norm(f64(t).reshape(ref_v.shape) - ref_v) / np.linalg.norm(ref_v)
+            assert err <= 1e-5, (name, err)
+        block_reference.check(g.dq, p.want_without_decays()["dq"] if not decays else want["dq"], True, "dq")
+        block_reference.check(g.dk, p.want_without_decays()["dk"] if not decays else want["dk"], True, "dk")
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
