@@ -259,13 +259,13 @@ LinArgs common_args(const vimscan_linattn* p, const vimscan_launch* l, const Lin
 }
 
 // The roles of a pass: reader, key, value.
-void set_roles(LinArgs* a, const LinRows& r, const LinRows& k, const LinRows& v, int64_t K, int64_t V) {
+void set_roles(int bytes, LinArgs* a, const LinRows& r, const LinRows& k, const LinRows& v, int64_t K, int64_t V) {
     a->r = r;
     a->k = k;
     a->v = v;
     a->K = static_cast<int32_t>(K);
     a->V = static_cast<int32_t>(V);
-    a->blocks = static_cast<int32_t>(vimscan_host::lin_blocks(V));
+    a->blocks = static_cast<int32_t>(vimscan_host::lin_blocks(bytes, K, V));
     a->waves = a->slots * a->H * a->blocks;
 }
 
@@ -290,9 +290,9 @@ void run_pass(int io, bool vec, LinKind kind, const LinArgs& a, hipStream_t s) {
     run_passes(io, vec, kind, p, s);
 }
 // Whether two passes can be one launch: the same instance, equally many waves.
-bool alike(const LinArgs& a, const LinArgs& b) {
+bool alike(int bytes, const LinArgs& a, const LinArgs& b) {
     return vimscan_host::lin_contract_tiles(a.K) == vimscan_host::lin_contract_tiles(b.K) &&
-           vimscan_host::lin_output_tiles(a.V) == vimscan_host::lin_output_tiles(b.V) && a.waves == b.waves;
+           vimscan_host::lin_output_tiles(bytes, a.K, a.V) == vimscan_host::lin_output_tiles(bytes, b.K, b.V) && a.waves == b.waves;
 }
 
 unsigned some_blocks(int64_t elements) {
@@ -337,14 +337,14 @@ int vimscan_linattn_fwd(const vimscan_linattn* p, int64_t seg_len, void* y, floa
     rc = vimscan_host::check_linattn_call(p, y, h_last, nullptr, launch, pl);
     if (rc != VIMSCAN_OK || pl.waves == 0) return rc;
     if (pl.tokens == 0 && !h_last) return VIMSCAN_OK;
-    const int io = launch->io_dtype;
+    const int io = launch->io_dtype, bytes = io == VIMSCAN_F32 ? 4 : 2;
     const bool vec = use_vectors(p, nullptr, y, pl, io);
     const int32_t rep = static_cast<int32_t>(pl.H / pl.G);
     const LinRows q = {p->q, p->ld_q, p->hs_q, rep}, k = {p->k, p->ld_k, p->hs_k, rep}, v = {p->v, p->ld_v, p->hs_v, 1};
     char* ws = static_cast<char*>(launch->workspace);
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     LinArgs a = common_args(p, launch, pl);
-    set_roles(&a, q, k, v, pl.dk, pl.dv);
+    set_roles(bytes, &a, q, k, v, pl.dk, pl.dv);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
     a.s0 = p->h0;
     a.s0_row = pl.dv;
@@ -378,13 +378,14 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     if (rc != VIMSCAN_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     const bool by_head = p->ld_decay == 0;
+    const int bytes = launch->io_dtype == VIMSCAN_F32 ? 4 : 2;
     LinArgs a = common_args(p, launch, pl);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
     if (pl.tokens == 0) {
         // gradients of empty sequences' states, and of decays that no token has
         if (pl.waves > 0 && grad->dh0) {
             const LinRows none = {nullptr, 0, 0, 1};
-            set_roles(&a, none, none, none, pl.dk, pl.dv);
+            set_roles(bytes, &a, none, none, none, pl.dk, pl.dv);
             a.back = 1;
             a.s0 = grad->dh_last;
             a.s0_row = pl.dv;
@@ -409,13 +410,13 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     a.s0_col = 1;
     if (pl.split) {
         LinArgs b = a;
-        set_roles(&b, k, k, v, pl.dk, pl.dv);
+        set_roles(bytes, &b, k, k, v, pl.dk, pl.dv);
         b.s_end = at(pl.off_s);
         b.tot = at(pl.off_tot);
         run_pass(io, vec, kLocal, b, s);
         run_fold(b, at(pl.off_s), at(pl.off_tot), p->h0, false, s);
         b = a;
-        set_roles(&b, q, q, dy, pl.dk, pl.dv);
+        set_roles(bytes, &b, q, q, dy, pl.dk, pl.dv);
         b.back = 1;
         b.key_scale = p->scale;
         b.s_end = at(pl.off_e);
@@ -428,7 +429,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     const int32_t by_slot = pl.split;
     const bool shared = rep > 1;
     LinArgs b = a;   // dq: forward, the state transposed
-    set_roles(&b, dy, v, k, pl.dv, pl.dk);
+    set_roles(bytes, &b, dy, v, k, pl.dv, pl.dk);
     b.s0 = s0;
     b.s0_row = 1;
     b.s0_col = pl.dv;
@@ -450,7 +451,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     std::memset(&three, 0, sizeof(three));
     three.a[0] = b;
     b = a;           // dk: from the end, the gradient of the state transposed
-    set_roles(&b, v, dy, q, pl.dv, pl.dk);
+    set_roles(bytes, &b, v, dy, q, pl.dv, pl.dk);
     b.back = 1;
     b.key_scale = p->scale;
     b.s0 = e0;
@@ -465,7 +466,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     }
     three.a[1] = b;
     b = a;           // dv, and the gradient of the state before the sequence
-    set_roles(&b, k, q, dy, pl.dk, pl.dv);
+    set_roles(bytes, &b, k, q, dy, pl.dk, pl.dv);
     b.back = 1;
     b.key_scale = p->scale;
     b.s0 = e0;
@@ -473,7 +474,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     b.s_end = grad->dh0;
     b.o = grad->dv;
     three.a[2] = b;
-    three.count = !decays && alike(three.a[0], b) ? 3 : 2;
+    three.count = !decays && alike(bytes, three.a[0], b) ? 3 : 2;
     run_passes(io, vec, decays ? kGradientDots : kGradient, three, s);
     if (three.count == 2) run_pass(io, vec, kGradient, b, s);
     if (decays) {

@@ -571,20 +571,26 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         int64_t mem;     // the chunk's lowest token, and how many it has
         int cnt;
         place(m, &mem, &cnt);
-        // sums of the log decays over the chunk
-        double run = half_wave_sums(log2_decay(gv));
-        const double total = lane_value(run, 31);
-        if (kKind == kLocal) all += total;
-        run += scaled;
+        // sums of the log decays over the chunk: before its rows are waited for or, with 128 contracted channels, during the
+        // products with the state (64 x 1025 packed x 24 heads of 128 x 64: 231 us, 272 before; 8 x 1025 x 12 of 64 x 64: 49, 47 before)
+        constexpr bool kSumLate = NK == 8 && kKind != kLocal;
+        const float g = gv;
+        double total = 0.0;
+        auto sum_up = [&] {
+            const double run = half_wave_sums(log2_decay(g));
+            total = lane_value(run, 31);
+            if (kKind == kLocal) all += total;
+            if (lane < kChunk) sums[lane] = as_pair(run + scaled);
+        };
         wave_sync();
+        if constexpr (!kSumLate) sum_up();
         if constexpr (kKind != kLocal) TK::put(tr, lane, sr);
         TK::put(tk, lane, sk);
         TV::put(tv, lane, sv);
-        if (lane < kChunk) sums[lane] = as_pair(run);
-        const double after = scaled + total;
         wave_sync();
         load(m + 1);
         __builtin_amdgcn_sched_barrier(0);   // (else the compiler moves loads down behind the products)
+        if constexpr (kSumLate) sum_up();
 
         V4f O[2][NV];
         [[maybe_unused]] float P[2][2][4];   // [key tile][reader tile], rows of keys
@@ -622,6 +628,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                             for (int j = 0; j < 2; ++j) O[j][v] = mfma(S[i][v][r], rr[j].w[state_channel(i, r)], O[j][v]);
                 }
             }
+            if constexpr (kSumLate) wave_sync();
             float2 gt[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -835,6 +842,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         // it need not be scaled in every chunk: the values are decayed to that point instead, which for more than 2^-16
         // costs no digits and stays in range.
         float2 end = make_float2(0.0f, 0.0f);
+        const double after = scaled + total;
         scaled = after;
         if (!(after > -16.0 && after < 16.0)) {
             end = as_pair(after);

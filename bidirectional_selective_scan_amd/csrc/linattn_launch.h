@@ -12,8 +12,12 @@ void launch_lin_instance(const LinPasses& p, hipStream_t s) {
 }
 template <typename IO, int NK, bool kVec, int kKind>
 void launch_lin_outputs(const LinPasses& p, hipStream_t s) {
-    if (vimscan_host::lin_output_tiles(p.a[0].V) == 2) launch_lin_instance<IO, NK, 2, kVec, kKind>(p, s);
-    else launch_lin_instance<IO, NK, 4, kVec, kKind>(p, s);
+    // (the instances that lin_output_tiles can ask for)
+    constexpr int e = sizeof(IoElem<IO>);
+    if constexpr (e == 2 && NK <= 4) {
+        if (vimscan_host::lin_output_tiles(e, p.a[0].K, p.a[0].V) == 4) return launch_lin_instance<IO, NK, 4, kVec, kKind>(p, s);
+    }
+    launch_lin_instance<IO, NK, 2, kVec, kKind>(p, s);
 }
 template <typename IO, bool kVec, int kKind>
 void launch_lin_dims(const LinPasses& p, hipStream_t s) {

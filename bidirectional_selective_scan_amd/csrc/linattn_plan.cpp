@@ -20,13 +20,17 @@ int check_dims(const vimscan_launch* l, int64_t heads, int64_t groups) {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tokens per segment, or 0: sequences stay whole. As many segments as fill the chip's places for waves (1024 SIMDs) once and do not
-// start a second round. The segments' own states and their fold cost about as much as 0.6 of the pass and three chunks: where that is
-// not less than the chunks saved, sequences stay whole.
-int64_t segment(int64_t length, int64_t waves, int64_t places) {
+// Tokens per segment, or 0: sequences stay whole. A wave for each SIMD of the chip (1024): more, shorter segments cost more
+// in their states than they gain (bf16, heads of 64 x 64, us, chunks of 32 tokens per segment: 8 x 1025 x 12, 2: 51, 5: 48, 9: 60, whole 96;
+// 1 x 4096 x 24, 2: 51, 5: 47, 9: 58, whole 337; 16 x 1025 x 12, 2: 91, 5: 69, 9: 71, whole 99; 1 x 65537 x 24, 17: 320, 33: 301, 66: 303).
+// Two where packed sequences differ in length (16 x up to 2000 x 24, 9: 121, 17: 143, 25: 162, whole 176; but 64 x up to 1025 x 12, whose
+// heads alone are 768 waves, in training 9: 510, whole 468), and twice as many in fp32, whose chunks take longer (packed 32 x up to 513 x 6
+// in training 3: 223, 9: 302, whole 288). The segments' own states and their fold cost about as much as 0.6 of the pass and three chunks:
+// where that is not less than the chunks saved, sequences stay whole.
+int64_t segment(int64_t length, int64_t waves, bool packed, int bytes) {
     constexpr int64_t kLeast = 2, kMost = 128;   // chunks
-    const int64_t chunks = up(length, kLinChunk), parts = places / waves;
-    if (parts < 2) return chunks > kMost ? kMost * kLinChunk : 0;
+    const int64_t chunks = up(length, kLinChunk), parts = 1024 * (packed ? 2 : 1) * (bytes == 4 ? 2 : 1) / waves;
+    if (parts < (packed ? 3 : 2)) return chunks > kMost ? kMost * kLinChunk : 0;
     int64_t seg = up(chunks, parts);
     if (seg < kLeast) seg = kLeast;
     if (seg > kMost) seg = kMost;
@@ -80,11 +84,11 @@ int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, i
     if (p->nseq == 0) return VIMSCAN_OK;
     // (packed sequences: the longest is taken to be twice the mean)
     const int64_t twice = packed ? 2 * up(p->tokens, p->nseq) : 0, length = !packed ? p->Lp : twice < p->tokens ? twice : p->tokens;
-    const int64_t blocks = lin_blocks(p->dv), qblocks = lin_blocks(p->dk);
+    const int bytes = static_cast<int>(io_bytes(l));
+    const int64_t blocks = lin_blocks(bytes, p->dk, p->dv), qblocks = lin_blocks(bytes, p->dv, p->dk);
     const int64_t most_waves = kMaxLinWaves / ((blocks > qblocks ? blocks : qblocks) * heads);
     if (p->nseq > most_waves) return VIMSCAN_ERR_SHAPE;
-    const int per_simd = lin_waves_per_simd(static_cast<int>(io_bytes(l)), lin_contract_tiles(p->dk), lin_output_tiles(p->dv));
-    p->seg = segment(length, p->nseq * heads * blocks, 1024 * per_simd);
+    p->seg = segment(length, p->nseq * heads * blocks, packed, bytes);
     p->split = p->seg > 0;
     p->segs = p->split && !packed ? up(p->Lp, p->seg) : 1;
     p->slots = !p->split ? p->nseq : packed ? p->tokens / p->seg + p->nseq : p->nseq * p->segs;
