@@ -92,11 +92,28 @@ template <> struct Raw<float, 4> {
 };
 
 // The same from and to any element address: the hardware takes a wide access at any alignment (the
-// unaligned access mode of the HSA target), which memcpy tells the compiler.
-template <typename IO, int V>
-__device__ __forceinline__ void load_any(Raw<IO, V>& r, const IoElem<IO>* p) { __builtin_memcpy(&r, p, sizeof(r)); }
-template <typename IO, int V>
-__device__ __forceinline__ void store_any(const Raw<IO, V>& r, IoElem<IO>* p) { __builtin_memcpy(p, &r, sizeof(r)); }
+// unaligned access mode of the HSA target), which memcpy tells the compiler. kOnce: past the caches.
+template <bool kOnce = false, typename IO, int V>
+__device__ __forceinline__ void load_any(Raw<IO, V>& r, const IoElem<IO>* p) {
+    if constexpr (kOnce && sizeof(r) % 4 == 0) {
+        using W = uint32_t __attribute__((ext_vector_type(sizeof(r) / 4), aligned(sizeof(IoElem<IO>))));
+        const W w = __builtin_nontemporal_load(reinterpret_cast<const W*>(p));
+        __builtin_memcpy(&r, &w, sizeof(r));
+    } else {
+        __builtin_memcpy(&r, p, sizeof(r));
+    }
+}
+template <bool kOnce = false, typename IO, int V>
+__device__ __forceinline__ void store_any(const Raw<IO, V>& r, IoElem<IO>* p) {
+    if constexpr (kOnce && sizeof(r) % 4 == 0) {
+        using W = uint32_t __attribute__((ext_vector_type(sizeof(r) / 4), aligned(sizeof(IoElem<IO>))));
+        W w;
+        __builtin_memcpy(&w, &r, sizeof(r));
+        __builtin_nontemporal_store(w, reinterpret_cast<W*>(p));
+    } else {
+        __builtin_memcpy(p, &r, sizeof(r));
+    }
+}
 // The first n < V elements.
 template <typename IO, int V>
 __device__ __forceinline__ void load_some(Raw<IO, V>& r, const IoElem<IO>* p, int n) {

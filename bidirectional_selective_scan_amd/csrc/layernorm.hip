@@ -27,7 +27,7 @@ struct LayerNormArgs {
     const float* weight;
     const float* bias;
     float eps, inv_d;
-    int32_t D;
+    int32_t D, once;
     int64_t rows;
     void* sum;
     void* n;
@@ -40,6 +40,16 @@ struct LayerNormArgs {
     float* dw[2];   // of weight and bias
     float* part;    // [workgroup][2][D] partial weight gradients, NULL when none is wanted
 };
+
+// Outputs of calls that move more than kOnceBytes are written past the caches: there each line throws out another (768 channels bf16,
+// us, kept and not: 25216 rows 43.3 and 40.2, 6272 rows 10.5 and 10.3; forward and backward 108.3 and 98.6, 33.4 and 28.8).
+// Smaller ones are kept for whoever reads them next.
+constexpr int64_t kOnceBytes = int64_t(32) << 20;
+template <typename T, typename S>
+__device__ __forceinline__ void st_out(bool once, void* base, int64_t at, int D, const float (&v)[S::NV][S::V]) {
+    if (once) st_row<T, S, true>(base, at, D, v);
+    else st_row<T, S>(base, at, D, v);
+}
 
 // The row minus its mean, and 1 / sqrt of its variance and eps: the mean first, then the squares about it (in
 // registers, a second look costs no memory; the difference of two large sums would cost digits where the mean is large).
@@ -89,13 +99,13 @@ __global__ __launch_bounds__(S::kThreads) void k_ln_fwd(LayerNormArgs a) {
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) s[k][v] = x[k].get(v) + r[k].get(v);
-        if (a.sum) st_row<RES, S>(a.sum, row * a.D, a.D, s);
+        if (a.sum) st_out<RES, S>(a.once, a.sum, row * a.D, a.D, s);
         const float rho = center<S>(a, s, lds, slot, wave);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) s[k][v] = fmaf(s[k][v] * rho, w[k][v], a.bias ? b[k][v] : 0.0f);
-        st_row<IO, S>(a.n, row * a.D, a.D, s);
+        st_out<IO, S>(a.once, a.n, row * a.D, a.D, s);
     }
 }
 
@@ -168,8 +178,8 @@ __global__ __launch_bounds__(S::kThreads) void k_ln_bwd(LayerNormArgs a) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 s[k][v] = fmaf(rho, fmaf(-s[k][v], t, fmaf(dn[k].get(v), w[k][v], -u)), ds[k].get(v));
-        if (a.dx) st_row<IO, S>(a.dx, row * a.ld_dx, a.D, s);
-        if (a.dres) st_row<RES, S>(a.dres, row * a.D, a.D, s);
+        if (a.dx) st_out<IO, S>(a.once, a.dx, row * a.ld_dx, a.D, s);
+        if (a.dres) st_out<RES, S>(a.once, a.dres, row * a.D, a.D, s);
     }
     if (!a.part) return;
     float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
@@ -321,6 +331,8 @@ int vimscan_layernorm_fwd(const vimscan_layernorm* p, void* sum, void* n, const 
     LayerNormArgs a = common_args(p, pl);
     a.sum = sum;
     a.n = n;
+    const int64_t e = launch->io_dtype == VIMSCAN_F32 ? 4 : 2, re = p->res_dtype == VIMSCAN_F32 ? 4 : 2, size = pl.rows * pl.D;
+    a.once = size * (2 * e + (p->residual ? re : 0) + (sum ? re : 0)) > kOnceBytes;
     hipStream_t s = static_cast<hipStream_t>(launch->stream);
     if (!record(launch, 0)) return VIMSCAN_ERR_HIP;
     launch_typed(a, pl, launch->io_dtype, p->res_dtype == VIMSCAN_F32, false, s);
@@ -341,6 +353,8 @@ int vimscan_layernorm_bwd(const vimscan_layernorm* p, const vimscan_layernorm_gr
     a.dx = grad->dx;
     a.ld_dx = grad->ld_dx;
     a.dres = grad->dresidual;
+    const int64_t e = launch->io_dtype == VIMSCAN_F32 ? 4 : 2, re = p->res_dtype == VIMSCAN_F32 ? 4 : 2, size = pl.rows * pl.D;
+    a.once = size * (3 * e + (p->residual ? re : 0) + (grad->dsum ? re : 0) + (grad->dresidual ? re : 0)) > kOnceBytes;
     a.dw[0] = grad->dweight;
     a.dw[1] = grad->dbias;
     const bool weights = a.dw[0] || a.dw[1];

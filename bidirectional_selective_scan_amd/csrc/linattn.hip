@@ -145,7 +145,8 @@ __global__ __launch_bounds__(256) void k_lin_group_sum(const float* part, int64_
     }
 }
 
-// One token: S' = e^g S + k^T v, y = scale q S'. The states' traffic bounds it (8 bytes for 5 operations). A workgroup takes a
+// One token: S' = e^g S + k^T v, y = scale q S'. The states' traffic bounds it (8 bytes for 5 operations): 256 x 24 heads of 64 x 64
+// (204 MB) 41.7 us, 4.9 TB/s, with states read and written past the caches, 45.4 through them. A workgroup takes a
 // row's head and up to 4 CL of its value channels: CL lanes of V channels to a state row, the rows spread over the rest.
 struct LinStepArgs {
     LinRows q, k, v;
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(256) void k_lin_step(LinStepArgs a) {
 #pragma unroll 4
         for (int r = rg; r < a.dk; r += kRows) {
             Raw<float, V> s;
-            s.load(src + static_cast<int64_t>(r) * a.dv);
+            load_any<true>(s, src + static_cast<int64_t>(r) * a.dv);
             Raw<IO, 1> qr, kr;
             qr.load(q + r);
             kr.load(k + r);
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(256) void k_lin_step(LinStepArgs a) {
                 sum[v] = fmaf(qr.get(0), n[v], sum[v]);
             }
             s.set(n);
-            s.store(dst + static_cast<int64_t>(r) * a.dv);
+            store_any<true>(s, dst + static_cast<int64_t>(r) * a.dv);
         }
     }
     // over the wave's rows, then over the waves in their order

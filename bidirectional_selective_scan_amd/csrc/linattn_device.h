@@ -246,7 +246,8 @@ __device__ __forceinline__ uint32_t piece_at(int c, int D) { return c < D ? stat
 // Cache policy of the passes' loads. kOnce: the lines are not kept. Calls whose inputs do not fit the memory-side cache take it:
 // lines that are kept throw out others, written ones among them, for nothing (k and v of 1 x 65537 x 24 x 64 x 64, 403 MB,
 // in the segments' states: 123 us kept, 90 us not); those that fit are read again by the passes that follow (128 x 197 x 12 x 64 x 64,
-// backward 147 us kept, 161 us not).
+// backward 147 us kept, 161 us not). Gradients in bf16 are written so always (forward and backward 195 us, 201 kept), y never
+// (64 packed x up to 1025 x 24 x 128 x 64: 236 us so, 231 kept).
 constexpr int kKeep = 0, kOnce = 2;
 template <int kPolicy>
 __device__ __forceinline__ U4 load_b128(__amdgpu_buffer_rsrc_t rsrc, uint32_t at) {
@@ -830,7 +831,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                     }
                 } else if constexpr (kVec) {
                     const U4 w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
-                    __builtin_amdgcn_raw_buffer_store_b128(w, ob, at, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(w, ob, at, 0, kKind == kForward ? kKeep : kOnce);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)

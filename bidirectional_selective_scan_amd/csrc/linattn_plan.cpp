@@ -15,6 +15,8 @@ int check_dims(const vimscan_launch* l, int64_t heads, int64_t groups) {
     if (heads < 1 || groups < 1 || heads > l->d_inner || heads % groups != 0 || l->d_inner % heads != 0)
         return VIMSCAN_ERR_SHAPE;
     if (l->d_state < 1 || l->d_state > kLinMaxDim || l->d_inner / heads > kLinMaxDim) return VIMSCAN_ERR_SHAPE;
+    // (rows of the gradients by head lie within a buffer resource, as those of d_inner channels)
+    if (heads * l->d_state >= (int64_t(1) << 22)) return VIMSCAN_ERR_SHAPE;
     return VIMSCAN_OK;
 }
 

@@ -110,7 +110,8 @@ __device__ __forceinline__ void settle(int D, Raw<T, S::V> (&o)[S::NV]) {
         }
     }
 }
-template <typename T, typename S>
+// kOnce: past the caches (the lines are not kept).
+template <typename T, typename S, bool kOnce = false>
 __device__ __forceinline__ void st_row(void* base, int64_t at, int D, const float (&v)[S::NV][S::V]) {
     constexpr int V = S::V;
     IoElem<T>* p = static_cast<IoElem<T>*>(base) + at;
@@ -120,9 +121,9 @@ __device__ __forceinline__ void st_row(void* base, int64_t at, int D, const floa
         Raw<T, V> o;
         o.set(v[k]);
         if constexpr (S::kWhole) {
-            if (c < D) store_any(o, p + c);
+            if (c < D) store_any<kOnce>(o, p + c);
         } else {
-            if (c + V <= D) store_any(o, p + c);
+            if (c + V <= D) store_any<kOnce>(o, p + c);
             else if (c < D) store_some(o, p + c, D - c);
         }
     }

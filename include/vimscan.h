@@ -509,8 +509,8 @@ int vimscan_layernorm_plan(const vimscan_launch* launch, int backward, vimscan_p
  * before it in walking order, no other head (but those that share the token's q and k) and no other
  * sequence.
  *
- * launch->d_state is dk and launch->d_inner heads * dv, dk and dv 1 to 128 (VIMSCAN_ERR_SHAPE). groups
- * divides heads. Token rows of q, k and v are ld_* elements apart (at least dk, dv; below 2^22), the heads
+ * launch->d_state is dk and launch->d_inner heads * dv, dk and dv 1 to 128, heads * dk < 2^22 (VIMSCAN_ERR_SHAPE).
+ * groups divides heads. Token rows of q, k and v are ld_* elements apart (at least dk, dv; below 2^22), the heads
  * or groups of a token hs_* elements (0 <= hs_* < 2^38): VIMSCAN_ERR_PARAM. So they may be slices of one projection's output, or
  * one sequence in [heads][tokens][d] order. ld_decay is 0 or at least heads, below 2^22. h0, h_last, y and
  * the gradients are dense. flags: VIMSCAN_FLAG_REVERSE only; chunk_len must be 0. tokens = batch * seqlen < 2^31.
