@@ -524,7 +524,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
     // are behind its rows; walking down the first chunk lacks them, before the first token. Either way they are at rows from
     // cnt on, outside the resource: no keys, no values, no decay.
     const int64_t n = sg.n;
-    const int chunks = static_cast<int>((n + kChunk - 1) / kChunk), lack = chunks * kChunk - static_cast<int>(n);
+    const int chunks = static_cast<int>((n + kChunk - 1) / kChunk), lack = static_cast<int>(static_cast<int64_t>(chunks) * kChunk - n);
     auto place = [&](int m, int64_t* first, int* c) {
         *first = desc ? sg.first + n + lack - static_cast<int64_t>(m + 1) * kChunk : sg.first + static_cast<int64_t>(m) * kChunk;
         *c = m >= chunks ? 0 : m == (desc ? 0 : chunks - 1) ? kChunk - lack : kChunk;

@@ -76,9 +76,9 @@ int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, i
     p->packed = packed;
     p->tokens = l->batch * l->seqlen;
     if (packed && nseq == 0 && p->tokens > 0) return VIMSCAN_ERR_SHAPE;
-    p->Lp = packed ? 0 : (seg_len > 0 ? seg_len : l->seqlen);
-    // uniform sequences of no tokens: one per batch row
-    p->nseq = packed ? nseq : (p->tokens > 0 ? p->tokens / p->Lp : l->batch);
+    p->Lp = packed || p->tokens == 0 ? 0 : (seg_len > 0 ? seg_len : l->seqlen);
+    // uniform sequences of no tokens: one per batch row (cut at seg_len: none)
+    p->nseq = packed ? nseq : p->tokens > 0 ? p->tokens / p->Lp : seg_len > 0 ? 0 : l->batch;
     p->H = heads;
     p->G = groups;
     p->dk = l->d_state;
@@ -88,7 +88,8 @@ int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, i
     const int64_t twice = packed ? 2 * up(p->tokens, p->nseq) : 0, length = !packed ? p->Lp : twice < p->tokens ? twice : p->tokens;
     const int bytes = static_cast<int>(io_bytes(l));
     const int64_t blocks = lin_blocks(bytes, p->dk, p->dv), qblocks = lin_blocks(bytes, p->dv, p->dk);
-    const int64_t most_waves = kMaxLinWaves / ((blocks > qblocks ? blocks : qblocks) * heads);
+    // (up to three passes of the backward pass are one launch)
+    const int64_t most_waves = kMaxLinWaves / ((blocks > qblocks ? blocks : qblocks) * heads * (backward ? 3 : 1));
     if (p->nseq > most_waves) return VIMSCAN_ERR_SHAPE;
     p->seg = segment(length, p->nseq * heads * blocks, packed, bytes);
     p->split = p->seg > 0;
@@ -216,11 +217,11 @@ int vimscan_linattn_plan(const vimscan_launch* launch, int64_t seg_len, int64_t 
     plan->chunks = p.nseq == 0 ? 0 : p.split && packed ? p.slots : p.segs;
     plan->workgroups = p.waves;
     // forward: the pass, where it is split after the segments' states and their fold; backward: the same
-    // states and those of the gradients, three passes, the decays' gradient (and its sum over the
-    // tokens), the sums over shared heads
+    // states and those of the gradients, the passes of dq and dk in one launch and that of dv, the decays'
+    // gradient (and its sum over the tokens), the sums over shared heads
     if (p.waves > 0) {
         if (!backward) plan->kernels = p.split ? 3 : 1;
-        else if (p.tokens > 0) plan->kernels = (p.split ? 4 : 0) + 3 + 2 + (p.G != p.H ? 2 : 0);
+        else if (p.tokens > 0) plan->kernels = (p.split ? 4 : 0) + 2 + 2 + (p.G != p.H ? 2 : 0);
         else plan->kernels = 2;
     }
     plan->workspace_bytes = p.ws;

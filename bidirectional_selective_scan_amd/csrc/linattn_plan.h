@@ -43,8 +43,8 @@ struct LinPlan {
     size_t off_s, off_e, off_tot, off_rq, off_rk, off_cd, off_hs, off_pq, off_pk, ws;
 };
 
-// Whether a segment's index space, base(q) = offsets[q] / seg + q, gives every sequence slots of its own: sequence
-// q has floor(offsets[q+1] / seg) - floor(offsets[q] / seg) + 1 >= ceil(length / seg) of them.
+// Packed sequence q takes the slots from offsets[q] / seg + q on: up to the next sequence's first these are
+// floor(offsets[q + 1] / seg) - floor(offsets[q] / seg) + 1 >= ceil(length / seg), one for each of its segments.
 int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, int64_t groups, bool packed, int64_t nseq,
                       bool backward, LinPlan* p);
 int check_linattn_call(const vimscan_linattn* a, const void* y, const float* h_last, const vimscan_linattn_grad* grad,
