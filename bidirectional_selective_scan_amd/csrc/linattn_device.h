@@ -9,7 +9,7 @@
 //     o_t = e^{G_t} r_t S_in + sum_{s <= t} e^{G_t - G_s} (r_t . k_s) v_s,   S_out = e^{G_end} S_in + sum_s e^{G_end - G_s} k_s^T v_s
 // so all but the decays is matrix products.
 //
-// What bounds it: memory, up to heads of 64 x 64 (bf16: 512 bytes and 55 matrix instructions of 16 cycles a token and head). So a
+// What bounds it: memory, up to heads of 64 x 64 (bf16: 512 bytes a token and head). So a
 // wave does all of a head (or 64 output channels of it) alone: it reads every number once, the state never leaves
 // its registers, and nothing waits for another wave. The operands are laid out so that what one product leaves
 // in the accumulators is the next one's operand as it stands (lane = 16 grp + col):
@@ -20,7 +20,7 @@
 //     of its tile i is channel 4 NK grp + 8 (i / 2) + 2 r + i % 2: a lane's rows are the 4 NK consecutive channels that it
 //     reads of a key or reader, in an order in which pairs of tiles are in place as the left operand of r S, and
 //     as columns they are read in pairs.
-// bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed values) are one to three bf16
+// bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed values) are two or three bf16
 // parts, each multiplied: three where what comes of them is fp32 in memory. fp32: fp32 matrix instructions.
 // Sums of g are in fp64, and their differences taken from a pair of fp32, so that a token of strong decay does not cost its
 // neighbours digits.
@@ -468,10 +468,11 @@ template <typename IO, int NK, int NV, bool kVec, int kKind>
 __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass(LinPasses passes) {
     constexpr bool kBf16 = sizeof(IoElem<IO>) == 2;
     constexpr int e = sizeof(IoElem<IO>);
-    // bf16: how many parts. The scores and the state, where they are read, take one where only an output in bf16 comes of
-    // them: their rounding, 2^-8 of a term at most and random, is below the output's own. The terms of the decays' gradient, in fp32,
-    // nearly cancel: three. The decayed values make the state, which is fp32 in memory: three.
-    constexpr int kReadParts = kKind == kGradientDots ? 3 : 1, kValueParts = 3;
+    // bf16: how many parts. The scores and the state, where they are read, take two (2^-17 of a term) where only an output in
+    // bf16 comes of them: with one their rounding is as large as the output's own (its error 1.4 times the least) for 4% (8 x 1025 x 12
+    // heads of 64 x 64 49 us, 47 with one) to 11% (64 packed x up to 1025 x 24 of 128 x 64 257 us, 232). The terms of the decays'
+    // gradient, in fp32, nearly cancel: three. The decayed values make the state, which is fp32 in memory: three.
+    constexpr int kReadParts = kKind == kGradientDots ? 3 : 2, kValueParts = 3;
     using L = LinTiles<IO, NK, NV, kKind>;
     using TK = Tile<IO, NK>;
     using TV = Tile<IO, NV>;
