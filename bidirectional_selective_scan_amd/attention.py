@@ -106,7 +106,7 @@ class LinAttnInputs:
             _check_tensor(h0, "h0", dev, torch.float32, self.state_shape)
         self.decay_stride = _decay_stride(log_decay, (Bsz, L), H, dev)
         self.q, self.k, self.v, self.log_decay, self.h0, self.offsets = q, k, v, log_decay, h0, offsets
-        self.scale = dk ** -0.5 if scale is None else float(scale)
+        self.scale = max(dk, 1) ** -0.5 if scale is None else float(scale)
         self.seg_len, self.reverse = int(seg_len), bool(reverse)
         self.dev, self.dtype = dev, q.dtype
         (ld_q, hs_q), (ld_k, hs_k), (ld_v, hs_v) = (head_strides(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v")))
@@ -228,7 +228,7 @@ class PreparedLinAttnStep(_Call):
         launch = _b.make_launch(Bsz, 1, H * dv, dk, io, 0, stream=_stream_of(dev, stream))
         (ld_q, hs_q), (ld_k, hs_k), (ld_v, hs_v) = (head_strides(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v")))
         p = _LinAttn(_ptr(q), _ptr(k), _ptr(v), ld_q, ld_k, ld_v, hs_q, hs_k, hs_v, _ptr(log_decay), decay_stride, None,
-                     None, 0, H, G, dk ** -0.5 if scale is None else float(scale))
+                     None, 0, H, G, max(dk, 1) ** -0.5 if scale is None else float(scale))
         args = (ctypes.byref(p), _ptr(state), int(state.shape[0]), _ptr(slots_in), _ptr(slots_out), _ptr(self.y),
                 ctypes.byref(launch))
         self._prepare(dev, stream, launch, lib.vimscan_linattn_step, args, [self.y] if out is None else [],

@@ -1,5 +1,7 @@
 """The block operators as differentiable torch functions: forward and backward both run the library's
-kernels (see ``block`` and ``attention``). Gradients of gradients are not defined and raise."""
+kernels (see ``block`` and ``attention``). Gradients of gradients are not defined and raise. To capture a backward
+pass in a graph, first let go of every eager result that still holds the same leaves' graph: torch ties a leaf's
+accumulation to the stream it was first used on, and joining that stream in a capture ends the process."""
 from __future__ import annotations
 
 import torch

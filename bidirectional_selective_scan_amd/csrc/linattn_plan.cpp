@@ -23,7 +23,7 @@ int check_dims(const vimscan_launch* l, int64_t heads, int64_t groups) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tokens per segment, or 0: sequences stay whole. A wave for each SIMD of the chip (1024): more, shorter segments cost more
-// in their states than they gain (bf16, heads of 64 x 64, us, chunks of 32 tokens per segment: 8 x 1025 x 12, 2: 51, 5: 48, 9: 60, whole 96;
+// in their states than they gain (bf16 with the state read in one part, about 4% less than in two; heads of 64 x 64, us, chunks of 32 tokens per segment: 8 x 1025 x 12, 2: 51, 5: 48, 9: 60, whole 96;
 // 1 x 4096 x 24, 2: 51, 5: 47, 9: 58, whole 337; 16 x 1025 x 12, 2: 91, 5: 69, 9: 71, whole 99; 1 x 65537 x 24, 17: 320, 33: 301, 66: 303).
 // Two where packed sequences differ in length (16 x up to 2000 x 24, 9: 121, 17: 143, 25: 162, whole 176; but 64 x up to 1025 x 12, whose
 // heads alone are 768 waves, in training 9: 510, whole 468), and twice as many in fp32, whose chunks take longer (packed 32 x up to 513 x 6
