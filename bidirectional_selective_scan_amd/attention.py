@@ -182,7 +182,7 @@ class PreparedLinAttnGrad(_Call):
         self.dlog_decay = torch.empty(tuple(inp.log_decay.shape), dtype=torch.float32, device=dev) if decays else None
         self.dh0 = torch.empty(inp.state_shape, dtype=torch.float32, device=dev) if inp.h0 is not None else None
         launch = inp.launch(_stream_of(dev, stream))
-        plan = inp.plan(launch, True)
+        plan = inp.plan(launch, 1 if decays else 2)
         self.plan = _plan_dict(plan)
         ws = _workspace(workspace, plan.workspace_bytes, dev, launch)
         g = _LinAttnGrad(_ptr(dy), ld_dy, hs_dy, _ptr(dh_last), _ptr(self.dq), _ptr(self.dk), _ptr(self.dv),
@@ -254,7 +254,7 @@ def linattn_step(q, k, v, log_decay, state, scale=None, slots_in=None, slots_out
 
 def linattn_info(batch, seqlen, heads, dk, dv, groups=None, seg_len=0, io_dtype="bf16", nseq=None, backward=False) -> dict:
     """The library's plan for a linear attention of this shape (host only; vimscan_linattn_plan); nseq: the
-    number of sequences when they are given by offsets."""
+    number of sequences when they are given by offsets; backward: 2 is the backward pass without the decays' gradient."""
     code = _b.VIMSCAN_BF16 if io_dtype == "bf16" else _b.VIMSCAN_F32
     launch = _b.make_launch(batch, seqlen, heads * dv, dk, code)
     plan = _b._Plan()

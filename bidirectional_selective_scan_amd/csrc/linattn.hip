@@ -7,9 +7,9 @@
 // Backward: the same states, and those of the gradient from the other end; then three passes, for dq, dk and dv, the first
 // two in one launch, all three where they are the same instance (128 x 197 x 12 heads of 64 x 64 bf16 201 us, 217 with a launch
 // for each; packed 32 x up to 513 x 6 of 40 x 56 fp32 227, 246).
-// The decays' gradient is exp(g_t) <S_{t-1}, D_t> = sum over u >= t of (q_u . dq_u - k_u . dk_u), from the segment's end, where it is
-// <S, E>. The dq and dk passes leave those products, without the pair of a token with itself, which is in both and
-// cancels; k_lin_decay_grad adds them up in fp64.
+// The decays' gradient is exp(g_t) <S_{t-1}, D_t> = sum over u = t .. e of (q_u . dq_u - k_u . dk_u) + the same behind e, where that is
+// <S_e, E_e>, formed at the segment's end and at the borders of windows in it (k_lin_borders). The dq and dk passes leave
+// the products q . dq and k . dk, without the pair of a token with itself, which is in both and cancels; k_lin_decay_grad adds them up.
 
 #include <hip/hip_runtime.h>
 
@@ -76,43 +76,125 @@ __global__ __launch_bounds__(256) void k_lin_fold(LinArgs a, float* states, cons
     }
 }
 
+// The values at the borders of windows, exp(g_t) <S_{t-1}, D_t>: the product of what the passes of dq and dk left there. A wave
+// a border, head and block (borders that no segment has are read and never asked for); memory bounds it: 128 x 12 borders of 64 x 64
+// (50 MB) 8.7 us.
+struct BorderArgs {
+    const float* s;
+    const float* e;
+    float* out;
+    int64_t count;
+    int32_t K, V, blocks, NK, NV;
+};
+constexpr int64_t kMaxBorderWgs = 65536;
+__global__ __launch_bounds__(64 * kWaves) void k_lin_borders(BorderArgs a) {
+    const int lane = static_cast<int>(threadIdx.x) & 63, tiles = a.NK * a.NV;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * kWaves + (static_cast<int>(threadIdx.x) >> 6); at < a.count;
+         at += static_cast<int64_t>(gridDim.x) * kWaves) {
+        float sum = 0.0f;
+        if (lin_lane_holds(lane, a.NK, a.NV, a.K, a.V - static_cast<int>(at % a.blocks) * 16 * a.NV)) {
+            const V4f* s = reinterpret_cast<const V4f*>(a.s) + at * tiles * 64 + lane;
+            const V4f* e = reinterpret_cast<const V4f*>(a.e) + at * tiles * 64 + lane;
+#pragma unroll 4
+            for (int t = 0; t < tiles; ++t) {
+                const V4f x = s[t * 64], y = e[t * 64];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum = fmaf(x[r], y[r], sum);
+            }
+        }
+        sum = over_groups(sum);
+        for (int m = 1; m < 16; m *= 2) sum += __shfl_xor(sum, m);
+        if (lane == 0) a.out[at] = sum;
+    }
+}
+
 struct DecayGradArgs {
     const float* rq;     // [blocks][tokens][H]: q . dq and k . dk, pairs of a token with itself left out
     const float* rk;
     const float* cdot;   // [slots][H][blocks]: <S, E> at the segment's end
+    const float* bdot;   // [borders][H][blocks]: the same at the borders of its windows
     int32_t blocks;
     float* by_token;     // [tokens][H] or NULL
     float* by_head;      // [slots][H], the segments' sums, or NULL
 };
 
-// From the segment's end, 64 tokens at a time: the sums of q . dq - k . dk in fp64 (they nearly cancel). A wave a segment and head:
-// 128 x 197 x 12 heads 6.7 us, 1536 waves of four rounds that wait for their loads in turn.
+// Below this log decay the factor is 0 in fp32 (half the least number is e^-103.97): the token's gradient is 0, and nothing behind the
+// token reaches one before it.
+constexpr float kNoFactor = -104.0f;
+
+// dg_t = exp(g_t) <S_{t-1}, D_t>, of which the passes leave the values at the borders of windows: inside a window the sum of
+// q . dq - k . dk from its end, over the value there. The sums hold pairs of tokens that both lie behind t, which cancel but for
+// their rounding and for NaN and infinity: so they go no further than a window, and start anew where a factor is 0. In fp64 (they nearly
+// cancel). A wave a segment and head, half of it a window: 128 x 197 x 12 heads 8.2 us, waves that wait for their loads.
 __global__ __launch_bounds__(64 * kWaves) void k_lin_decay_grad(LinArgs a, DecayGradArgs d) {
-    const int lane = static_cast<int>(threadIdx.x) & 63;
+    constexpr int kPer = vimscan_host::kLinWindow / kChunk;
+    const int lane = static_cast<int>(threadIdx.x) & 63, half = lane >> 5, l = lane & 31;
     const int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     if (task >= a.slots * a.H) return;
     const int64_t slot = task / a.H, h = task - slot * a.H;
     const LinSegment sg = lin_segment(a, slot);
-    double carry = 0.0, mine = 0.0;
+    double mine = 0.0;
     if (sg.valid) {
-        for (int b = 0; b < d.blocks; ++b) carry += d.cdot[task * d.blocks + b];
-        for (int64_t at = 0; at < sg.n; at += 64) {
-            const int64_t i = sg.n - 1 - at - lane;       // walking position
-            const bool in = i >= 0;
-            const int64_t tok = in ? (a.rev ? sg.first + sg.n - 1 - i : sg.first + i) : 0;
+        const int64_t windows = (sg.n + kPer * kChunk - 1) / (kPer * kChunk);
+        auto at_border = [&](int64_t window) {   // behind that window of rows
             double v = 0.0;
-            if (in)
-                for (int b = 0; b < d.blocks; ++b) {
-                    const int64_t k = (b * a.tokens + tok) * a.H + h;
-                    v += static_cast<double>(d.rq[k]) - static_cast<double>(d.rk[k]);
+            for (int b = 0; b < d.blocks; ++b) v += d.bdot[((sg.border + window) * a.H + h) * d.blocks + b];
+            return v;
+        };
+        for (int64_t m0 = 0; m0 < windows; m0 += 2) {
+            const int64_t m = m0 + half;                       // window, from the walk's end
+            const int64_t w = a.rev ? m : windows - 1 - m;     // in rows
+            const bool there = m < windows;
+            // every chunk's terms first: their loads overlap
+            double v[kPer];
+            int cut[kPer];   // a token without a factor is among those from the chunk's end on
+            int64_t tok[kPer];
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+                const int64_t row = w * (kPer * kChunk) + (a.rev ? c * kChunk + l : (kPer - c) * kChunk - 1 - l);
+                tok[c] = there && row < sg.n ? sg.first + row : -1;
+                v[c] = 0.0;
+                cut[c] = 0;
+                if (tok[c] >= 0) {
+                    cut[c] = (a.ld_g ? a.g[tok[c] * a.ld_g + h] : a.g[h]) < kNoFactor;
+                    if (!cut[c])
+                        for (int b = 0; b < d.blocks; ++b) {
+                            const int64_t k = (b * a.tokens + tok[c]) * a.H + h;
+                            v[c] += static_cast<double>(d.rq[k]) - static_cast<double>(d.rk[k]);
+                        }
                 }
-            v = half_wave_sums(v);
-            const double low = lane_value(v, 31);
-            v += carry + (lane >= 32 ? low : 0.0);
-            carry = lane_value(v, 63);
-            if (in) {
-                if (d.by_token) d.by_token[tok * a.H + h] = static_cast<float>(v);
-                mine += v;
+            }
+            double behind = 0.0;   // the value behind the chunk
+            if (there) {
+                if (m > 0) behind = at_border(a.rev ? w - 1 : w);
+                else
+                    for (int b = 0; b < d.blocks; ++b) behind += d.cdot[task * d.blocks + b];
+            }
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+                const int own = cut[c];
+                if (__any(own)) {
+#pragma unroll
+                    for (int s = 1; s < kChunk; s *= 2) {
+                        const double before = __shfl_up(v[c], s, kChunk);
+                        const int cut_before = __shfl_up(cut[c], s, kChunk);
+                        if (l >= s && !cut[c]) {
+                            v[c] += before;
+                            cut[c] = cut_before;
+                        }
+                    }
+                } else {
+                    v[c] = half_wave_sums(v[c]);
+                }
+                if (!cut[c]) v[c] += behind;
+                const double low = lane_value(v[c], kChunk - 1), high = lane_value(v[c], 2 * kChunk - 1);
+                behind = half ? high : low;
+                // (the token at the window's other border has the value there)
+                if (c == kPer - 1 && l == kChunk - 1 && m + 1 < windows && !own) v[c] = at_border(a.rev ? w : w - 1);
+                if (tok[c] >= 0) {
+                    if (d.by_token) d.by_token[tok[c] * a.H + h] = static_cast<float>(v[c]);
+                    mine += v[c];
+                }
             }
         }
     }
@@ -257,6 +339,7 @@ LinArgs common_args(const vimscan_linattn* p, const vimscan_launch* l, const Lin
     a.split = pl.split;
     a.rev = (l->flags & VIMSCAN_FLAG_REVERSE) ? 1 : 0;
     a.slots = pl.slots;
+    a.seg_borders = static_cast<int32_t>(pl.seg_borders);
     // (q, k, v and one more array of v's size, against the 256 MB of the memory-side cache)
     const int64_t e = l->io_dtype == VIMSCAN_F32 ? 4 : 2;
     a.once = pl.tokens * e * (2 * pl.G * pl.dk + 2 * pl.H * pl.dv) > (int64_t(256) << 20);
@@ -295,12 +378,6 @@ void run_pass(int io, bool vec, LinKind kind, const LinArgs& a, hipStream_t s) {
     p.a[0] = a;
     run_passes(io, vec, kind, p, s);
 }
-// Whether two passes can be one launch: the same instance, equally many waves.
-bool alike(int bytes, const LinArgs& a, const LinArgs& b) {
-    return vimscan_host::lin_contract_tiles(a.K) == vimscan_host::lin_contract_tiles(b.K) &&
-           vimscan_host::lin_output_tiles(bytes, a.K, a.V) == vimscan_host::lin_output_tiles(bytes, b.K, b.V) && a.waves == b.waves;
-}
-
 unsigned some_blocks(int64_t elements) {
     const int64_t n = (elements + 255) / 256;
     return static_cast<unsigned>(n < 65536 ? n : 65536);
@@ -452,6 +529,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
         b.e_col = pl.dv;
         b.e_by_slot = by_slot;
         b.cdot = at(pl.off_cd);
+        b.marks = at(pl.off_ms);
     }
     const int32_t qblocks = b.blocks;
     LinPasses three;
@@ -470,6 +548,7 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     if (decays) {
         b.w = k;
         b.dots = at(pl.off_rk);
+        b.marks = at(pl.off_me);
     }
     three.a[1] = b;
     b = a;           // dv, and the gradient of the state before the sequence
@@ -481,11 +560,18 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     b.s_end = grad->dh0;
     b.o = grad->dv;
     three.a[2] = b;
-    three.count = !decays && alike(bytes, three.a[0], b) ? 3 : 2;
+    three.count = !decays && vimscan_host::lin_alike(bytes, pl.dk, pl.dv) ? 3 : 2;
     run_passes(io, vec, decays ? kGradientDots : kGradient, three, s);
     if (three.count == 2) run_pass(io, vec, kGradient, b, s);
     if (decays) {
-        DecayGradArgs d = {at(pl.off_rq), at(pl.off_rk), at(pl.off_cd), qblocks, by_head ? nullptr : grad->dlog_decay,
+        if (pl.borders > 0) {
+            const BorderArgs c = {at(pl.off_ms), at(pl.off_me), at(pl.off_bd), pl.borders * pl.H * qblocks, static_cast<int32_t>(pl.dv),
+                                  static_cast<int32_t>(pl.dk), qblocks, vimscan_host::lin_contract_tiles(pl.dv),
+                                  vimscan_host::lin_output_tiles(bytes, pl.dv, pl.dk)};
+            hipLaunchKernelGGL(k_lin_borders, dim3(static_cast<unsigned>(c.count < kMaxBorderWgs * kWaves ? (c.count + kWaves - 1) / kWaves : kMaxBorderWgs)),
+                               dim3(64 * kWaves), 0, s, c);
+        }
+        DecayGradArgs d = {at(pl.off_rq), at(pl.off_rk), at(pl.off_cd), at(pl.off_bd), qblocks, by_head ? nullptr : grad->dlog_decay,
                            by_head ? at(pl.off_hs) : nullptr};
         const int64_t waves = pl.slots * pl.H;
         hipLaunchKernelGGL(k_lin_decay_grad, dim3(static_cast<unsigned>((waves + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0, s,

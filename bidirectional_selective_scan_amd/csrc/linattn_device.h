@@ -93,6 +93,10 @@ struct LinArgs {
     int64_t e_row, e_col;
     int32_t e_by_slot;
     float* cdot;
+    // kGradientDots: the state at the borders of windows (of dq: S_{t-1}, of dk: exp(g_t) D_t, t the first token behind the border in
+    // the walk of S), [border][H][block], as the wave has it in its registers
+    float* marks;
+    int32_t seg_borders;       // of a segment of a uniform sequence
 };
 
 // Passes of one launch: equally many waves each, of the same instance.
@@ -105,6 +109,7 @@ struct LinPasses {
 struct LinSegment {
     int64_t seq, first;
     int64_t n;
+    int64_t border;            // its first border of windows: those of a segment are consecutive, no two segments share one
     bool valid, head, last;    // the sequence's first or last segment
 };
 
@@ -161,8 +166,14 @@ __device__ __forceinline__ LinSegment lin_segment(const LinArgs& a, int64_t slot
     s.last = w1 == len;
     s.n = uniform(w1 - w0);
     s.first = uniform(a.rev ? hi - w1 : lo + w0);
+    s.border = uniform(a.offsets ? (lo + w0) / vimscan_host::kLinWindow : slot * a.seg_borders);
     s.seq = uniform(s.seq);
     return s;
+}
+
+// Whether a lane's part of a state, NK x NV tiles of which K rows and V columns are the head's, holds any of those.
+__device__ __forceinline__ bool lin_lane_holds(int lane, int NK, int NV, int K, int V) {
+    return 4 * NK * (lane >> 4) < K && NV * (lane & 15) < V;
 }
 
 // The state before (or the gradient behind) a segment.
@@ -893,6 +904,32 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
 #pragma unroll
                     for (int i = 0; i < NK; ++i) S[i][j] = mfma(kc.w[k][i], x, S[i][j]);
                 }
+        }
+        if constexpr (kKind == kGradientDots) {
+            // The border of two windows, between the rows of chunks e_border - 1 and e_border.
+            constexpr int kPer = vimscan_host::kLinWindow / kChunk;
+            const int e_border = desc ? chunks - 1 - m : m + 1;
+            if (m + 1 < chunks && e_border % kPer == 0) {
+                double decay = scaled;
+                if (a.back) {
+                    const int64_t tok = desc ? mem : mem + cnt - 1;
+                    decay += log2_decay(a.ld_g ? a.g[tok * a.ld_g + h] : a.g[h]);
+                }
+                const float2 p = as_pair(decay);
+                const float keep = fast_exp2(p.x + p.y);
+                V4f* const mark = reinterpret_cast<V4f*>(a.marks) +
+                                  (((sg.border + e_border / kPer - 1) * a.H + h) * a.blocks + block) * (64 * NK * NV) + lane;
+                if (lin_lane_holds(lane, NK, NV, a.K, a.V - c0))
+#pragma unroll
+                    for (int i = 0; i < NK; ++i)
+#pragma unroll
+                        for (int j = 0; j < NV; ++j) {
+                            V4f w;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) w[r] = S[i][j][r] * keep;
+                            mark[(i * NV + j) * 64] = w;
+                        }
+            }
         }
     }
 

@@ -119,6 +119,15 @@ int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, i
         p->off_pq = take(rows * p->dk * sizeof(float));
         p->off_pk = take(rows * p->dk * sizeof(float));
     }
+    p->ws_plain = p->ws;
+    // (packed: a segment of n tokens from walking position t on has (n - 1) / window borders from t / window on, at most those before
+    // the next's)
+    p->seg_borders = packed ? 0 : (p->seg - 1) / kLinWindow;
+    p->borders = packed ? p->tokens / kLinWindow : p->slots * p->seg_borders;
+    const size_t at_borders = static_cast<size_t>(p->borders) * heads, marks = at_borders * lin_state_floats(bytes, p->dv, p->dk) * sizeof(float);
+    p->off_ms = take(marks);
+    p->off_me = take(marks);
+    p->off_bd = take(at_borders * qblocks * sizeof(float));
     return VIMSCAN_OK;
 }
 
@@ -164,7 +173,7 @@ int check_linattn_call(const vimscan_linattn* a, const void* y, const float* h_l
     for (int k = 1; k < 5; ++k)
         for (int j = 0; j < k; ++j)
             if (meet(outs[k], outs[j])) return VIMSCAN_ERR_ALIAS;
-    return check_workspace(l, p.ws, ins, outs);
+    return check_workspace(l, g->dlog_decay ? p.ws : p.ws_plain, ins, outs);
 }
 
 int check_linattn_step(const vimscan_linattn* a, const float* state, int64_t nslots, const int32_t* slots_in,
@@ -217,14 +226,16 @@ int vimscan_linattn_plan(const vimscan_launch* launch, int64_t seg_len, int64_t 
     plan->chunks = p.nseq == 0 ? 0 : p.split && packed ? p.slots : p.segs;
     plan->workgroups = p.waves;
     // forward: the pass, where it is split after the segments' states and their fold; backward: the same
-    // states and those of the gradients, the passes of dq and dk in one launch and that of dv, the decays'
-    // gradient (and its sum over the tokens), the sums over shared heads
+    // states and those of the gradients, the passes of dq and dk in one launch and that of dv, the values at
+    // the windows' borders, the decays' gradient and its sum over the tokens (without it passes that are alike are one launch), the sums over shared heads
+    const bool decays = backward != 2;
     if (p.waves > 0) {
         if (!backward) plan->kernels = p.split ? 3 : 1;
-        else if (p.tokens > 0) plan->kernels = (p.split ? 4 : 0) + 2 + 2 + (p.G != p.H ? 2 : 0);
-        else plan->kernels = 2;
+        else if (p.tokens == 0) plan->kernels = decays ? 2 : 1;
+        else plan->kernels = (p.split ? 4 : 0) + (decays ? 4 + (p.borders > 0) : lin_alike(static_cast<int>(io_bytes(launch)), p.dk, p.dv) ? 1 : 2) +
+                             (p.G != p.H ? 2 : 0);
     }
-    plan->workspace_bytes = p.ws;
+    plan->workspace_bytes = backward && !decays && p.tokens > 0 ? p.ws_plain : p.ws;
     return VIMSCAN_OK;
 }
 

@@ -12,6 +12,10 @@ namespace vimscan_host {
 
 constexpr int64_t kLinMaxDim = 128;    // of dk and dv
 constexpr int kLinChunk = 32;          // tokens that a wave works on at once
+// Tokens that a sum of the decays' gradient reaches over. Between windows the state and its gradient are written, read and multiplied
+// (8 dk dv bytes each way): backward of 128 x 197 x 12 heads of 64 x 64 bf16, us, windows of 64: 199, 128: 160, 256: 152, sequences whole: 146;
+// 1 x 16385 x 24: 364, 308, 276, 250. Shorter ones keep a token's rounding (and NaN) nearer to it.
+constexpr int kLinWindow = 128;
 constexpr int64_t kMaxHeadStride = int64_t(1) << 38;
 // Workgroups of 64 threads (a wave) and of 256: a grid holds fewer than 2^32 threads.
 constexpr int64_t kMaxLinWaves = (int64_t(1) << 26) - 1, kMaxLinWgs = (int64_t(1) << 24) - 1;
@@ -41,7 +45,22 @@ struct LinPlan {
     // workspace: the segments' states and decays; backward also their gradients, the terms of the decays'
     // gradient, and gradients of shared q and k by head
     size_t off_s, off_e, off_tot, off_rq, off_rk, off_cd, off_hs, off_pq, off_pk, ws;
+    // at its end, for the decays' gradient alone: the borders of windows inside segments, and the state, its gradient and their product
+    // at each
+    int64_t borders, seg_borders;      // in all; of a segment of a uniform sequence
+    size_t off_ms, off_me, off_bd, ws_plain;   // ws_plain: what a backward pass without the decays' gradient needs
 };
+
+// Numbers that waves hold of a head's state, all blocks of output channels, whole tiles.
+constexpr int64_t lin_state_floats(int bytes, int64_t k, int64_t v) {
+    return int64_t(256) * lin_contract_tiles(k) * lin_output_tiles(bytes, k, v) * lin_blocks(bytes, k, v);
+}
+
+// Whether passes (contracted, output) = (k, v) and (v, k) can be one launch: the same instance, equally many waves.
+constexpr bool lin_alike(int bytes, int64_t k, int64_t v) {
+    return lin_contract_tiles(k) == lin_contract_tiles(v) && lin_output_tiles(bytes, k, v) == lin_output_tiles(bytes, v, k) &&
+           lin_blocks(bytes, k, v) == lin_blocks(bytes, v, k);
+}
 
 // Packed sequence q takes the slots from offsets[q] / seg + q on: up to the next sequence's first these are
 // floor(offsets[q + 1] / seg) - floor(offsets[q] / seg) + 1 >= ceil(length / seg), one for each of its segments.

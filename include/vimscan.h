@@ -558,8 +558,10 @@ typedef struct vimscan_linattn_grad {
  * dq and dk are summed over the heads of a group, dlog_decay [heads] over all tokens, in a fixed order: the
  * same bits on every run. Nothing but the inputs is kept from the forward pass. The gradients
  * must not overlap an input, each other or the workspace, which every call with tokens needs
- * (vimscan_linattn_plan). A NaN or infinity may reach gradients of up to 31 tokens beyond those that
- * depend on it, in its sequence and head.
+ * (vimscan_linattn_plan; without dlog_decay a smaller one). A NaN or infinity may reach gradients of up to 31 tokens
+ * beyond those that depend on it, in its sequence and head, dlog_decay of up to 127. dg_t is formed from sums over up
+ * to 127 tokens behind t in which what does not belong to it cancels: their rounding, 2^-24 of the terms, stays. Where
+ * g_t is below -104, a factor that is 0 in fp32, dg_t is 0 and nothing behind t reaches dg of a token before it.
  */
 int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan_linattn_grad* grad,
                         const vimscan_launch* launch);
@@ -575,10 +577,11 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
 int vimscan_linattn_step(const vimscan_linattn* p, float* state, int64_t nslots, const int32_t* slots_in,
                          const int32_t* slots_out, void* y, const vimscan_launch* launch);
 
-/* Plan of a vimscan_linattn_fwd (backward 0) or vimscan_linattn_bwd (backward 1) call: sequences; seq_tokens
-   (0 with offsets); chunk_len = tokens per segment, chunks = segments per sequence (with offsets: segments at
-   most), 1 and the sequence's tokens (0 with offsets) when sequences are not cut; workgroups of the pass that
-   writes the outputs; kernels (with every gradient wanted); workspace_bytes. packed: 1 when offsets are set. Host only. */
+/* Plan of a vimscan_linattn_fwd (backward 0) or vimscan_linattn_bwd (backward 1; 2: without dlog_decay) call:
+   sequences; seq_tokens (0 with offsets); chunk_len = tokens per segment, chunks = segments per sequence (with
+   offsets: segments at most), 1 and the sequence's tokens (0 with offsets) when sequences are not cut; workgroups of
+   the pass that writes the outputs; kernels (with a decay per head and dh0 wanted: the most); workspace_bytes. packed: 1
+   when offsets are set. Host only. */
 int vimscan_linattn_plan(const vimscan_launch* launch, int64_t seg_len, int64_t heads, int64_t groups, int packed,
                          int64_t nseq, int backward, vimscan_plan* plan);
 
