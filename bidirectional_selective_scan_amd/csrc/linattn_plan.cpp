@@ -23,19 +23,24 @@ int check_dims(const vimscan_launch* l, int64_t heads, int64_t groups) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tokens per segment, or 0: sequences stay whole. A wave for each SIMD of the chip (1024): more, shorter segments cost more
-// in their states than they gain (bf16 with the state read in one part, about 4% less than in two; heads of 64 x 64, us, chunks of 32 tokens per segment: 8 x 1025 x 12, 2: 51, 5: 48, 9: 60, whole 96;
-// 1 x 4096 x 24, 2: 51, 5: 47, 9: 58, whole 337; 16 x 1025 x 12, 2: 91, 5: 69, 9: 71, whole 99; 1 x 65537 x 24, 17: 320, 33: 301, 66: 303).
-// Two where packed sequences differ in length (16 x up to 2000 x 24, 9: 121, 17: 143, 25: 162, whole 176; but 64 x up to 1025 x 12, whose
-// heads alone are 768 waves, in training 9: 510, whole 468), and twice as many in fp32, whose chunks take longer (packed 32 x up to 513 x 6
-// in training 3: 223, 9: 302, whole 288). The segments' own states and their fold cost about as much as 0.6 of the pass and three chunks:
-// where that is not less than the chunks saved, sequences stay whole.
+// in their states than they gain (heads of 64 x 64 bf16, forward, us, chunks of 32 tokens per segment; 8 x 1025 x 12 with the state read
+// in one part, about 4% less than in two: 2: 51, 5: 48, 9: 60, whole 96; 1 x 65537 x 24, 17: 324, 25: 305, 33: 296, 49: 306).
+// Two where packed sequences differ in length (in one part too: 16 x up to 2000 x 24, 9: 121, 17: 143, 25: 162, whole 176; but 64 x up to
+// 1025 x 12, whose heads alone are 768 waves, in training 9: 510, whole 468), and twice as many in fp32, whose chunks take
+// longer (packed 32 x up to 513 x 6 in training 3: 223, 9: 302, whole 288).
+// Where sequences and heads alone are more than half as many waves, they stay whole, however long (64 x 4097 x 24 whole 788, 64: 1233, 128: 1300;
+// 43 x 8200 x 24 1219, 1571, 1790; 22 x 8200 x 24 812, 900, 931).
+// Segments are of nearly equal length (16 x 8200 x 24, 257 chunks: three of 86 657, two of 128 and a single chunk 817). Their own states and
+// the fold cost about as much as 0.6 of the pass and three chunks: where that is not less than the chunks saved, sequences stay whole.
 int64_t segment(int64_t length, int64_t waves, bool packed, int bytes) {
     constexpr int64_t kLeast = 2, kMost = 128;   // chunks
     const int64_t chunks = up(length, kLinChunk), parts = 1024 * (packed ? 2 : 1) * (bytes == 4 ? 2 : 1) / waves;
-    if (parts < (packed ? 3 : 2)) return chunks > kMost ? kMost * kLinChunk : 0;
+    if (parts < (packed ? 3 : 2)) return packed && chunks > kMost ? kMost * kLinChunk : 0;
+    if (chunks <= kLeast) return 0;
     int64_t seg = up(chunks, parts);
     if (seg < kLeast) seg = kLeast;
     if (seg > kMost) seg = kMost;
+    seg = up(chunks, up(chunks, seg));
     return 10 * chunks <= 16 * seg + 30 ? 0 : seg * kLinChunk;
 }
 
