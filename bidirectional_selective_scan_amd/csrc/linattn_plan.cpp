@@ -30,6 +30,9 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // longer (packed 32 x up to 513 x 6 in training 3: 223, 9: 302, whole 288).
 // Where sequences and heads alone are more than half as many waves, they stay whole, however long (64 x 4097 x 24 whole 788, 64: 1233, 128: 1300;
 // 43 x 8200 x 24 1219, 1571, 1790; 22 x 8200 x 24 812, 900, 931).
+// The fold walks a sequence's segments one behind the other, eight at a time, so with few heads a segment is no shorter than the square root of
+// chunks / 32, where a segment's chunks and the fold cost alike (1 x 65537 x 1 head, 3: 119, 4: 99, 8: 84, 12: 91; 1 x 16385 x 1,
+// 2: 59, 4: 52, 6: 55; 4 x 8192 x 2, 2: 50, 3: 47, 4: 46; 1 x 65537 x 2 in training 5: 334, 8: 309, 12: 327).
 // Segments are of nearly equal length (16 x 8200 x 24, 257 chunks: three of 86 657, two of 128 and a single chunk 817). Their own states and
 // the fold cost about as much as 0.6 of the pass and three chunks: where that is not less than the chunks saved, sequences stay whole.
 int64_t segment(int64_t length, int64_t waves, bool packed, int bytes) {
@@ -40,6 +43,7 @@ int64_t segment(int64_t length, int64_t waves, bool packed, int bytes) {
     int64_t seg = up(chunks, parts);
     if (seg < kLeast) seg = kLeast;
     if (seg > kMost) seg = kMost;
+    while (32 * seg * seg < chunks) ++seg;
     seg = up(chunks, up(chunks, seg));
     return 10 * chunks <= 16 * seg + 30 ? 0 : seg * kLinChunk;
 }

@@ -20,3 +20,11 @@ def test_segments_are_of_nearly_equal_length(batch, length):
     seg, count = segments(batch, length, 24, 64, 64)
     chunks = -(-length // 32)
     assert seg == -(-chunks // count) * 32 and (count - 1) * seg < length <= count * seg
+
+
+@pytest.mark.parametrize("heads,io,d", [(1, "bf16", 64), (2, "bf16", 64), (1, "f32", 16), (1, "f32", 128)])
+@pytest.mark.parametrize("length", [2048, 16385, 65537, 1 << 20, (1 << 31) - 1])
+def test_few_heads_do_not_wait_for_the_fold(heads, io, d, length):
+    """The fold's rounds of eight segments, each some 0.4 of a chunk in two passes, are not many more than the segment's chunks."""
+    seg, count = segments(1, length, heads, d, d, io_dtype=io)
+    assert 0.4 * count / 8 <= 1.6 * seg / 32 + 1
