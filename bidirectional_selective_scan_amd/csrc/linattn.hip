@@ -39,11 +39,21 @@ using vimscan_host::LinPlan;
 constexpr int kWaves = 4;   // waves of the workgroups of the kernels here
 
 constexpr int kFoldAhead = 8;
-// Replaces every segment's own state by the state it starts from, in the order of the walk (from the end: from the last
-// segment on): X = init; for each segment: its place <- X, X = decay X + (what was there). One element a thread; a chain of
-// loads bounds it, eight on their way at once: 42 segments of 24 heads of 64 x 64 (33 MB moved) 12 us.
+// Replaces every segment's own state but those at the sequence's edges by the state it starts from, in the order of the walk (from the
+// end: from the last segment on): X = init; for each segment: its place <- X (the first starts from init itself), X = decay X + (what was
+// there; of the last nothing is needed). One element a thread; a chain of loads bounds it, eight on their way at once: 42 segments of 24 heads
+// of 64 x 64 (33 MB moved) 12 us.
 __global__ __launch_bounds__(256) void k_lin_fold(LinArgs a, float* states, const float* tot, const float* init, int from_end) {
     const int64_t ks = static_cast<int64_t>(a.K) * a.V, per_seq = a.H * ks, all = a.nseq * per_seq;
+    if (a.offsets && a.nseq <= 4096) {   // often no packed sequence is cut: one look at all of them
+        bool any = false;
+        for (int64_t seq = threadIdx.x; seq < a.nseq; seq += 256) {
+            int64_t lo, hi;
+            lin_bounds(a, seq, &lo, &hi);
+            any = any || hi - lo > a.seg;
+        }
+        if (!__syncthreads_or(any)) return;
+    }
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; t < all; t += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t seq = t / per_seq, at = t - seq * per_seq, h = at / ks;
         int64_t first = seq * a.segs, count = a.segs;
@@ -52,24 +62,23 @@ __global__ __launch_bounds__(256) void k_lin_fold(LinArgs a, float* states, cons
             lin_bounds(a, seq, &lo, &hi);
             first = lin_base(a, seq);
             count = (hi - lo + a.seg - 1) / a.seg;
-            if (count < 1) count = 1;
         }
+        if (count < 2) continue;
         float x = init ? init[t] : 0.0f;
-        // (an empty sequence's one segment has no decay and adds nothing: both were written by its pass)
         const int64_t from = first + (from_end ? count - 1 : 0), step = from_end ? -1 : 1;
         for (int64_t j = 0; j < count; j += kFoldAhead) {
             // as many loads on their way at once
             float mine[kFoldAhead], dec[kFoldAhead];
 #pragma unroll
             for (int k = 0; k < kFoldAhead; ++k) {
-                const int64_t slot = from + (j + k < count ? j + k : count - 1) * step;
+                const int64_t slot = from + (j + k < count - 1 ? j + k : count - 2) * step;
                 mine[k] = states[slot * per_seq + at];
                 dec[k] = tot[slot * a.H + h];
             }
 #pragma unroll
             for (int k = 0; k < kFoldAhead; ++k)
                 if (j + k < count) {
-                    states[(from + (j + k) * step) * per_seq + at] = x;
+                    if (j + k > 0) states[(from + (j + k) * step) * per_seq + at] = x;
                     x = fmaf(dec[k], x, mine[k]);
                 }
         }
@@ -385,7 +394,7 @@ unsigned some_blocks(int64_t elements) {
 
 void run_fold(const LinArgs& a, float* states, const float* tot, const float* init, bool from_end, hipStream_t s) {
     const int64_t all = static_cast<int64_t>(a.nseq) * a.H * a.K * a.V;
-    hipLaunchKernelGGL(k_lin_fold, dim3(some_blocks(all)), dim3(256), 0, s, a, states, tot, init, from_end ? 1 : 0);
+    hipLaunchKernelGGL(k_lin_fold, dim3(some_blocks(all) < 2048 ? some_blocks(all) : 2048), dim3(256), 0, s, a, states, tot, init, from_end ? 1 : 0);
 }
 
 // Whether rows are whole pieces of 16 bytes that start at multiples of four bytes (the hardware takes those as they are).
@@ -440,8 +449,7 @@ int vimscan_linattn_fwd(const vimscan_linattn* p, int64_t seg_len, void* y, floa
         b.tot = tot;
         run_pass(io, vec, kLocal, b, s);
         run_fold(a, states, tot, p->h0, false, s);
-        a.s0 = states;
-        a.s0_by_slot = 1;
+        a.s0_seg = states;
     }
     a.out_scale = p->scale;
     a.o = y;
@@ -504,30 +512,30 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
         b.back = 1;
         b.key_scale = p->scale;
         b.s_end = at(pl.off_e);
+        b.tot = at(pl.off_tot);
         run_pass(io, vec, kLocal, b, s);
         run_fold(b, at(pl.off_e), at(pl.off_tot), grad->dh_last, true, s);
     }
     const bool decays = grad->dlog_decay != nullptr;
-    const float* s0 = pl.split ? at(pl.off_s) : p->h0;
-    const float* e0 = pl.split ? at(pl.off_e) : grad->dh_last;
-    const int32_t by_slot = pl.split;
+    const float* s_seg = pl.split ? at(pl.off_s) : nullptr;
+    const float* e_seg = pl.split ? at(pl.off_e) : nullptr;
     const bool shared = rep > 1;
     LinArgs b = a;   // dq: forward, the state transposed
     set_roles(bytes, &b, dy, v, k, pl.dv, pl.dk);
-    b.s0 = s0;
+    b.s0 = p->h0;
+    b.s0_seg = s_seg;
     b.s0_row = 1;
     b.s0_col = pl.dv;
-    b.s0_by_slot = by_slot;
     b.out_scale = p->scale;
     b.o = shared ? at(pl.off_pq) : grad->dq;
     b.o_f32 = shared;
     if (decays) {
         b.w = q;
         b.dots = at(pl.off_rq);
-        b.e = e0;
+        b.e = grad->dh_last;
+        b.e_seg = e_seg;
         b.e_row = 1;
         b.e_col = pl.dv;
-        b.e_by_slot = by_slot;
         b.cdot = at(pl.off_cd);
         b.marks = at(pl.off_ms);
     }
@@ -539,10 +547,10 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     set_roles(bytes, &b, v, dy, q, pl.dv, pl.dk);
     b.back = 1;
     b.key_scale = p->scale;
-    b.s0 = e0;
+    b.s0 = grad->dh_last;
+    b.s0_seg = e_seg;
     b.s0_row = 1;
     b.s0_col = pl.dv;
-    b.s0_by_slot = by_slot;
     b.o = shared ? at(pl.off_pk) : grad->dk;
     b.o_f32 = shared;
     if (decays) {
@@ -555,8 +563,8 @@ int vimscan_linattn_bwd(const vimscan_linattn* p, int64_t seg_len, const vimscan
     set_roles(bytes, &b, k, q, dy, pl.dk, pl.dv);
     b.back = 1;
     b.key_scale = p->scale;
-    b.s0 = e0;
-    b.s0_by_slot = by_slot;
+    b.s0 = grad->dh_last;
+    b.s0_seg = e_seg;
     b.s_end = grad->dh0;
     b.o = grad->dv;
     three.a[2] = b;

@@ -78,20 +78,21 @@ struct LinArgs {
     int32_t once;              // inputs that are not kept in the caches
     int32_t back;              // walk from the segment's end (on top of rev), decays moved by one
     float key_scale, out_scale;
-    // state before the segment: of its sequence or, by_slot, of itself; NULL: 0. Element (i, j) is at i row + j col
+    // state before a sequence (in the pass' walk; NULL: 0) and before its other segments, by slot. Element (i, j) is at i row + j col
     const float* s0;
+    const float* s0_seg;
     int64_t s0_row, s0_col;
-    int32_t s0_by_slot;
     float* s_end;              // kLocal: of the segment; else of the sequence, written by its last segment; dense K x V
     float* tot;                // kLocal: the segment's decay
+    // (kLocal leaves out the segment that its walk ends with: nothing comes after it)
     void* o;                   // [tokens][H][V], dense
     int32_t o_f32;             // in fp32 whatever the io type
     // kGradientDots: dots[block][token][head] = w . o without a token's pair with itself
     LinRows w;
     float* dots;
-    const float* e;            // gradient of the state behind the segment (as s0); cdot[slot][head][block] = <S, e>
+    const float* e;            // gradient of the state behind a sequence, e_seg its other segments (as s0); cdot[slot][head][block] = <S, e>
+    const float* e_seg;
     int64_t e_row, e_col;
-    int32_t e_by_slot;
     float* cdot;
     // kGradientDots: the state at the borders of windows (of dq: S_{t-1}, of dk: exp(g_t) D_t, t the first token behind the border in
     // the walk of S), [border][H][block], as the wave has it in its registers
@@ -176,10 +177,11 @@ __device__ __forceinline__ bool lin_lane_holds(int lane, int NK, int NV, int K, 
     return 4 * NK * (lane >> 4) < K && NV * (lane & 15) < V;
 }
 
-// The state before (or the gradient behind) a segment.
-__device__ __forceinline__ const float* lin_state(const float* p, int32_t by_slot, int64_t slot, int64_t seq, const LinArgs& a,
-                                                  int64_t h) {
-    return p ? p + ((by_slot ? slot : seq) * a.H + h) * (static_cast<int64_t>(a.K) * a.V) : nullptr;
+// The state before (or the gradient behind) a segment: the sequence's at its edge, else the segment's own.
+__device__ __forceinline__ const float* lin_state(const float* of_seq, const float* of_slot, bool edge, int64_t slot, int64_t seq,
+                                                  const LinArgs& a, int64_t h) {
+    const float* p = edge ? of_seq : of_slot;
+    return p ? p + ((edge ? seq : slot) * a.H + h) * (static_cast<int64_t>(a.K) * a.V) : nullptr;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -505,7 +507,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
     const int block = static_cast<int>(task % a.blocks);
     const int64_t rest = task / a.blocks, h = rest % a.H, slot = rest / a.H;
     const LinSegment sg = lin_segment(a, slot);
-    if (!sg.valid) return;
+    if (!sg.valid || (kKind == kLocal && (a.back ? sg.head : sg.last))) return;
     const bool desc = (a.rev != 0) != (a.back != 0);
     const int c0 = block * 16 * NV, vc = c0 + NV * col;   // the block's and the lane's value channels
 
@@ -513,7 +515,7 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
     V4f S[NK][NV];
     const int64_t ks = static_cast<int64_t>(a.K) * a.V;
     {
-        const float* s0 = kKind == kLocal ? nullptr : lin_state(a.s0, a.s0_by_slot, slot, sg.seq, a, h);
+        const float* s0 = kKind == kLocal ? nullptr : lin_state(a.s0, a.s0_seg, a.back ? sg.last : sg.head, slot, sg.seq, a, h);
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
@@ -950,10 +952,11 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         const double g = log2_decay(a.ld_g ? a.g[tok * a.ld_g + h] : a.g[h]);
         const float2 p = as_pair(g);
         rest_decay = fast_exp2(p.x + p.y);
+        if (kKind == kLocal) all += g;
     }
     if constexpr (kKind == kGradientDots) {
         if (a.cdot) {
-            const float* ep = lin_state(a.e, a.e_by_slot, slot, sg.seq, a, h);
+            const float* ep = lin_state(a.e, a.e_seg, sg.last, slot, sg.seq, a, h);
             float sum = 0.0f;
             if (ep)
                 state_elements<NK, NV>(ep, a.K, a.V, a.e_row, a.e_col, grp, vc,

@@ -38,8 +38,7 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t segment(int64_t length, int64_t waves, bool packed, int bytes) {
     constexpr int64_t kLeast = 2, kMost = 128;   // chunks
     const int64_t chunks = up(length, kLinChunk), parts = 1024 * (packed ? 2 : 1) * (bytes == 4 ? 2 : 1) / waves;
-    if (parts < (packed ? 3 : 2)) return packed && chunks > kMost ? kMost * kLinChunk : 0;
-    if (chunks <= kLeast) return 0;
+    if (parts < (packed ? 3 : 2) || chunks <= kLeast) return 0;
     int64_t seg = up(chunks, parts);
     if (seg < kLeast) seg = kLeast;
     if (seg > kMost) seg = kMost;
@@ -101,6 +100,14 @@ int make_linattn_plan(const vimscan_launch* l, int64_t seg_len, int64_t heads, i
     const int64_t most_waves = kMaxLinWaves / ((blocks > qblocks ? blocks : qblocks) * heads * (backward ? 3 : 1));
     if (p->nseq > most_waves) return VIMSCAN_ERR_SHAPE;
     p->seg = segment(length, p->nseq * heads * blocks, packed, bytes);
+    // packed sequences that are whole by that: any that is longer than they are taken to be is cut, if it could be a long chain
+    // (24 heads of 64 x 64 bf16, forward and backward, us: 65537 + 63 x 1 tokens 763 + 2610, whole 6320 + 20900; 12 heads, 20000 + 200 x 100
+    // 494 + 1200, whole 1926 + 6010). Where none is cut the two launches cost some 10 us (256 x up to 513 x 12 138 + 495, whole 127 + 455;
+    // 64 x up to 65 x 12 23 + 56, whole 14 + 40, which at most 8192 tokens stay).
+    if (packed && p->seg == 0 && p->tokens > kLinLongest) {
+        const int64_t most = length > kLinLongest / 4 ? up(length, kLinChunk) * kLinChunk : kLinLongest / 4;
+        if (p->tokens > most && p->tokens / most + p->nseq <= most_waves) p->seg = most;
+    }
     p->split = p->seg > 0;
     p->segs = p->split && !packed ? up(p->Lp, p->seg) : 1;
     p->slots = !p->split ? p->nseq : packed ? p->tokens / p->seg + p->nseq : p->nseq * p->segs;

@@ -16,6 +16,7 @@ constexpr int kLinChunk = 32;          // tokens that a wave works on at once
 // (8 dk dv bytes each way): backward of 128 x 197 x 12 heads of 64 x 64 bf16, us, windows of 64: 199, 128: 160, 256: 152, sequences whole: 146;
 // 1 x 16385 x 24: 364, 308, 276, 250. Shorter ones keep a token's rounding (and NaN) nearer to it.
 constexpr int kLinWindow = 128;
+constexpr int64_t kLinLongest = 8192;   // tokens of packed sequences that a plan may leave whole on their mean alone
 constexpr int64_t kMaxHeadStride = int64_t(1) << 38;
 // Workgroups of 64 threads (a wave) and of 256: a grid holds fewer than 2^32 threads.
 constexpr int64_t kMaxLinWaves = (int64_t(1) << 26) - 1, kMaxLinWgs = (int64_t(1) << 24) - 1;

@@ -28,3 +28,17 @@ def test_few_heads_do_not_wait_for_the_fold(heads, io, d, length):
     """The fold's rounds of eight segments, each some 0.4 of a chunk in two passes, are not many more than the segment's chunks."""
     seg, count = segments(1, length, heads, d, d, io_dtype=io)
     assert 0.4 * count / 8 <= 1.6 * seg / 32 + 1
+
+
+@pytest.mark.parametrize("tokens,nseq", [(65600, 64), (65569, 33), (40000, 201), (8448, 257), (1 << 20, 4096), (1 << 20, 40), (33000, 1000)])
+@pytest.mark.parametrize("heads,io", [(24, "bf16"), (1, "bf16"), (24, "f32")])
+@pytest.mark.parametrize("backward", [False, True])
+def test_one_long_packed_sequence_is_never_walked_whole(tokens, nseq, heads, io, backward):
+    """Only the mean length is known: where all tokens could be one sequence's, it is cut at 2048 tokens or twice the mean."""
+    p = binding.linattn_info(1, tokens, heads, 64, 64, io_dtype=io, nseq=nseq, backward=backward)
+    assert 0 < p["chunk_len"] <= max(2048, 2 * -(-tokens // nseq) + 31)
+    assert p["chunks"] == tokens // p["chunk_len"] + nseq
+
+
+def test_few_packed_tokens_take_one_kernel():
+    assert binding.linattn_info(1, 8192, 12, 64, 64, nseq=128)["kernels"] == 1
