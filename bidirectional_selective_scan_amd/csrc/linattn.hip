@@ -356,7 +356,8 @@ LinArgs common_args(const vimscan_linattn* p, const vimscan_launch* l, const Lin
     return a;
 }
 
-// The roles of a pass: reader, key, value.
+// The roles of a pass: reader, key, value. Its rows are not kept in the caches (kOnce) only where no other wave asks for their lines: a
+// block of a head's outputs, a head of a group, the head beside it in a line of 128 bytes would fetch them from memory again.
 void set_roles(int bytes, LinArgs* a, const LinRows& r, const LinRows& k, const LinRows& v, int64_t K, int64_t V) {
     a->r = r;
     a->k = k;
@@ -365,6 +366,7 @@ void set_roles(int bytes, LinArgs* a, const LinRows& r, const LinRows& k, const 
     a->V = static_cast<int32_t>(V);
     a->blocks = static_cast<int32_t>(vimscan_host::lin_blocks(bytes, K, V));
     a->waves = a->slots * a->H * a->blocks;
+    if (a->blocks > 1 || r.div > 1 || k.div > 1 || v.div > 1 || K * bytes % 128 != 0) a->once = 0;
 }
 
 void run_passes(int io, bool vec, LinKind kind, const LinPasses& p, hipStream_t s) {

@@ -259,10 +259,12 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
 template <typename T>
 __device__ __forceinline__ uint32_t piece_at(int c, int D) { return c < D ? static_cast<uint32_t>(c * sizeof(IoElem<T>)) : kOutside; }
 // Cache policy of the passes' loads. kOnce: the lines are not kept. Calls whose inputs do not fit the memory-side cache take it:
-// lines that are kept throw out others, written ones among them, for nothing (k and v of 1 x 65537 x 24 x 64 x 64, 403 MB,
-// in the segments' states: 123 us kept, 90 us not); those that fit are read again by the passes that follow (128 x 197 x 12 x 64 x 64,
-// backward 147 us kept, 161 us not). Gradients in bf16 are written so always (forward and backward 195 us, 201 kept), y never
-// (64 packed x up to 1025 x 24 x 128 x 64: 236 us so, 231 kept).
+// lines that are kept throw out others, written ones among them, for nothing (64 x 1025 x 24 heads of 64 x 64 bf16 202 us, kept 218; 1 x 65537 x 24
+// 300, 325); those that fit are read again by the passes that follow (128 x 197 x 12 of 64 x 64, backward 160 us kept, 187 not). Where other waves
+// ask for the same lines they are kept at any size (32 x 1025 x 16 of 128 x 128, four blocks a head, 211 us kept, 276 not; 64 x 1025 x 24 of
+// 32 x 32, two heads a line, 216, 230; 64 x 1025 x 12 of 64 x 64 fp32 269, 285; 64 x 1025 x 24 in 4 groups, backward 1128, 1160).
+// Gradients in bf16 are written so always, y never (64 packed x up to 1025 x 24 in one group of 128 x 64: 217 us so, 227 kept;
+// 1 x 65537 x 24 of 64 x 64: 306, 301; 32 x 1025 x 16 of 128 x 128: 288, 279; 128 x 197 x 12 alike).
 constexpr int kKeep = 0, kOnce = 2;
 template <int kPolicy>
 __device__ __forceinline__ U4 load_b128(__amdgpu_buffer_rsrc_t rsrc, uint32_t at) {
@@ -589,7 +591,8 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
         int cnt;
         place(m, &mem, &cnt);
         // sums of the log decays over the chunk: before its rows are waited for or, with 128 contracted channels, during the
-        // products with the state (64 x 1025 packed x 24 heads of 128 x 64: 231 us, 272 before; 8 x 1025 x 12 of 64 x 64: 49, 47 before)
+        // products with the state (32 x 1025 x 16 heads of 128 x 128: 278 us, 289 before; but 128 x 197 x 12 of 64 x 64 50, 46 before, 1 x 65537 x 24
+        // 367, 301)
         constexpr bool kSumLate = NK == 8 && kKind != kLocal;
         const float g = gv;
         double total = 0.0;
