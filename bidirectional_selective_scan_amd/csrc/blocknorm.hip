@@ -89,7 +89,7 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_fwd(NormArgs a) {
         float rho = 1.0f;
         if (a.w_post) {
             row_sum<L, W>(&ss, &none, lds, slot, wave);
-            rho = fast_rsq(fmaf(ss, a.inv_d, a.eps));
+            rho = root_inverse(fmaf(ss, a.inv_d, a.eps));
         }
         ss = none = 0.0f;
         all([&](int k, int v) { s[k][v] *= rho * wp[k][v]; });
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_fwd(NormArgs a) {
         if (a.sum) st_row<RES, S>(a.sum, row * a.D, a.D, s);
         if (!a.w_pre) continue;
         row_sum<L, W>(&ss, &none, lds, slot, wave);
-        rho = fast_rsq(fmaf(ss, a.inv_d, a.eps));
+        rho = root_inverse(fmaf(ss, a.inv_d, a.eps));
         all([&](int k, int v) { s[k][v] *= rho * wn[k][v]; });
         st_row<IO, S>(a.n, row * a.D, a.D, s);
     }
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
         float rho1 = 1.0f, rho2 = 0.0f, k2 = 0.0f;
         if (a.w_post) {
             row_sum<L, W>(&u, &t, lds, slot, wave);
-            rho1 = fast_rsq(fmaf(u, a.inv_d, a.eps));
+            rho1 = root_inverse(fmaf(u, a.inv_d, a.eps));
         }
         u = t = 0.0f;
         read_first();
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(S::kThreads) void k_norm_bwd(NormArgs a) {
                 t = fmaf(dn[k].get(v) * wn[k][v], s[k][v], t);
             });
             row_sum<L, W>(&u, &t, lds, slot, wave);
-            rho2 = fast_rsq(fmaf(u, a.inv_d, a.eps));
+            rho2 = root_inverse(fmaf(u, a.inv_d, a.eps));
             k2 = t * a.inv_d * rho2 * rho2 * rho2;
             read_last();
             // from here s is the gradient of the sum

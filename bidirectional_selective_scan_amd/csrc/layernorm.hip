@@ -72,7 +72,7 @@ __device__ __forceinline__ float center(const LayerNormArgs& a, float (&s)[S::NV
             u = fmaf(s[k][v], s[k][v], u);
         }
     row_sum<S::L, S::W>(&u, &t, lds, slot, wave);
-    return fast_rsq(fmaf(u, a.inv_d, a.eps));
+    return root_inverse(fmaf(u, a.inv_d, a.eps));
 }
 
 // Forward: s = x + residual, n = (s - mean) rsq(var + eps) weight + bias. Memory bounds it: a row stays in registers from

@@ -59,6 +59,12 @@ __device__ __forceinline__ void row_sum(float* u, float* v, float2 (*lds)[W], in
     }
 }
 
+// 1 / sqrt(v). The hardware's takes subnormal numbers, which a small eps alone may leave, for 0.
+__device__ __forceinline__ float root_inverse(float v) {
+    const bool tiny = v < 0x1p-126f;
+    return fast_rsq(tiny ? v * 0x1p24f : v) * (tiny ? 0x1p12f : 1.0f);
+}
+
 // A row spread over L lanes of a wave (W = 1) or W whole waves (L = 64), each lane NV vectors of V channels
 // (NormSpread, whose tables say which widths take which). kWhole: the width is a multiple of V; otherwise a row's last vector is
 // read as the row's last V elements and shifted into place once every load of the row has been issued
