@@ -129,3 +129,74 @@ def test_one_long_sequence_packed_with_many_short_ones(io, reverse):
         check(got[name].reshape(p.n, 48, -1)[:, heads], want[name], p.bf16 and name != "dg", name)
     for name in ("h_last", "dh0"):
         check(got[name][:, heads], want[name], False, name)
+
+
+def test_gradients_of_cut_sequences_against_differences():
+    """Gradients against central differences of the forward pass in fp32, several segments and windows. A difference over 2 eps of a
+    loss of value W carries rounding of about 2^-22 |W| / eps and, the loss being bilinear in all but the decays, no truncation there; of
+    the decays eps^2 |W|."""
+    p = Call((1, 700), 2, 1, 12, 20, "f32", seed=10)
+    call = PreparedLinAttn(p.q, p.k, p.v, p.g, None, p.h0)
+    grad = PreparedLinAttnGrad(call, p.dy, p.dh)
+    call()
+    grad()
+    assert call.plan["kernels"] == 3
+
+    def loss():
+        call()
+        return ((call.y.double() * p.dy.double()).sum() + (call.h_last.double() * p.dh.double()).sum()).item()
+
+    size = (call.y.double() * p.dy.double()).abs().sum().item() + (call.h_last.double() * p.dh.double()).abs().sum().item()
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(1)
+    for t, g in ((p.q, grad.dq), (p.k, grad.dk), (p.v, grad.dv), (p.g, grad.dlog_decay), (p.h0, grad.dh0)):
+        d = torch.randn(t.shape, generator=gen, device=DEV)
+        keep, eps = t.clone(), 2.0 ** -7
+        t.copy_(keep + eps * d)
+        up = loss()
+        t.copy_(keep - eps * d)
+        down = loss()
+        t.copy_(keep)
+        assert abs((up - down) / (2 * eps) - (g.double() * d.double()).sum().item()) <= size * (2.0 ** -22 / eps + 8 * eps ** 2)
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_folded_sequences_cut_are_those_of_a_batch(reverse):
+    p = Call((2, 700), 2, 2, 32, 64, "bf16", reverse=reverse, seed=11)
+    want = p.run()
+    assert p.plan["kernels"] == 3
+    q, k, v, g, dy = (t.reshape(1, 1400, *t.shape[2:]) for t in (p.q, p.k, p.v, p.g, p.dy))
+    call = PreparedLinAttn(q, k, v, g, None, p.h0, 700, None, reverse)
+    call()
+    grad = PreparedLinAttnGrad(call, dy, p.dh)
+    grad()
+    for name, t in dict(y=call.y, h_last=call.h_last, dq=grad.dq, dk=grad.dk, dv=grad.dv, dg=grad.dlog_decay, dh0=grad.dh0).items():
+        assert (t.double().cpu().numpy().reshape(want[name].shape) == want[name]).all(), name
+
+
+def test_captured_and_replayed_over_windows():
+    """A graph of a forward and a backward pass with borders of windows, replayed between eager calls on other inputs."""
+    p = Call((300, 300), 3, 3, 32, 32, "bf16", state=False, seed=12)
+    call = PreparedLinAttn(p.q, p.k, p.v, p.g)
+    grad = PreparedLinAttnGrad(call, p.dy)
+    call()
+    grad()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        c2 = PreparedLinAttn(p.q, p.k, p.v, p.g)
+        g2 = PreparedLinAttnGrad(c2, p.dy)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            c2()
+            g2()
+    for _ in range(3):
+        p.v.copy_(torch.randn_like(p.v))
+        p.g.copy_(-torch.rand_like(p.g))
+        call()
+        grad()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in ((call.y, c2.y), (grad.dq, g2.dq), (grad.dk, g2.dk), (grad.dv, g2.dv), (grad.dlog_decay, g2.dlog_decay)):
+            assert torch.equal(a, b)
