@@ -89,7 +89,7 @@ __device__ __forceinline__ float2 center(const LayerNormArgs& a, float (&s)[S::N
 
 // Forward: s = x + residual, n = (s - mean) rsq(var + eps) weight + bias. Memory bounds it: a row stays in registers from
 // its one read to its one write, and the workgroups walk the rows so that the weights are read once per workgroup. 25216 x 768 bf16
-// with an fp32 residual (232 MB): 40 us, 5.8 TB/s; 13056 x 1531 fp32 (160 MB, 4-byte accesses) 44 us, VALU busy 46%.
+// with an fp32 residual (232 MB): 40 us, 5.8 TB/s; 13056 x 1531 fp32 (160 MB, 4-byte accesses) 47 us, VALU busy 52%.
 template <typename IO, typename RES, typename S>
 __global__ __launch_bounds__(S::kThreads) void k_ln_fwd(LayerNormArgs a) {
     constexpr int NV = S::NV, V = S::V;
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(S::kThreads) void k_ln_fwd(LayerNormArgs a) {
 // g = dn weight: ds = dsum + rho (g - mean g - xh mean(g xh)); dx = dresidual = ds. The weights' gradients, sums of dn xh
 // and dn over the rows, stay with the thread over all its rows, are added up over the workgroup's rows at the end and left
 // for k_ln_cols: no atomics, the same bits every time. Memory bounds it: 25216 x 768 bf16 (349 MB) 53 us, 6.5 TB/s (two thirds
-// of it reads); 13056 x 1531 fp32 (240 MB) 60 us, VALU busy 60%.
+// of it reads); 13056 x 1531 fp32 (240 MB) 65 us, VALU busy 64%.
 template <typename IO, typename RES, typename S>
 __global__ __launch_bounds__(S::kThreads) void k_ln_bwd(LayerNormArgs a) {
     constexpr int NV = S::NV, L = S::L, W = S::W, V = S::V;

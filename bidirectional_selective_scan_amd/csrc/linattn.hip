@@ -1,12 +1,12 @@
 // Linear attention with a decay for each head for AMD MI355X (gfx950): the entry points of include/vimscan.h
 // (vimscan_linattn_*) and the kernels around the passes (linattn_device.h).
 //
-// Forward: one pass. Where sequences and heads alone do not fill the chip, or are long, sequences are cut into segments: every
-// segment's own state first (k_lin_pass, kLocal), a fold of those over the sequence (k_lin_fold), then the pass
-// with every segment from its state.
-// Backward: the same states, and those of the gradient from the other end; then three passes, for dq, dk and dv, the first
-// two in one launch, all three where they are the same instance (128 x 197 x 12 heads of 64 x 64 bf16 201 us, 217 with a launch
-// for each; packed 32 x up to 513 x 6 of 40 x 56 fp32 227, 246).
+// Forward: one pass. Where sequences and heads alone do not fill the chip, or one may be far longer than the others, sequences are cut
+// into segments: every segment's own state first (k_lin_pass, kLocal), a fold of those over the sequence (k_lin_fold), then the
+// pass with every segment from its state.
+// Backward: the same states, and those of the gradient from the other end; then three passes, for dq, dk and dv. With the decays' gradient
+// the first two, which leave its terms, are one launch (128 x 197 x 12 heads of 64 x 64 bf16 160 us, 184 with a launch for each;
+// packed 32 x up to 513 x 6 of 40 x 56 fp32 152, 164); without it all three where they are the same instance (101, 127; 117, 141).
 // The decays' gradient is exp(g_t) <S_{t-1}, D_t> = sum over u = t .. e of (q_u . dq_u - k_u . dk_u) + the same behind e, where that is
 // <S_e, E_e>, formed at the segment's end and at the borders of windows in it (k_lin_borders). The dq and dk passes leave
 // the products q . dq and k . dk, without the pair of a token with itself, which is in both and cancels; k_lin_decay_grad adds them up.
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void k_lin_fold(LinArgs a, float* states, cons
 
 // The values at the borders of windows, exp(g_t) <S_{t-1}, D_t>: the product of what the passes of dq and dk left there. A wave
 // a border, head and block (borders that no segment has are read and never asked for); memory bounds it: 128 x 12 borders of 64 x 64
-// (50 MB) 8.7 us.
+// (50 MB) 9.5 us.
 struct BorderArgs {
     const float* s;
     const float* e;
@@ -134,7 +134,7 @@ constexpr float kNoFactor = -104.0f;
 // dg_t = exp(g_t) <S_{t-1}, D_t>, of which the passes leave the values at the borders of windows: inside a window the sum of
 // q . dq - k . dk from its end, over the value there. The sums hold pairs of tokens that both lie behind t, which cancel but for
 // their rounding and for NaN and infinity: so they go no further than a window, and start anew where a factor is 0. In fp64 (they nearly
-// cancel). A wave a segment and head, half of it a window: 128 x 197 x 12 heads 8.2 us, waves that wait for their loads.
+// cancel). A wave a segment and head, half of it a window: 128 x 197 x 12 heads 9.0 us, waves that wait for their loads.
 __global__ __launch_bounds__(64 * kWaves) void k_lin_decay_grad(LinArgs a, DecayGradArgs d) {
     constexpr int kPer = vimscan_host::kLinWindow / kChunk;
     const int lane = static_cast<int>(threadIdx.x) & 63, half = lane >> 5, l = lane & 31;
@@ -242,8 +242,9 @@ __global__ __launch_bounds__(256) void k_lin_group_sum(const float* part, int64_
 }
 
 // One token: S' = e^g S + k^T v, y = scale q S'. The states' traffic bounds it (8 bytes for 5 operations): 256 x 24 heads of 64 x 64
-// (204 MB) 41.7 us, 4.9 TB/s, with states read and written past the caches, 45.4 through them. A workgroup takes a
-// row's head and up to 4 CL of its value channels: CL lanes of V channels to a state row, the rows spread over the rest.
+// (204 MB) 41.7 us, 4.9 TB/s, with states read and written past the caches, 45.4 through them. (Pools of up to 25 MB take the same either way,
+// 1.6 MB 4.2 us, 6.3 MB 5.0, 25 MB 8.0. Larger ones that nothing else throws out of the memory-side cache between two tokens would be faster
+// through it, 201 MB updated in place 68 and 60 us; a model's other layers do throw them out.) A workgroup takes a row's head and up to 4 CL of its value channels: CL lanes of V channels to a state row, the rows spread over the rest.
 struct LinStepArgs {
     LinRows q, k, v;
     int32_t H, dk, dv, blocks;
@@ -399,7 +400,10 @@ void run_fold(const LinArgs& a, float* states, const float* tot, const float* in
     hipLaunchKernelGGL(k_lin_fold, dim3(some_blocks(all) < 2048 ? some_blocks(all) : 2048), dim3(256), 0, s, a, states, tot, init, from_end ? 1 : 0);
 }
 
-// Whether rows are whole pieces of 16 bytes that start at multiples of four bytes (the hardware takes those as they are).
+// Whether rows are whole pieces of 16 bytes that start at multiples of four bytes (the hardware takes those as they are). Else every array
+// goes element by element, for which loads and stores bound the pass (bf16, forward and backward, us: 32 x 513 x 12 heads of 100 x 100
+// 573 + 2042, of 104 x 104 92 + 445; 128 x 197 x 12 of 64 x 64 from an odd element on 176 + 609, else 46 + 160; of 20 x 20 99 + 275, of 24 x 24
+// 37 + 110; fp32 64 x 513 x 8 of 30 x 30 97 + 316, of 32 x 32 69 + 201): pad heads to multiples of 8 (fp32: 4).
 bool use_vectors(const vimscan_linattn* p, const vimscan_linattn_grad* g, const void* y, const LinPlan& pl, int io) {
     const int64_t n = io == VIMSCAN_F32 ? 4 : 8;
     if (pl.dk % n != 0 || pl.dv % n != 0) return false;

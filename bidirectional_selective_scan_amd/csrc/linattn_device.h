@@ -11,8 +11,8 @@
 //
 // What bounds it: by its floor memory (bf16, heads of 64 x 64: 512 bytes and 16 K operations a token and head); as built the chain of a
 // chunk's steps (tile in, scores, products, tile out), which a SIMD's one to three waves cover in part: 1 x 65537 x 24 heads of
-// 64 x 64 bf16 213 us for 803 MB, 3.8 TB/s, VALU busy 38%, matrix cores 16%; the gradients of q and k of 128 x 197 x 12 109 us, VALU
-// 46%. A wave does all of a head (or 32 or 64 output channels of it) alone: it reads every number once, the state never leaves
+// 64 x 64 bf16 204 us for 803 MB, 3.9 TB/s, VALU busy 41%, matrix cores 18%; the gradients of q and k of 128 x 197 x 12 111 us, VALU
+// 45%. A wave does all of a head (or 32 or 64 output channels of it) alone: it reads every number once, the state never leaves
 // its registers, and nothing waits for another wave. The operands are laid out so that what one product leaves
 // in the accumulators is the next one's operand as it stands (lane = 16 grp + col):
 //   * the scores are formed transposed, rows = key tokens, columns = reader tokens: a lane holds the tokens 4 grp + 0..3
@@ -23,7 +23,8 @@
 //     reads of a key or reader, in an order in which pairs of tiles are in place as the left operand of r S, and
 //     as columns they are read in pairs.
 // bf16: the numbers of the inputs are exact operands. Those in fp32 (state, scores, decayed values) are two or three bf16
-// parts, each multiplied: three where what comes of them is fp32 in memory. fp32: fp32 matrix instructions.
+// parts, each multiplied: three of what makes states and the terms of the decays' gradient, two of what is read for an output (y and the
+// gradients of q, k and v, those by head that the sums of shared heads take in fp32 among them). fp32: fp32 matrix instructions.
 // Sums of g are in fp64, and their differences taken from a pair of fp32, so that a token of strong decay does not cost its
 // neighbours digits.
 #ifndef VIMSCAN_LINATTN_DEVICE_H
@@ -485,10 +486,10 @@ template <typename IO, int NK, int NV, bool kVec, int kKind>
 __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass(LinPasses passes) {
     constexpr bool kBf16 = sizeof(IoElem<IO>) == 2;
     constexpr int e = sizeof(IoElem<IO>);
-    // bf16: how many parts. The scores and the state, where they are read, take two (2^-17 of a term) where only an output in
-    // bf16 comes of them: with one their rounding is as large as the output's own (its error 1.4 times the least) for 4% (8 x 1025 x 12
-    // heads of 64 x 64 49 us, 47 with one) to 11% (64 packed x up to 1025 x 24 of 128 x 64 257 us, 232). The terms of the decays'
-    // gradient, in fp32, nearly cancel: three. The decayed values make the state, which is fp32 in memory: three.
+    // bf16: how many parts. The scores and the state, where they are read, take two (2^-17 of a term) where an output that is rounded to
+    // bf16 comes of them: with one their rounding is as large as the output's own (its error 1.4 times the least) for 3% (8 x 1025 x 12
+    // heads of 64 x 64 47 us, 46 with one) to 12% (128 x 197 x 12 47 us, 41; 64 packed x up to 1025 x 24 of 128 x 64 228, 205). The
+    // terms of the decays' gradient, in fp32, nearly cancel: three. The decayed values make the state, which is fp32 in memory: three.
     constexpr int kReadParts = kKind == kGradientDots ? 3 : 2, kValueParts = 3;
     using L = LinTiles<IO, NK, NV, kKind>;
     using TK = Tile<IO, NK>;
@@ -815,17 +816,17 @@ __global__ __launch_bounds__(64, (kLinWavesPerSimd<IO, NK, NV>)) void k_lin_pass
                         if constexpr (kBf16) return (c & 1) ? bf16_hi(u[0][c / 2]) : bf16_lo(u[0][c / 2]);
                         else return __uint_as_float(u[c / 4][c % 4]);
                     };
-                        U4 w[kW];
+                    U4 w[kW];
 #pragma unroll
-                        for (int q = 0; q < kW; ++q)
-                            w[q] = load_piece<IO, kVec>(wb, !kVec ? wx + static_cast<uint32_t>(k * kRows) * W.ld : q == 0 || oc + nw < W.D ? wx + static_cast<uint32_t>(k * kRows) * W.ld + q * 16 : kOutside,
-                                                        oc + q * nw, W.D);
-                        float dot = 0.0f;
+                    for (int q = 0; q < kW; ++q)
+                        w[q] = load_piece<IO, kVec>(wb, !kVec ? wx + static_cast<uint32_t>(k * kRows) * W.ld : q == 0 || oc + nw < W.D ? wx + static_cast<uint32_t>(k * kRows) * W.ld + q * 16 : kOutside,
+                                                    oc + q * nw, W.D);
+                    float dot = 0.0f;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) dot = fmaf(x[c], value(w, c), dot);
+                    for (int c = 0; c < 8; ++c) dot = fmaf(x[c], value(w, c), dot);
 #pragma unroll
-                        for (int q = 1; q < kLanes; q *= 2) dot += __shfl_xor(dot, q);
-                        if (lane % kLanes == 0 && row < cnt) a.dots[(static_cast<int64_t>(block) * a.tokens + mem + row) * a.H + h] = dot;
+                    for (int q = 1; q < kLanes; q *= 2) dot += __shfl_xor(dot, q);
+                    if (lane % kLanes == 0 && row < cnt) a.dots[(static_cast<int64_t>(block) * a.tokens + mem + row) * a.H + h] = dot;
                     U4 v[kW];
 #pragma unroll
                     for (int q = 0; q < kW; ++q) v[q] = *reinterpret_cast<const U4*>(tv + row * TV::kRow + lane % kLanes * 8 * e + q * 16);

@@ -23,11 +23,11 @@ int check_dims(const vimscan_launch* l, int64_t heads, int64_t groups) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tokens per segment, or 0: sequences stay whole. A wave for each SIMD of the chip (1024): more, shorter segments cost more
-// in their states than they gain (heads of 64 x 64 bf16, forward, us, chunks of 32 tokens per segment; 8 x 1025 x 12 with the state read
-// in one part, about 4% less than in two: 2: 51, 5: 48, 9: 60, whole 96; 1 x 65537 x 24, 17: 324, 25: 305, 33: 296, 49: 306).
-// Two where packed sequences differ in length (in one part too: 16 x up to 2000 x 24, 9: 121, 17: 143, 25: 162, whole 176; but 64 x up to
-// 1025 x 12, whose heads alone are 768 waves, in training 9: 510, whole 468), and twice as many in fp32, whose chunks take
-// longer (packed 32 x up to 513 x 6 in training 3: 223, 9: 302, whole 288).
+// in their states than they gain (heads of 64 x 64 bf16, forward, us, chunks of 32 tokens per segment; 8 x 1025 x 12, 2: 51, 4: 47, 5: 48, 9: 62,
+// whole 105; 1 x 4096 x 24, 2: 55, 4: 48, 6: 52, 9: 63, whole 388; 1 x 65537 x 24, 17: 324, 25: 305, 33: 296 to 308, 49: 298 to 308).
+// Two where packed sequences differ in length (16 x up to 2000 x 24, 9: 108, 13: 127, 17: 148, 25: 170, whole 195; 64 x up to
+// 1025 x 12, whose heads alone are 768 waves, hardly gains, in training 9: 491, 17: 582, whole 508), and twice as many in fp32, whose chunks take
+// longer (packed 32 x up to 513 x 6 of 40 x 56 in training 2: 214, 3: 216, 4: 231, 9: 292, whole 290).
 // Where sequences and heads alone are more than half as many waves, they stay whole, however long (64 x 4097 x 24 whole 788, 64: 1233, 128: 1300;
 // 43 x 8200 x 24 1219, 1571, 1790; 22 x 8200 x 24 812, 900, 931).
 // The fold walks a sequence's segments one behind the other, eight at a time, so with few heads a segment is no shorter than the square root of

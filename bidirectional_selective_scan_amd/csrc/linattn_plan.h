@@ -23,9 +23,9 @@ constexpr int64_t kMaxLinWaves = (int64_t(1) << 26) - 1, kMaxLinWgs = (int64_t(1
 
 // Tiles of 16 that a wave's state has over a contracted dimension (at least as wide as it) and over an
 // output dimension, of which a wave takes a block of 2 or 4. Two in fp32 and over more than 64 contracted channels, where four
-// leave room for one wave a SIMD (64 packed x up to 1025 x 24 heads of 128 x 64 bf16: 257 us, 381 with four; 1 x 2048 x 8 of
-// 64 x 64 fp32, forward and backward: 112 us, 144 with four); in bf16 four are faster else (128 x 197 x 12 of 64 x 64,
-// forward and backward: 200 us, 283 with two).
+// leave room for one wave a SIMD (64 packed x up to 1025 x 24 heads of 128 x 64 bf16: 228 us, 337 with four; 1 x 2048 x 8 of
+// 64 x 64 fp32, forward and backward: 117 us, 151 with four); in bf16 four are faster else (128 x 197 x 12 of 64 x 64,
+// forward and backward: 207 us, 263 with two).
 constexpr int lin_contract_tiles(int64_t d) { return d <= 32 ? 2 : d <= 64 ? 4 : 8; }
 constexpr int lin_output_tiles(int bytes, int64_t k, int64_t v) { return v <= 32 || k > 64 || bytes == 4 ? 2 : 4; }
 constexpr int64_t lin_blocks(int bytes, int64_t k, int64_t v) {
